@@ -117,7 +117,8 @@ enum {
                               max_seq_len when set)                            */
   PKV_DEVERR_TOTAL = 4,    /* flat mode: kv_indptr[b] + seq_len > max_total_tokens */
   PKV_DEVERR_SLOT = 8,     /* a flat slot or out_loc outside [0, pool_slots)    */
-  PKV_DEVERR_TIMEOUT = 16  /* a bounded wait on an async copy ran out (~1 s)    */
+  PKV_DEVERR_TIMEOUT = 16, /* a bounded wait on an async copy ran out (~1 s)    */
+  PKV_DEVERR_POSITION = 32 /* pkv_qk_norm_rope: position < 0 or >= max_positions */
 };
 
 /*
@@ -453,6 +454,145 @@ pkv_status pkv_merge_lse(int n_rows, int head_dim, const float *o_a, const float
 pkv_status pkv_extend_append(const pkv_workspace *ws, int batch, int layer,
                              const int32_t *qo_indptr, int max_qo_len, const void *k_new,
                              const void *v_new, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * KV cache in 8 bits.  The pools hold one byte per element (a code) and one
+ * fp32 scale for each block of tokens and KV head; an element stands for
+ * code * scale.  Page table, flat indices, lengths, workspace and outputs are
+ * the bf16 cache's; ws->k_pool and ws->v_pool are not used and may be NULL.
+ * ------------------------------------------------------------------------ */
+
+/* pkv_kv8.dtype */
+enum {
+  PKV_KV8_E4M3 = 0, /* 8-bit floats, 4 exponent and 3 mantissa bits, no infinities, max 448 */
+  PKV_KV8_INT8 = 1  /* two's complement integers in [-127, 127]                             */
+};
+
+/*
+ * An 8-bit cache beside a workspace.  A block is scale_block consecutive slots
+ * of one page that start at a multiple of scale_block in it.
+ */
+typedef struct pkv_kv8 {
+  int32_t dtype;       /* PKV_KV8_*                                                      */
+  int32_t scale_block; /* tokens per scale, 1 .. 128, page_size % scale_block == 0       */
+  void *k_pool;        /* codes [NL, pool_slots, Hkv, D], 16-byte aligned                */
+  void *v_pool;
+  float *k_scale;      /* [NL, pool_slots / P, Hkv, P / scale_block], 4-byte aligned.    */
+  float *v_scale;      /* Positive, in [2^-100, 2^100], wherever a request holds tokens  */
+} pkv_kv8;
+
+/* Bytes of the named pkv_kv8 buffer ("k_pool", "v_pool", "k_scale", "v_scale")
+ * for the shapes in `ws` and `c`; 0 for an unknown name or a scale_block that
+ * does not divide the page size.  Host only. */
+size_t pkv_kv8_bytes(const pkv_workspace *ws, const pkv_kv8 *c, const char *which);
+
+/*
+ * Append to the 8-bit cache, one new row per request: rows k_new[rel, b],
+ * v_new[rel, b] (bf16 [layer_count, batch, Hkv, D], 16-byte aligned) of layer
+ * layer_begin + rel go to slot out_loc[b] (pkv_bind_step).  Slots of the
+ * row's block before it hold the request's older tokens.  For each head:
+ *   need  = the smallest 2^e, e in [-100, 100], with max |row| <= qmax * 2^e
+ *           (qmax 448 or 127; elements that are not finite do not count)
+ *   scale = need in an empty block, else max(scale, need)
+ *   code  = round to nearest even (x / scale), saturating at +-qmax; NaN is
+ *           kept by e4m3 and becomes 0 in int8
+ * and where the scale grew, the block's older codes are rounded once more,
+ * code = rn(code * old scale / new scale).  The division is exact: new scales
+ * are powers of two.  Two entries of a batch must not share a block.
+ * Device errors: PKV_DEVERR_SLOT (that row is skipped).
+ * Host errors: PKV_ERR_INVALID (null or misaligned pointer, bad dtype or
+ * scale_block), PKV_ERR_UNSUPPORTED (head_dim not 64 / 128), PKV_ERR_CAPACITY.
+ */
+pkv_status pkv_kv8_append(const pkv_workspace *ws, const pkv_kv8 *c, int batch, int layer_begin,
+                          int layer_count, const void *k_new, const void *v_new,
+                          pkv_stream_t stream);
+
+/*
+ * Append of a chunk to the 8-bit cache: the rows and checks of
+ * pkv_extend_append, quantised as by pkv_kv8_append with each block's new rows
+ * taken together (one maximum over them, one rounding of older codes).
+ */
+pkv_status pkv_kv8_extend_append(const pkv_workspace *ws, const pkv_kv8 *c, int batch, int layer,
+                                 const int32_t *qo_indptr, int max_qo_len, const void *k_new,
+                                 const void *v_new, pkv_stream_t stream);
+
+/*
+ * Cached rows read back: tokens starts[b] .. seq_lens[b] - 1 of request b
+ * become rows dst_indptr[b], dst_indptr[b] + 1, ... of k_out and v_out.
+ *   starts      device int32 [batch] or NULL (0 for every request); a request
+ *               whose start is its length or more has no rows.
+ *   dst_indptr  device int32 [batch]: each request's first row (of at least
+ *               [batch] entries; rows of two requests must not overlap).
+ *   n_rows      rows that k_out and v_out hold.
+ *   k_out, v_out device bf16 [n_rows, Hkv, D] (fp32 with PKV_FLAG_OUT_F32),
+ *               16-byte aligned; rows that no token maps to are left as they
+ *               were.  A value is code * scale rounded once, which is exact for
+ *               power-of-two scales.
+ * Device errors: PKV_DEVERR_LEN (a length out of range or a negative start),
+ * PKV_DEVERR_TOTAL (rows outside [0, n_rows)): the request is skipped;
+ * PKV_DEVERR_PAGE, _SLOT: the row is written as zeros.
+ * Host errors as pkv_kv8_append; PKV_ERR_INVALID for another flag.
+ */
+pkv_status pkv_kv8_read(const pkv_workspace *ws, const pkv_kv8 *c, int batch, int layer,
+                        const int32_t *starts, const int32_t *dst_indptr, int n_rows, void *k_out,
+                        void *v_out, int flags, pkv_stream_t stream);
+
+/*
+ * One layer of a decode step on the 8-bit cache: the append (skipped when k_new
+ * and v_new are both NULL), split-KV GQA decode attention and the split merge.
+ * Arguments, workspace buffers and results are pkv_decode_layer's, with the
+ * scores and values of the dequantised cache:
+ *   s_t = scale * k_scale_t * (q . code_k,t),  o = sum_t softmax(s)_t v_scale_t code_v,t.
+ *   num_splits  S in [1, max_splits]; S > 1 needs o_part, ml_part and
+ *               split_counters (zeroed once, left zeroed).
+ *   flags       PKV_FLAG_OUT_F32, PKV_FLAG_WRITE_LSE, PKV_FLAG_PLAN_EARLY.
+ * The partial of a split holds its (normalised output, log-sum-exp, 1).
+ * Host errors: as pkv_decode_layer and pkv_kv8_append; PKV_ERR_INVALID for
+ * another flag; PKV_ERR_UNSUPPORTED for G not in {1, 2, 4, 8, 16}.
+ */
+pkv_status pkv_kv8_decode_layer(const pkv_workspace *ws, const pkv_kv8 *c, int batch, int layer,
+                                const void *q, const void *k_new, const void *v_new, float scale,
+                                int num_splits, int flags, pkv_stream_t stream);
+
+/*
+ * RMS norm of every query and key head with the position rotation, in one
+ * pass: the step between a layer's projection and its append and attention.
+ */
+typedef struct pkv_qk_norm_rope_args {
+  int32_t n_q_heads;     /* Hq >= 1                                                      */
+  int32_t n_kv_heads;    /* Hkv >= 0 (0: queries only; k and k_out may be NULL)          */
+  int32_t head_dim;      /* D in {64, 128, 256}                                          */
+  int32_t rot_dim;       /* leading elements that rotate, 0 .. D, a multiple of 16       */
+  int32_t max_positions; /* rows of cos_sin                                              */
+  int32_t interleaved;   /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1)       */
+  float eps;             /* added to the mean square; >= 0                               */
+  int32_t reserved;      /* 0                                                            */
+  const void *q_weight;  /* bf16 [D], 16-byte aligned; NULL: queries are not normalised  */
+  const void *k_weight;  /* the same for keys                                            */
+  const float *cos_sin;  /* [max_positions, rot_dim]: rot_dim / 2 cosines, then sines;
+                            16-byte aligned; NULL only when rot_dim == 0                 */
+  int32_t *err;          /* sticky word of PKV_DEVERR_* bits                             */
+} pkv_qk_norm_rope_args;
+
+/*
+ * For every token t < n_tokens and head x of q[t] (and of k[t]):
+ *   y = x * w / sqrt(mean(x^2) + eps)      (x where the weight is NULL)
+ *   a pair (y_i, y_j), the i-th of rot_dim / 2, becomes
+ *   (y_i cos - y_j sin, y_j cos + y_i sin) with row positions[t] of cos_sin,
+ * in fp32, rounded once to bf16.  Elements from rot_dim on do not rotate.
+ *   q, k        device bf16, head h of token t at t * stride + h * D; strides in
+ *               elements, multiples of 8, at least the heads' width (so q and k
+ *               may be parts of one projection's rows).
+ *   positions   device int32 [n_tokens] (ws->position_ids in a decode step).
+ *   q_out, k_out as q and k; may be q and k themselves with the same strides.
+ * Device errors: PKV_DEVERR_POSITION (the token's heads are written as zeros).
+ * Host errors: PKV_ERR_INVALID (null or misaligned pointer, bad size or
+ * stride), PKV_ERR_UNSUPPORTED (head_dim, rot_dim).
+ */
+pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, const void *q,
+                            int64_t q_stride, const void *k, int64_t k_stride,
+                            const int32_t *positions, void *q_out, int64_t q_out_stride,
+                            void *k_out, int64_t k_out_stride, pkv_stream_t stream);
 
 /*
  * Host steady-state test (cache.py page, bullets 1-4): non-zero when the

@@ -23,6 +23,8 @@ PKV_FLAG_EXTEND_FULL = 512
 PKV_FLAG_EXTEND_WARP_MMA = 1024
 PKV_DEVERR_PAGE, PKV_DEVERR_LEN, PKV_DEVERR_TOTAL, PKV_DEVERR_SLOT, PKV_DEVERR_TIMEOUT = \
     1, 2, 4, 8, 16
+PKV_DEVERR_POSITION = 32
+PKV_KV8_E4M3, PKV_KV8_INT8 = 0, 1
 
 # Every symbol include/pkv.h declares (checked by the ABI test).
 EXPORTS = ("pkv_workspace_bytes", "pkv_bind_step", "pkv_choose_splits", "pkv_choose_pieces",
@@ -31,6 +33,8 @@ EXPORTS = ("pkv_workspace_bytes", "pkv_bind_step", "pkv_choose_splits", "pkv_cho
            "pkv_merge_partials", "pkv_decode_layer", "pkv_plan_step",
            "pkv_decode_attn_static_scratch",
            "pkv_extend_attn", "pkv_extend_append", "pkv_merge_lse",
+           "pkv_kv8_bytes", "pkv_kv8_append", "pkv_kv8_extend_append", "pkv_kv8_read",
+           "pkv_kv8_decode_layer", "pkv_qk_norm_rope",
            "pkv_is_steady_increment",
            "pkv_status_string", "pkv_version")
 PKV_STATIC_SCRATCH_BYTES = 8 << 20
@@ -55,6 +59,29 @@ class PkvWorkspace(ctypes.Structure):
         ("lse", ctypes.c_void_p), ("err", ctypes.c_void_p),
         ("split_counters", ctypes.c_void_p), ("work_plan", ctypes.c_void_p),
         ("max_seq_len", ctypes.c_int32),
+    ]
+
+
+class PkvKv8(ctypes.Structure):
+    """Mirror of ``pkv_kv8``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("scale_block", ctypes.c_int32),
+        ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class PkvQkNormRopeArgs(ctypes.Structure):
+    """Mirror of ``pkv_qk_norm_rope_args``."""
+
+    _fields_ = [
+        ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("max_positions", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("cos_sin", ctypes.c_void_p), ("err", ctypes.c_void_p),
     ]
 
 
@@ -103,6 +130,20 @@ def load(path: str = LIB_PATH):
     lib.pkv_extend_append.restype = i32
     lib.pkv_merge_lse.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp, i32, vp]
     lib.pkv_merge_lse.restype = i32
+    C8, i64 = ctypes.POINTER(PkvKv8), ctypes.c_int64
+    lib.pkv_kv8_bytes.argtypes = [W, C8, ctypes.c_char_p]
+    lib.pkv_kv8_bytes.restype = ctypes.c_size_t
+    lib.pkv_kv8_append.argtypes = [W, C8, i32, i32, i32, vp, vp, vp]
+    lib.pkv_kv8_append.restype = i32
+    lib.pkv_kv8_extend_append.argtypes = [W, C8, i32, i32, vp, i32, vp, vp, vp]
+    lib.pkv_kv8_extend_append.restype = i32
+    lib.pkv_kv8_read.argtypes = [W, C8, i32, i32, vp, vp, i32, vp, vp, i32, vp]
+    lib.pkv_kv8_read.restype = i32
+    lib.pkv_kv8_decode_layer.argtypes = [W, C8, i32, i32, vp, vp, vp, f32, i32, i32, vp]
+    lib.pkv_kv8_decode_layer.restype = i32
+    lib.pkv_qk_norm_rope.argtypes = [ctypes.POINTER(PkvQkNormRopeArgs), i32, vp, i64, vp, i64, vp,
+                                     vp, i64, vp, i64, vp]
+    lib.pkv_qk_norm_rope.restype = i32
     p64, p32 = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int32)
     lib.pkv_is_steady_increment.argtypes = [p64, p32, i32, p64, p32, i32]
     lib.pkv_is_steady_increment.restype = i32
@@ -240,6 +281,70 @@ def pkv_merge_lse(n_rows, head_dim, o_a, lse_a, o_b, lse_b, out, lse_out=None, f
     s = load().pkv_merge_lse(int(n_rows), int(head_dim), _ptr(o_a), _ptr(lse_a), _ptr(o_b),
                              _ptr(lse_b), _ptr(out), _ptr(lse_out), int(flags), _stream(stream))
     return _check("pkv_merge_lse", s) if check else s
+
+
+def pkv_kv8_bytes(ws, cache, which: str) -> int:
+    return int(load().pkv_kv8_bytes(_ws(ws), _ws(cache), which.encode()))
+
+
+def pkv_kv8_append(ws, cache, batch, layer_begin, layer_count, k_new, v_new, stream=None,
+                   check=True):
+    """New rows [layer_count, batch, Hkv, D] quantised into an 8-bit cache (a
+    Kv8Cache or a PkvKv8) at ws.out_loc."""
+    s = load().pkv_kv8_append(_ws(ws), _ws(cache), int(batch), int(layer_begin), int(layer_count),
+                              _ptr(k_new), _ptr(v_new), _stream(stream))
+    return _check("pkv_kv8_append", s) if check else s
+
+
+def pkv_kv8_extend_append(ws, cache, batch, layer, qo_indptr, max_qo_len, k_new, v_new,
+                          stream=None, check=True):
+    s = load().pkv_kv8_extend_append(_ws(ws), _ws(cache), int(batch), int(layer), _ptr(qo_indptr),
+                                     int(max_qo_len), _ptr(k_new), _ptr(v_new), _stream(stream))
+    return _check("pkv_kv8_extend_append", s) if check else s
+
+
+def pkv_kv8_read(ws, cache, batch, layer, starts, dst_indptr, n_rows, k_out, v_out, flags=0,
+                 stream=None, check=True):
+    """Cached rows of every request from token starts[b] on (None: 0) as rows
+    dst_indptr[b], ... of k_out and v_out [n_rows, Hkv, D]."""
+    s = load().pkv_kv8_read(_ws(ws), _ws(cache), int(batch), int(layer), _ptr(starts),
+                            _ptr(dst_indptr), int(n_rows), _ptr(k_out), _ptr(v_out), int(flags),
+                            _stream(stream))
+    return _check("pkv_kv8_read", s) if check else s
+
+
+def pkv_kv8_decode_layer(ws, cache, batch, layer, q, k_new, v_new, scale, num_splits=1, flags=0,
+                         stream=None, check=True):
+    """Append (unless k_new is None), attention and merge of one layer on the
+    8-bit cache."""
+    s = load().pkv_kv8_decode_layer(_ws(ws), _ws(cache), int(batch), int(layer), _ptr(q),
+                                    _ptr(k_new), _ptr(v_new), float(scale), int(num_splits),
+                                    int(flags), _stream(stream))
+    return _check("pkv_kv8_decode_layer", s) if check else s
+
+
+def _stride(x, width, head_dim):
+    """Elements between the tokens of x: a pointer or None is dense; a tensor is
+    [tokens, width] or [tokens, heads, head_dim] with dense heads."""
+    if x is None or isinstance(x, int):
+        return width
+    if x.stride(-1) != 1 or x.dim() not in (2, 3) or (x.dim() == 3 and x.stride(1) != head_dim):
+        raise ValueError("heads must be dense: [tokens, width] or [tokens, heads, head_dim]")
+    return x.stride(0)
+
+
+def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None, check=True):
+    """RMS norm and rotation of every head of q and k into q_out and k_out
+    (args: a QkNormRope or a PkvQkNormRopeArgs); q and k may be slices of one
+    projection's rows."""
+    st = args.struct if hasattr(args, "struct") else args
+    D = st.head_dim
+    qw, kw = st.n_q_heads * D, st.n_kv_heads * D
+    s = load().pkv_qk_norm_rope(ctypes.byref(st), int(n_tokens), _ptr(q), _stride(q, qw, D),
+                                _ptr(k), _stride(k, kw, D), _ptr(positions), _ptr(q_out),
+                                _stride(q_out, qw, D), _ptr(k_out), _stride(k_out, kw, D),
+                                _stream(stream))
+    return _check("pkv_qk_norm_rope", s) if check else s
 
 
 def pkv_is_steady_increment(prev_ids, prev_lens, ids, lens) -> bool:

@@ -6,8 +6,6 @@
 
 #include <cuda.h>
 
-#include <utility>
-
 #include "decode_plan.cuh"
 
 namespace pkv {
@@ -117,24 +115,6 @@ inline bool xencode_pool_map(CUtensorMap *m, void *base, const pkv_workspace &ws
 inline bool xtma_pages(const pkv_workspace &ws) {
   return ws.index_mode == PKV_IDX_PAGE_TABLE && ws.page_size % 16 == 0 &&
          (long long)ws.n_layers * ws.pool_slots < 0x7fffffffll;
-}
-
-// Launch with programmatic dependent launch allowed (the kernels wait for
-// the previous kernel on the stream at entry).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t st, Args &&...args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 // The split merge after an extend launch with a.S > 1 (extend_mma.cu).

@@ -40,6 +40,26 @@ cudaError_t launch_plan(const DecodeArgs &a, cudaStream_t st);
 size_t plan_bytes();
 bool decode_mma_supported(int head_dim, int group);
 
+// 8-bit cache (kv8_cache.cu, kv8_decode.cu).
+struct Kv8Args;
+cudaError_t launch_kv8_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,
+                              int layer_begin, int layer_count, const void *k_new,
+                              const void *v_new, cudaStream_t st);
+cudaError_t launch_kv8_extend_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,
+                                     int layer, const int *qo_indptr, int max_qo_len,
+                                     const void *k_new, const void *v_new, cudaStream_t st);
+cudaError_t launch_kv8_read(const pkv_workspace &ws, const pkv_kv8 &c, int batch, int layer,
+                            const int *starts, const int *dst_indptr, int n_rows, void *k_out,
+                            void *v_out, int flags, cudaStream_t st);
+cudaError_t launch_kv8_decode(const Kv8Args &a, cudaStream_t st);
+bool kv8_decode_supported(int head_dim, int group);
+
+// Norm and rotation of queries and keys (qk_norm_rope.cu).
+cudaError_t launch_qk_norm_rope(const pkv_qk_norm_rope_args &p, int n_tokens, const void *q,
+                                long long q_stride, const void *k, long long k_stride,
+                                const int *positions, void *q_out, long long q_out_stride,
+                                void *k_out, long long k_out_stride, cudaStream_t st);
+
 cudaError_t launch_merge(const pkv_workspace &ws, int batch, int num_splits, int flags,
                          cudaStream_t st);
 

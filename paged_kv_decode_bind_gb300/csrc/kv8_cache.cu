@@ -1,0 +1,386 @@
+// The 8-bit cache's writes and read-back: rows quantised as they are appended
+// (one per request, or a chunk per request) and cached rows back as bf16.
+//
+// All three move each byte once and are bound by memory for long inputs and
+// by the chain of dependent loads (slot, scale, rows) for short ones.  Codes
+// and scales follow pkv.h; every division is by a power of two, so the values
+// compared and rounded are exact and the results do not depend on the order
+// of any sum.
+#include "kernels.cuh"
+#include "kv8.cuh"
+
+namespace pkv {
+
+namespace {
+
+// 8 bf16 values in fp32.
+__device__ __forceinline__ float row_max(const uint4 &v) {
+  float f[8];
+  unpack8(v, f);
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(f[i]));
+  return m;
+}
+
+template <int DT>
+__device__ __forceinline__ uint2 encode8(const uint4 &v, float inv) {
+  float f[8];
+  unpack8(v, f);
+  return make_uint2(encode4<DT>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                    encode4<DT>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+}
+
+// Codes of 8 elements under a new scale: ratio = old scale / new scale.
+template <int DT>
+__device__ __forceinline__ uint2 recode8(const uint2 &w, float ratio) {
+  float a[4], b[4];
+  decode4<DT>(w.x, a);
+  decode4<DT>(w.y, b);
+  return make_uint2(encode4<DT>(a[0] * ratio, a[1] * ratio, a[2] * ratio, a[3] * ratio),
+                    encode4<DT>(b[0] * ratio, b[1] * ratio, b[2] * ratio, b[3] * ratio));
+}
+
+// Scale of a block for new rows with finite maximum amax; `held`: the block
+// already has rows under `old`.  *inv = 1 / scale.
+template <int DT>
+__device__ __forceinline__ float block_scale(float amax, bool held, float old, float *inv,
+                                             bool *grown) {
+  const int e = need_exp<DT>(amax);
+  const float need = pow2i(e);
+  *grown = held && !(old >= need);
+  if (held && !*grown) {
+    *inv = 1.f / old;  // exact for the powers of two that the appends write
+    return old;
+  }
+  *inv = pow2i(-e);
+  return need;
+}
+
+constexpr int kKAThreads = 256;
+
+// One CTA per (request, layer).  D / 8 lanes hold one head's new row of K or
+// V; its maximum is a butterfly over them.  Only a block whose scale grows is
+// read again (at most scale_block - 1 rows of D bytes).
+template <int D, int DT>
+__global__ void __launch_bounds__(kKAThreads)
+    kv8_append_kernel(const __grid_constant__ pkv_workspace ws, const __grid_constant__ pkv_kv8 c,
+                      int batch, int layer_begin, const uint4 *__restrict__ k_new,
+                      const uint4 *__restrict__ v_new) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int LPR = D / 8;
+  const int b = blockIdx.x, rel = blockIdx.y, layer = layer_begin + rel;
+  const int loc = ws.out_loc[b];
+  if (loc < 0 || loc >= ws.pool_slots) {
+    if (threadIdx.x == 0) atomicOr(ws.err, PKV_DEVERR_SLOT);
+    return;
+  }
+  const int H = ws.n_kv_heads, inside = loc % ws.page_size % c.scale_block;
+  const int j = threadIdx.x % LPR;
+  for (int i0 = 0; i0 < 2 * H; i0 += kKAThreads / LPR) {
+    const int item = i0 + threadIdx.x / LPR;
+    const bool live = item < 2 * H;
+    const int side = item >= H, g = item - side * H;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    float *sp = nullptr;
+    float old = 0.f;
+    if (live) {
+      x = (side ? v_new : k_new)[(((long long)rel * batch + b) * H + g) * LPR + j];
+      sp = (side ? c.v_scale : c.k_scale) + scale_index(ws, c.scale_block, layer, loc, g);
+      if (inside > 0) old = *sp;
+    }
+    float amax = row_max(x);
+#pragma unroll
+    for (int d = LPR / 2; d >= 1; d >>= 1)
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    __syncwarp();  // every lane has read the old scale
+    if (!live) continue;
+    float inv;
+    bool grown;
+    const float s = block_scale<DT>(amax, inside > 0, old, &inv, &grown);
+    uint8_t *pool = static_cast<uint8_t *>(side ? c.v_pool : c.k_pool);
+    const long long row = ((long long)layer * ws.pool_slots + loc) * H + g;
+    uint2 *dst = reinterpret_cast<uint2 *>(pool + row * D) + j;
+    const long long step = (long long)H * LPR;  // 8-byte words between slots
+    if (grown) {
+      const float ratio = old * inv;
+      for (int r = 1; r <= inside; ++r) dst[-r * step] = recode8<DT>(dst[-r * step], ratio);
+    }
+    *dst = encode8<DT>(x, inv);
+    if (j == 0 && (inside == 0 || grown)) *sp = s;
+  }
+}
+
+constexpr int kKXWarps = 4;
+constexpr int kKXRows = 8;  // rows a lane keeps between the maximum and the rounding
+
+// One warp per (request, block that gets rows, head, K or V): 32 / (D / 8)
+// rows side by side.  Blocks of up to kKXRows passes stay in registers between
+// the maximum and the rounding; larger ones are read a second time.
+template <int D, int DT>
+__global__ void __launch_bounds__(kKXWarps * 32)
+    kv8_extend_append_kernel(const __grid_constant__ pkv_workspace ws,
+                             const __grid_constant__ pkv_kv8 c, int batch, int layer,
+                             const int *__restrict__ qo_indptr, int max_qo_len, int per_req,
+                             const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int LPR = D / 8, RPP = 32 / LPR;
+  const int b = blockIdx.x / per_req;
+  const bool lead = blockIdx.x == b * per_req && threadIdx.x == 0;
+  const int q0 = qo_indptr[b], n = qo_indptr[b + 1] - q0, L = ws.seq_lens[b];
+  bool ok = n >= 0 && n <= L && n <= max_qo_len && q0 >= 0 && q0 + n <= qo_indptr[batch] &&
+            (long long)L <= len_cap(ws);
+  long long base = 0;
+  if (ok && ws.index_mode == PKV_IDX_FLAT) {
+    base = ws.kv_indptr[b];
+    ok = base >= 0 && base + L <= ws.max_total_tokens;
+  } else if (ok) {
+    const int row = ws.req_pool_indices[b];
+    ok = row >= 0 && row < ws.max_reqs;
+    base = ok ? (long long)row * ws.max_pages_per_req : 0;
+  }
+  if (!ok) {
+    if (lead) atomicOr(ws.err, PKV_DEVERR_LEN);
+    return;
+  }
+  const int lane = threadIdx.x & 31, sub = lane / LPR, j = lane % LPR;
+  const int H = ws.n_kv_heads, SB = c.scale_block, P = ws.page_size;
+  const int item = (blockIdx.x - b * per_req) * kKXWarps + (threadIdx.x >> 5);
+  const int blk = item / (2 * H), hs = item - blk * 2 * H;
+  const int side = hs >= H, g = hs - side * H;
+  const int first = L - n;  // position of the first new token
+  // blocks lie inside pages: block number = page * (P / SB) + block in page
+  const int p0 = first / P, in0 = first - p0 * P;
+  const int nb = p0 * (P / SB) + in0 / SB + blk;
+  const int pg = nb / (P / SB), tb = pg * P + (nb - pg * (P / SB)) * SB;  // first position
+  if (n == 0 || tb >= L) return;  // warp-uniform
+  const int lo = max(first - tb, 0), hi = min(SB, L - tb);
+  int kind = 0;
+  const int slot = token_slot(ws, base, tb, &kind);
+  if (slot < 0) {
+    if (lane == 0 && hs == 0) atomicOr(ws.err, kind);
+    return;
+  }
+  const long long step = (long long)H * LPR;  // 16-byte bf16 words, or 8-byte code words
+  const uint4 *src = (side ? v_new : k_new) + ((long long)q0 + tb - first) * step + g * LPR + j;
+  uint2 *dst = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(side ? c.v_pool : c.k_pool)) +
+               ((long long)layer * ws.pool_slots + slot) * step + g * LPR + j;
+  float *sp = (side ? c.v_scale : c.k_scale) + scale_index(ws, SB, layer, slot, g);
+  const float old = lo > 0 ? *sp : 0.f;
+
+  uint4 v[kKXRows];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kKXRows; ++i) {
+      const int r = r0 + i * RPP + sub;
+      v[i] = r < hi ? src[r * step] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  float amax = 0.f;
+  for (int r0 = lo; r0 < hi; r0 += kKXRows * RPP) {
+    load(r0);
+#pragma unroll
+    for (int i = 0; i < kKXRows; ++i) amax = fmaxf(amax, row_max(v[i]));
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  float inv;
+  bool grown;
+  const float s = block_scale<DT>(amax, lo > 0, old, &inv, &grown);
+  if (grown) {
+    const float ratio = old * inv;
+    for (int r = sub; r < lo; r += RPP) dst[r * step] = recode8<DT>(dst[r * step], ratio);
+  }
+  const bool kept = hi - lo <= kKXRows * RPP;
+  for (int r0 = lo; r0 < hi; r0 += kKXRows * RPP) {
+    if (!kept) load(r0);
+#pragma unroll
+    for (int i = 0; i < kKXRows; ++i) {
+      const int r = r0 + i * RPP + sub;
+      if (r < hi) dst[r * step] = encode8<DT>(v[i], inv);
+    }
+  }
+  if (lane == 0 && (lo == 0 || grown)) *sp = s;
+}
+
+constexpr int kKRThreads = 256;
+constexpr int kKRTokens = 8;  // tokens per tile
+
+// gx CTAs per request walk its tiles of kKRTokens tokens: the tile's slots are
+// resolved once, then each thread turns 8 codes at a time into 8 values
+// (16-byte stores, consecutive threads on consecutive words of a token's row).
+template <int D, int DT, bool F32>
+__global__ void __launch_bounds__(kKRThreads)
+    kv8_read_kernel(const __grid_constant__ pkv_workspace ws, const __grid_constant__ pkv_kv8 c,
+                    int layer, int gx, const int *__restrict__ starts,
+                    const int *__restrict__ dst_indptr, int n_rows, void *k_out, void *v_out) {
+  __shared__ int s_slot[kKRTokens];
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x / gx, x = blockIdx.x - b * gx;
+  const bool lead = x == 0 && threadIdx.x == 0;
+  const int L = ws.seq_lens[b], start = starts ? starts[b] : 0;
+  const long long row0 = dst_indptr[b];
+  bool ok = L >= 0 && (long long)L <= len_cap(ws) && start >= 0;
+  long long base = 0;
+  int kind = ok ? 0 : PKV_DEVERR_LEN;
+  const int n = ok ? L - start : 0;
+  if (ok && n > 0) {
+    if (row0 < 0 || row0 + n > n_rows) kind = PKV_DEVERR_TOTAL;
+    if (ws.index_mode == PKV_IDX_FLAT) {
+      base = ws.kv_indptr[b];
+      if (base < 0 || base + L > ws.max_total_tokens) kind = PKV_DEVERR_TOTAL;
+    } else {
+      const int row = ws.req_pool_indices[b];
+      // no row of the table: every token is bad (written as zeros below)
+      base = row >= 0 && row < ws.max_reqs ? (long long)row * ws.max_pages_per_req : -1;
+    }
+  }
+  if (kind) {
+    if (lead) atomicOr(ws.err, kind);
+    return;
+  }
+  const int H = ws.n_kv_heads, W = H * (D / 8);  // 8-code words of a token's row
+  for (int t0 = x * kKRTokens; t0 < n; t0 += gx * kKRTokens) {
+    const int m = min(kKRTokens, n - t0);
+    __syncthreads();  // the last tile's slots are no longer read
+    if (threadIdx.x < m) {
+      int bad = 0, slot = -1;
+      if (base >= 0) slot = token_slot(ws, base, start + t0 + threadIdx.x, &bad);
+      else bad = PKV_DEVERR_PAGE;
+      if (bad) atomicOr(ws.err, bad);
+      s_slot[threadIdx.x] = slot;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < m * 2 * W; i += kKRThreads) {
+      const int r = i / W, w = i - r * W, t = r >> 1, side = r & 1;
+      const int slot = s_slot[t], g = w / (D / 8);
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (slot >= 0) {
+        const uint2 code = reinterpret_cast<const uint2 *>(
+            side ? c.v_pool : c.k_pool)[((long long)layer * ws.pool_slots + slot) * W + w];
+        const float s =
+            (side ? c.v_scale : c.k_scale)[scale_index(ws, c.scale_block, layer, slot, g)];
+        float a[4], e[4];
+        decode4<DT>(code.x, a);
+        decode4<DT>(code.y, e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[k] = a[k] * s;
+          f[4 + k] = e[k] * s;
+        }
+      }
+      const long long o = (row0 + t0 + t) * W + w;
+      void *out = side ? v_out : k_out;
+      if constexpr (F32) {
+        float4 *p = static_cast<float4 *>(out) + 2 * o;
+        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+      } else {
+        static_cast<uint4 *>(out)[o] =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7]));
+      }
+    }
+  }
+}
+
+template <typename F>
+cudaError_t by_shape(const pkv_workspace &ws, const pkv_kv8 &c, F f) {
+  if (ws.head_dim == 128)
+    return c.dtype == PKV_KV8_E4M3 ? f.template operator()<128, PKV_KV8_E4M3>()
+                                   : f.template operator()<128, PKV_KV8_INT8>();
+  if (ws.head_dim == 64)
+    return c.dtype == PKV_KV8_E4M3 ? f.template operator()<64, PKV_KV8_E4M3>()
+                                   : f.template operator()<64, PKV_KV8_INT8>();
+  return cudaErrorNotSupported;
+}
+
+struct AppendLaunch {
+  const pkv_workspace &ws;
+  const pkv_kv8 &c;
+  int batch, layer_begin, layer_count;
+  const void *k, *v;
+  cudaStream_t st;
+  template <int D, int DT>
+  cudaError_t operator()() {
+    return launch_pdl(kv8_append_kernel<D, DT>, dim3(batch, layer_count), dim3(kKAThreads), 0, st,
+                      ws, c, batch, layer_begin, static_cast<const uint4 *>(k),
+                      static_cast<const uint4 *>(v));
+  }
+};
+
+struct ExtendAppendLaunch {
+  const pkv_workspace &ws;
+  const pkv_kv8 &c;
+  int batch, layer;
+  const int *qo_indptr;
+  int max_qo_len;
+  const void *k, *v;
+  cudaStream_t st;
+  template <int D, int DT>
+  cudaError_t operator()() {
+    // a request's new rows touch at most this many blocks
+    const long long blocks = ((long long)max_qo_len + c.scale_block - 1) / c.scale_block + 1;
+    const long long per = (blocks * 2 * ws.n_kv_heads + kKXWarps - 1) / kKXWarps;
+    if (per * batch > 0x7fffffffll || blocks * 2 * ws.n_kv_heads > 0x7fffffffll)
+      return cudaErrorInvalidConfiguration;
+    return launch_pdl(kv8_extend_append_kernel<D, DT>, dim3((unsigned)(per * batch)),
+                      dim3(kKXWarps * 32), 0, st, ws, c, batch, layer, qo_indptr, max_qo_len,
+                      (int)per, static_cast<const uint4 *>(k), static_cast<const uint4 *>(v));
+  }
+};
+
+struct ReadLaunch {
+  const pkv_workspace &ws;
+  const pkv_kv8 &c;
+  int batch, layer;
+  const int *starts, *dst_indptr;
+  int n_rows;
+  void *k, *v;
+  int flags;
+  cudaStream_t st;
+  template <int D, int DT>
+  cudaError_t operator()() {
+    // about 16 CTAs for each of 152 SMs over the batch, no more per request
+    // than it can have tiles
+    const long long most = len_cap(ws) < n_rows ? len_cap(ws) : n_rows;
+    long long gx = (most + kKRTokens - 1) / kKRTokens;
+    const long long share = (152 * 16 + batch - 1) / batch;
+    if (gx > share) gx = share;
+    if (gx < 1) gx = 1;
+    if (gx * batch > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(gx * batch));
+    if (flags & PKV_FLAG_OUT_F32)
+      return launch_pdl(kv8_read_kernel<D, DT, true>, grid, dim3(kKRThreads), 0, st, ws, c, layer,
+                        (int)gx, starts, dst_indptr, n_rows, k, v);
+    return launch_pdl(kv8_read_kernel<D, DT, false>, grid, dim3(kKRThreads), 0, st, ws, c, layer,
+                      (int)gx, starts, dst_indptr, n_rows, k, v);
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,
+                              int layer_begin, int layer_count, const void *k_new,
+                              const void *v_new, cudaStream_t st) {
+  return by_shape(ws, c, AppendLaunch{ws, c, batch, layer_begin, layer_count, k_new, v_new, st});
+}
+
+cudaError_t launch_kv8_extend_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,
+                                     int layer, const int *qo_indptr, int max_qo_len,
+                                     const void *k_new, const void *v_new, cudaStream_t st) {
+  return by_shape(
+      ws, c, ExtendAppendLaunch{ws, c, batch, layer, qo_indptr, max_qo_len, k_new, v_new, st});
+}
+
+cudaError_t launch_kv8_read(const pkv_workspace &ws, const pkv_kv8 &c, int batch, int layer,
+                            const int *starts, const int *dst_indptr, int n_rows, void *k_out,
+                            void *v_out, int flags, cudaStream_t st) {
+  return by_shape(ws, c, ReadLaunch{ws, c, batch, layer, starts, dst_indptr, n_rows, k_out, v_out,
+                                    flags, st});
+}
+
+}  // namespace pkv

@@ -4,6 +4,7 @@
 #include <cstring>
 
 #include "kernels.cuh"
+#include "kv8.cuh"
 
 using namespace pkv;
 
@@ -27,6 +28,8 @@ namespace {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // ml_part is read as (m, l) float pairs
 bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Shape checks shared by every entry point.
 pkv_status check_shape(const pkv_workspace *ws) {
@@ -345,6 +348,133 @@ pkv_status pkv_merge_lse(int n_rows, int head_dim, const float *o_a, const float
   if (n_rows == 0) return PKV_OK;
   return from_cuda(launch_merge_lse(n_rows, head_dim, o_a, lse_a, o_b, lse_b, out, lse_out, flags,
                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Checks of an 8-bit cache against its workspace's shapes.
+static pkv_status check_kv8(const pkv_workspace *ws, const pkv_kv8 *c) {
+  pkv_status st = check_shape(ws);
+  if (st != PKV_OK) return st;
+  if (!c || (c->dtype != PKV_KV8_E4M3 && c->dtype != PKV_KV8_INT8)) return PKV_ERR_INVALID;
+  if (c->scale_block < 1 || c->scale_block > kKv8MaxBlock || ws->page_size % c->scale_block != 0)
+    return PKV_ERR_INVALID;
+  if (ws->head_dim != 64 && ws->head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (!c->k_pool || !c->v_pool || !c->k_scale || !c->v_scale) return PKV_ERR_INVALID;
+  if (!aligned16(c->k_pool) || !aligned16(c->v_pool) || !aligned4(c->k_scale) ||
+      !aligned4(c->v_scale))
+    return PKV_ERR_INVALID;
+  return PKV_OK;
+}
+
+size_t pkv_kv8_bytes(const pkv_workspace *ws, const pkv_kv8 *c, const char *which) {
+  if (!ws || !c || !which || ws->page_size <= 0 || c->scale_block <= 0 ||
+      ws->page_size % c->scale_block != 0)
+    return 0;
+  const size_t rows = (size_t)(ws->n_layers > 0 ? ws->n_layers : 0) *
+                      (ws->pool_slots > 0 ? ws->pool_slots : 0) *
+                      (ws->n_kv_heads > 0 ? ws->n_kv_heads : 0);
+  if (!strcmp(which, "k_pool") || !strcmp(which, "v_pool"))
+    return rows * (ws->head_dim > 0 ? ws->head_dim : 0);
+  if (!strcmp(which, "k_scale") || !strcmp(which, "v_scale")) return rows / c->scale_block * 4;
+  return 0;
+}
+
+pkv_status pkv_kv8_append(const pkv_workspace *ws, const pkv_kv8 *c, int batch, int layer_begin,
+                          int layer_count, const void *k_new, const void *v_new,
+                          pkv_stream_t stream) {
+  pkv_status st = check_kv8(ws, c);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || layer_begin < 0 || layer_count < 0) return PKV_ERR_INVALID;
+  if (batch > ws->max_batch || (long long)layer_begin + layer_count > ws->n_layers ||
+      layer_count > 65535)
+    return PKV_ERR_CAPACITY;
+  if (batch == 0 || layer_count == 0) return PKV_OK;
+  if (!ws->out_loc || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))
+    return PKV_ERR_INVALID;
+  return from_cuda(launch_kv8_append(*ws, *c, batch, layer_begin, layer_count, k_new, v_new,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_kv8_extend_append(const pkv_workspace *ws, const pkv_kv8 *c, int batch, int layer,
+                                 const int32_t *qo_indptr, int max_qo_len, const void *k_new,
+                                 const void *v_new, pkv_stream_t stream) {
+  pkv_status st = check_kv8(ws, c);
+  if (st != PKV_OK) return st;
+  if ((st = check_index(ws)) != PKV_OK) return st;
+  if (batch < 0 || layer < 0 || max_qo_len < 0) return PKV_ERR_INVALID;
+  if (batch > ws->max_batch || layer >= ws->n_layers) return PKV_ERR_CAPACITY;
+  if (!qo_indptr || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))
+    return PKV_ERR_INVALID;
+  if (batch == 0 || max_qo_len == 0) return PKV_OK;
+  return from_cuda(launch_kv8_extend_append(*ws, *c, batch, layer, qo_indptr, max_qo_len, k_new,
+                                            v_new, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_kv8_read(const pkv_workspace *ws, const pkv_kv8 *c, int batch, int layer,
+                        const int32_t *starts, const int32_t *dst_indptr, int n_rows, void *k_out,
+                        void *v_out, int flags, pkv_stream_t stream) {
+  pkv_status st = check_kv8(ws, c);
+  if (st != PKV_OK) return st;
+  if ((st = check_index(ws)) != PKV_OK) return st;
+  if (batch < 0 || layer < 0 || n_rows < 0 || (flags & ~PKV_FLAG_OUT_F32)) return PKV_ERR_INVALID;
+  if (batch > ws->max_batch || layer >= ws->n_layers) return PKV_ERR_CAPACITY;
+  if (!dst_indptr || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+    return PKV_ERR_INVALID;
+  if (batch == 0) return PKV_OK;
+  return from_cuda(launch_kv8_read(*ws, *c, batch, layer, starts, dst_indptr, n_rows, k_out, v_out,
+                                   flags, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_kv8_decode_layer(const pkv_workspace *ws, const pkv_kv8 *c, int batch, int layer,
+                                const void *q, const void *k_new, const void *v_new, float scale,
+                                int num_splits, int flags, pkv_stream_t stream) {
+  pkv_status st = check_kv8(ws, c);
+  if (st != PKV_OK) return st;
+  if ((st = check_index(ws)) != PKV_OK) return st;
+  if (batch < 0 || layer < 0 || num_splits < 1 ||
+      (flags & ~(PKV_FLAG_OUT_F32 | PKV_FLAG_WRITE_LSE | PKV_FLAG_PLAN_EARLY)))
+    return PKV_ERR_INVALID;
+  if (batch > ws->max_batch || layer >= ws->n_layers || num_splits > ws->max_splits)
+    return PKV_ERR_CAPACITY;
+  if (!kv8_decode_supported(ws->head_dim, ws->n_q_heads / ws->n_kv_heads))
+    return PKV_ERR_UNSUPPORTED;
+  if (!q || !ws->out || !aligned16(q) || !aligned16(ws->out)) return PKV_ERR_INVALID;
+  if (num_splits > 1 && (!ws->o_part || !ws->ml_part || !aligned16(ws->o_part) ||
+                         !aligned8(ws->ml_part) || !ws->split_counters))
+    return PKV_ERR_INVALID;
+  if ((flags & PKV_FLAG_WRITE_LSE) && !ws->lse) return PKV_ERR_INVALID;
+  if ((k_new == nullptr) != (v_new == nullptr)) return PKV_ERR_INVALID;
+  if (k_new && (!aligned16(k_new) || !aligned16(v_new) || !ws->out_loc)) return PKV_ERR_INVALID;
+  if ((long long)num_splits * batch * ws->n_q_heads > 0x7fffffffll) return PKV_ERR_CAPACITY;
+  if (batch == 0) return PKV_OK;
+  const Kv8Args a{*ws, *c, batch, layer, q, k_new, v_new, scale, num_splits, flags, 0};
+  return from_cuda(launch_kv8_decode(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, const void *q,
+                            int64_t q_stride, const void *k, int64_t k_stride,
+                            const int32_t *positions, void *q_out, int64_t q_out_stride,
+                            void *k_out, int64_t k_out_stride, pkv_stream_t stream) {
+  if (!args || n_tokens < 0 || args->n_q_heads < 1 || args->n_kv_heads < 0 || !args->err ||
+      args->max_positions < 0 || !(args->eps >= 0.f) || args->reserved != 0 ||
+      (args->interleaved != 0 && args->interleaved != 1))
+    return PKV_ERR_INVALID;
+  const int D = args->head_dim, rot = args->rot_dim;
+  if (D != 64 && D != 128 && D != 256) return PKV_ERR_UNSUPPORTED;
+  if (rot < 0 || rot > D || rot % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  if (!aligned16(args->q_weight) || !aligned16(args->k_weight) || !aligned16(args->cos_sin))
+    return PKV_ERR_INVALID;
+  if (rot > 0 && (!args->cos_sin || !positions)) return PKV_ERR_INVALID;
+  const int64_t qw = (int64_t)args->n_q_heads * D, kw = (int64_t)args->n_kv_heads * D;
+  if (!q || !q_out || !aligned16(q) || !aligned16(q_out) || q_stride % 8 || q_out_stride % 8 ||
+      q_stride < qw || q_out_stride < qw)
+    return PKV_ERR_INVALID;
+  if (kw > 0 && (!k || !k_out || !aligned16(k) || !aligned16(k_out) || k_stride % 8 ||
+                 k_out_stride % 8 || k_stride < kw || k_out_stride < kw))
+    return PKV_ERR_INVALID;
+  if (n_tokens == 0) return PKV_OK;
+  return from_cuda(launch_qk_norm_rope(*args, n_tokens, q, q_stride, k, k_stride, positions, q_out,
+                                       q_out_stride, k_out, k_out_stride,
+                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int pkv_is_steady_increment(const int64_t *prev_ids, const int32_t *prev_lens, int n_prev,

@@ -1,0 +1,544 @@
+"""The 8-bit cache's operators on the GPU against the 64-bit oracle: append (one
+row, chunks), read-back and decode attention.
+
+Codes, scales and read-back values are compared bit for bit: every scale is a
+power of two, so the values that are rounded are exact.  Attention is held to
+the bounds of Problem.attention (derived from the roundings it makes)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.kv8 as K8
+import oracle.ref as R
+import pkv_inputs as W
+from kv8_problem import K8_values, Problem, check_attention
+from paged_kv_decode_bind_gb300 import _abi as A
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = 2.0 ** -8, 2.0 ** -24
+
+# (page size, scale block): one block a page, several, one token each, odd
+# sizes, blocks over several 16-token pieces, token-level indices
+PAGES = [(16, 16), (16, 4), (32, 32), (8, 8), (5, 5), (12, 3), (48, 24), (64, 64), (128, 128),
+         (1, 1)]
+
+
+def _problem(lens, dtype="e4m3", page=16, block=16, heads=(8, 2), d=128, layers=1, steps=0,
+             seed=7, outlier=0.0):
+    p = W.make_problem(batch=len(lens), n_layers=layers, n_q_heads=heads[0], n_kv_heads=heads[1],
+                       head_dim=d, page_size=page, seq_lens=lens, steps=steps, seed=seed,
+                       pool_factor=1.3, outlier_frac=outlier)
+    return Problem(p, dtype, block)
+
+
+def _same(cache, prob):
+    torch.cuda.synchronize()
+    for got, want in ((cache.k_pool, prob.k.codes), (cache.v_pool, prob.v.codes),
+                      (cache.k_scale, prob.k.scales), (cache.v_scale, prob.v.scales)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+def _rows(shape, seed, spread=1.5):
+    """bf16 rows whose sizes differ, so that some make their block's scale grow."""
+    g = torch.Generator().manual_seed(seed)
+    size = torch.exp(torch.randn(shape[:-1] + (1,), generator=g) * spread)
+    return (torch.randn(shape, generator=g) * size).bfloat16()
+
+
+def _attend(prob, ws, cache, q, S, lens, flags=0, new=(None, None), layer=0, what=""):
+    B = prob.p.batch
+    f32 = flags & A.PKV_FLAG_OUT_F32
+    A.pkv_kv8_decode_layer(ws, cache, B, layer, q, *new, prob.p.scale, S,
+                           flags | A.PKV_FLAG_WRITE_LSE)
+    torch.cuda.synchronize()
+    got = (ws.out_f32(B) if f32 else ws.out_bf16(B)).double().cpu().numpy()
+    check_attention(got, ws.lse[:B].double().cpu().numpy(),
+                    prob.attention(layer, q.cpu(), lens), what, F32 if f32 else BF16)
+    assert int(ws.err.item()) == 0
+    assert int(ws.split_counters.abs().sum()) == 0
+    return got
+
+
+# ------------------------------------------------------------------ append ----
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("page,block", PAGES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_rows(cuda, dtype, page, block, d):
+    lens = [1, 2, page, page + 1, 3 * page + 2, 37]
+    prob = _problem(lens, dtype, page, block, d=d, layers=2)
+    ws, cache = prob.device()
+    k, v = _rows((2, len(lens), 2, d), 1), _rows((2, len(lens), 2, d), 2)
+    A.pkv_kv8_append(ws, cache, len(lens), 0, 2, k.cuda(), v.cuda())
+    for layer in range(2):
+        for b, n in enumerate(lens):
+            for side, x in ((prob.k, k), (prob.v, v)):
+                side.append(layer, prob.slots(b, n - 1, n), K8_values(x[layer, b:b + 1]))
+    _same(cache, prob)
+    assert int(ws.err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("hkv", [1, 3, 40])
+def test_append_head_counts(cuda, dtype, hkv):
+    # 40 heads: more rows than one pass of the block holds
+    lens = [5, 20]
+    prob = _problem(lens, dtype, heads=(hkv, hkv))
+    ws, cache = prob.device()
+    k, v = _rows((1, 2, hkv, 128), 3), _rows((1, 2, hkv, 128), 4)
+    A.pkv_kv8_append(ws, cache, 2, 0, 1, k.cuda(), v.cuda())
+    for b, n in enumerate(lens):
+        prob.k.append(0, prob.slots(b, n - 1, n), K8_values(k[0, b:b + 1]))
+        prob.v.append(0, prob.slots(b, n - 1, n), K8_values(v[0, b:b + 1]))
+    _same(cache, prob)
+
+
+SPECIAL = [0.0, -0.0, float("inf"), float("-inf"), float("nan"), 3e38, -3e38, 1e-38, 448.0, 449.0,
+           127.0, 127.5, 2.0 ** -9, 2.0 ** -10, -2.0 ** -10, 1e-30]
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("fill", ["mixed", "zero", "nan", "inf", "huge", "tiny"])
+def test_append_special_values(cuda, dtype, fill):
+    lens = [1, 9, 16]
+    prob = _problem(lens, dtype)
+    ws, cache = prob.device()
+    k = torch.zeros((1, 3, 2, 128))
+    if fill == "mixed":
+        k[...] = torch.tensor(SPECIAL * 8)
+    else:
+        k += {"zero": 0.0, "nan": float("nan"), "inf": float("-inf"), "huge": 3e38,
+              "tiny": 1e-39}[fill]
+    k = k.bfloat16()
+    v = -k
+    A.pkv_kv8_append(ws, cache, 3, 0, 1, k.cuda(), v.cuda())
+    with np.errstate(invalid="ignore", over="ignore"):
+        for b, n in enumerate(lens):
+            prob.k.append(0, prob.slots(b, n - 1, n), K8_values(k[0, b:b + 1]))
+            prob.v.append(0, prob.slots(b, n - 1, n), K8_values(v[0, b:b + 1]))
+    torch.cuda.synchronize()
+    for got, want in ((cache.k_pool, prob.k.codes), (cache.v_pool, prob.v.codes)):
+        got = got.cpu().numpy()
+        if dtype == "e4m3":  # the sign of a NaN is not kept by the conversion
+            got, want = np.where(got == 0xff, 0x7f, got), np.where(want == 0xff, 0x7f, want)
+        assert np.array_equal(got, want)
+    assert np.array_equal(cache.k_scale.cpu().numpy(), prob.k.scales)
+    assert np.array_equal(cache.v_scale.cpu().numpy(), prob.v.scales)
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("page,block", PAGES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_chunks(cuda, dtype, page, block, d):
+    before = [0, 1, page - 1, page, 2 * page + 3, 40]
+    new = [3 * page + 1, 1, 2, 0, 5, 70]
+    lens = [a + b for a, b in zip(before, new)]
+    prob = _problem(lens, dtype, page, block, d=d, layers=2)
+    ws, cache = prob.device()
+    T = sum(new)
+    qo = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    k, v = _rows((T, 2, d), 5), _rows((T, 2, d), 6)
+    A.pkv_kv8_extend_append(ws, cache, len(lens), 1, torch.from_numpy(qo).cuda(), max(new),
+                            k.cuda(), v.cuda())
+    for b in range(len(lens)):
+        s = prob.slots(b, before[b], lens[b])
+        i = 0
+        while i < len(s):  # the oracle takes runs of consecutive slots of a block
+            n = min(len(s) - i, block - int(s[i]) % page % block)
+            prob.k.append(1, s[i:i + n], K8_values(k[qo[b] + i:qo[b] + i + n]))
+            prob.v.append(1, s[i:i + n], K8_values(v[qo[b] + i:qo[b] + i + n]))
+            i += n
+    _same(cache, prob)
+    assert int(ws.err.item()) == 0
+
+
+# --------------------------------------------------------------- read-back ----
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("page,block", PAGES)
+@pytest.mark.parametrize("d,hkv", [(64, 1), (128, 3)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_read(cuda, dtype, page, block, d, hkv, f32):
+    lens = [0, 1, page, 3 * page + 1, 75]
+    starts = [0, 0, 1, page, 75]
+    prob = _problem(lens, dtype, page, block, heads=(hkv, hkv), d=d, layers=2)
+    ws, cache = prob.device()
+    rows = [n - s for n, s in zip(lens, starts)]
+    dst = np.cumsum([3] + rows[:-1]).astype(np.int32) + 2 * np.arange(len(rows), dtype=np.int32)
+    total = int(dst[-1] + rows[-1] + 4)
+    dt = torch.float32 if f32 else torch.bfloat16
+    k = torch.full((total, hkv, d), -7.0, dtype=dt, device="cuda")
+    v = torch.full_like(k, -7.0)
+    A.pkv_kv8_read(ws, cache, len(lens), 1, torch.tensor(starts, dtype=torch.int32).cuda(),
+                   torch.from_numpy(dst).cuda(), total, k, v, A.PKV_FLAG_OUT_F32 if f32 else 0)
+    torch.cuda.synchronize()
+    for got, side in ((k, prob.k), (v, prob.v)):
+        want = np.full((total, hkv, d), -7.0)  # rows that no token maps to stay
+        for b in range(len(lens)):
+            want[dst[b]:dst[b] + rows[b]] = side.rows(1, prob.slots(b, starts[b], lens[b]))
+        assert np.array_equal(got.double().cpu().numpy(), want)
+    assert int(ws.err.item()) == 0
+
+
+def test_read_rounds_other_scales_once(cuda):
+    # a calibrated scale need not be a power of two
+    prob = _problem([20], "int8")
+    prob.k.scales *= np.float32(0.7)
+    ws, cache = prob.device()
+    k = torch.zeros((20, 2, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    A.pkv_kv8_read(ws, cache, 1, 0, None, torch.zeros(1, dtype=torch.int32).cuda(), 20, k, v)
+    want = prob.k.rows(0, prob.slots(0, 0, 20))
+    got = k.double().cpu().numpy()
+    # code * scale to fp32, then to bf16
+    assert np.all(np.abs(got - want) <= np.abs(want) * (BF16 + 2 * F32))
+
+
+# --------------------------------------------------------------- attention ----
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("heads", [(2, 2), (4, 2), (8, 2), (24, 3), (32, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S", [1, 3])
+def test_attention_heads(cuda, dtype, heads, d, S):
+    lens = [1, 17, 300, 0, 64, 129]
+    prob = _problem(lens, dtype, heads=heads, d=d, outlier=0.02)
+    ws, cache = prob.device(max_splits=S)
+    q = W.normal_bf16((len(lens), heads[0], d), 11).cuda()
+    _attend(prob, ws, cache, q, S, lens, what=f"{dtype} {heads} {d} {S}")
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("page,block", PAGES)
+@pytest.mark.parametrize("S", [1, 4])
+def test_attention_pages(cuda, dtype, page, block, S):
+    lens = [1, 15, 16, 33, page + 1, 500]
+    prob = _problem(lens, dtype, page, block)
+    ws, cache = prob.device(max_splits=S)
+    q = W.normal_bf16((len(lens), 8, 128), 12).cuda()
+    _attend(prob, ws, cache, q, S, lens, what=f"{page} {block} {S}")
+
+
+@pytest.mark.parametrize("S", [1, 2, 7, 16])
+def test_attention_splits_long(cuda, S):
+    lens = [4097, 2000, 5]
+    prob = _problem(lens, "e4m3", heads=(8, 2))
+    ws, cache = prob.device(max_splits=S)
+    q = W.normal_bf16((3, 8, 128), 13).cuda()
+    _attend(prob, ws, cache, q, S, lens, A.PKV_FLAG_OUT_F32, what=f"S={S}")
+
+
+@pytest.mark.parametrize("B", [33, 200, 257, 300])
+def test_attention_batches(cuda, B):
+    # past 32 and 256 requests the split plan is made another way
+    lens = [(37 * i) % 90 for i in range(B)]
+    prob = _problem(lens, "int8", heads=(2, 1), d=64)
+    ws, cache = prob.device(max_splits=2)
+    q = W.normal_bf16((B, 2, 64), 14).cuda()
+    for S in (1, 2):
+        _attend(prob, ws, cache, q, S, lens, what=f"B={B} S={S}")
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+def test_attention_scales_far_apart(cuda, dtype):
+    # value blocks of very different sizes, zero blocks among them, and keys that
+    # move the maximum from block to block
+    lens = [200, 64]
+    prob = _problem(lens, dtype, block=4)
+    rng = np.random.default_rng(5)
+    shape = prob.v.scales.shape
+    prob.v.scales[...] = 2.0 ** rng.integers(-30, 31, shape)
+    prob.v.codes[:, ::7] = 0
+    prob.k.scales[...] = 2.0 ** rng.integers(-12, 0, shape)
+    ws, cache = prob.device(max_splits=3)
+    q = W.normal_bf16((2, 8, 128), 15).cuda()
+    for S in (1, 3):
+        _attend(prob, ws, cache, q, S, lens, A.PKV_FLAG_OUT_F32, what=f"S={S}")
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -20, 2.0 ** 20, 2.0 ** 100])
+def test_attention_query_sizes(cuda, size):
+    # queries far outside the range of 16-bit floats, with a scale that undoes it
+    lens = [100, 31]
+    prob = _problem(lens)
+    prob.p.scale = float(np.float32(prob.p.scale / size))
+    ws, cache = prob.device(max_splits=2)
+    q = (W.normal_bf16((2, 8, 128), 16).float() * size).bfloat16().cuda()
+    _attend(prob, ws, cache, q, 2, lens, what=f"{size}")
+
+
+def test_attention_ignores_what_no_token_holds(cuda):
+    # NaN codes, and NaN and infinite scales, in every slot that no live token
+    # uses, page tails included
+    lens = [1, 18, 250, 0]
+    prob = _problem(lens, "e4m3", block=1)
+    used = np.zeros(prob.p.pool_slots, dtype=bool)
+    for b, n in enumerate(lens):
+        used[prob.slots(b, 0, n)] = True
+    for side, bad in ((prob.k, np.nan), (prob.v, np.inf)):
+        side.codes[:, ~used] = 0x7f
+        free = ~used.reshape(-1, 16)
+        side.scales.transpose(0, 1, 3, 2)[:, free] = bad
+    ws, cache = prob.device(max_splits=3)
+    q = W.normal_bf16((4, 8, 128), 17).cuda()
+    for S in (1, 3):
+        _attend(prob, ws, cache, q, S, lens, what=f"S={S}")
+
+
+def test_attention_nan_reaches_its_own_request_only(cuda):
+    lens = [40, 40]
+    prob = _problem(lens)
+    prob.k.codes[0, prob.slots(0, 7, 8)[0], 1, 3] = 0x7f
+    ws, cache = prob.device(max_splits=2)
+    q = W.normal_bf16((2, 8, 128), 18).cuda()
+    A.pkv_kv8_decode_layer(ws, cache, 2, 0, q, None, None, prob.p.scale, 2)
+    got = ws.out_bf16(2).double().cpu().numpy()
+    assert np.isnan(got[0, 4:]).all()  # the heads of KV head 1
+    got[0, 4:] = 0
+    o, _, bo, _ = prob.attention(0, q.cpu(), lens)
+    o[0, 4:] = 0
+    bo[0, 4:] = 0
+    check_attention(got, None, (o, None, bo, None), "others", BF16)
+
+
+@pytest.mark.parametrize("batch", [1, 2])
+def test_rows_behind_the_batch_are_left(cuda, batch):
+    prob = _problem([30, 40, 50])
+    ws, cache = prob.device(max_splits=2)
+    q = W.normal_bf16((3, 8, 128), 19).cuda()
+    ws.out.fill_(5.0)
+    ws.lse.fill_(5.0)
+    A.pkv_kv8_decode_layer(ws, cache, batch, 0, q, None, None, prob.p.scale, 2,
+                           A.PKV_FLAG_OUT_F32 | A.PKV_FLAG_WRITE_LSE)
+    torch.cuda.synchronize()
+    assert torch.all(ws.out[batch:] == 5.0) and torch.all(ws.lse[batch:] == 5.0)
+    assert not torch.any(ws.out[:batch] == 5.0)
+
+
+# ------------------------------------------------------- the layer together ----
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("page,block", PAGES)
+def test_decode_steps(cuda, dtype, page, block):
+    # bind, append and attend for several steps, across block and page ends;
+    # one request starts empty
+    lens, steps, layers = [0, 14, 15, 130], 5, 2
+    prob = _problem(lens, dtype, page, block, layers=layers, steps=steps)
+    ws, cache = prob.device(max_splits=3)
+    B = len(lens)
+    for step in range(steps):
+        q, k, v = W.step_inputs(prob.p, step)
+        k = _rows(tuple(k.shape), 100 + step, 1.0)
+        A.pkv_bind_step(ws, B, A.PKV_BIND_STEADY)
+        lens = [n + 1 for n in lens]
+        for layer in range(layers):
+            for b, n in enumerate(lens):
+                prob.k.append(layer, prob.slots(b, n - 1, n), K8_values(k[layer, b:b + 1]))
+                prob.v.append(layer, prob.slots(b, n - 1, n), K8_values(v[layer, b:b + 1]))
+            _attend(prob, ws, cache, q[layer].cuda(), 3, lens, new=(k[layer].cuda(), v[layer].cuda()),
+                    layer=layer, what=f"step {step}")
+    _same(cache, prob)
+
+
+def test_chunk_then_read_then_decode(cuda):
+    before, new = [0, 21], [40, 9]
+    lens = [a + b for a, b in zip(before, new)]
+    prob = _problem(lens, "int8", steps=1)
+    ws, cache = prob.device(max_splits=2)
+    qo = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    k, v = _rows((49, 2, 128), 21), _rows((49, 2, 128), 22)
+    A.pkv_kv8_extend_append(ws, cache, 2, 0, torch.from_numpy(qo).cuda(), 40, k.cuda(), v.cuda())
+    for b in range(2):
+        s = prob.slots(b, before[b], lens[b])
+        i = 0
+        while i < len(s):
+            n = min(len(s) - i, 16 - int(s[i]) % 16)
+            prob.k.append(0, s[i:i + n], K8_values(k[qo[b] + i:qo[b] + i + n]))
+            prob.v.append(0, s[i:i + n], K8_values(v[qo[b] + i:qo[b] + i + n]))
+            i += n
+    rk = torch.zeros((sum(lens), 2, 128), dtype=torch.bfloat16, device="cuda")
+    rv = torch.zeros_like(rk)
+    A.pkv_kv8_read(ws, cache, 2, 0, None, ws.kv_indptr, sum(lens), rk, rv)
+    want = np.concatenate([prob.k.rows(0, prob.slots(b, 0, n)) for b, n in enumerate(lens)])
+    assert np.array_equal(rk.double().cpu().numpy(), want)
+    q, k1, v1 = W.step_inputs(prob.p, 0)
+    A.pkv_bind_step(ws, 2, A.PKV_BIND_STEADY)
+    for b, n in enumerate(lens):
+        prob.k.append(0, prob.slots(b, n, n + 1), K8_values(k1[0, b:b + 1]))
+        prob.v.append(0, prob.slots(b, n, n + 1), K8_values(v1[0, b:b + 1]))
+    _attend(prob, ws, cache, q[0].cuda(), 2, [n + 1 for n in lens],
+            new=(k1[0].cuda(), v1[0].cuda()))
+    _same(cache, prob)
+
+
+def test_graph_replay_and_other_stream(cuda):
+    lens = [33, 500]
+    prob = _problem(lens, steps=4)
+    ws, cache = prob.device(max_splits=4)
+    q, k, v = (x[0].cuda() for x in W.step_inputs(prob.p, 0))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def step(stream):
+        A.pkv_bind_step(ws, 2, A.PKV_BIND_STEADY, stream=stream)
+        A.pkv_kv8_decode_layer(ws, cache, 2, 0, q, k, v, prob.p.scale, 4, A.PKV_FLAG_WRITE_LSE,
+                               stream=stream)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        step(torch.cuda.current_stream())
+    for n in range(2):  # replayed, then eagerly on a stream of its own
+        g.replay()
+    torch.cuda.synchronize()
+    step(side)
+    torch.cuda.synchronize()
+    for n in range(1, 4):
+        for b in range(2):
+            s = prob.slots(b, lens[b] + n - 1, lens[b] + n)
+            prob.k.append(0, s, K8_values(k[b:b + 1].cpu()))
+            prob.v.append(0, s, K8_values(v[b:b + 1].cpu()))
+    _same(cache, prob)
+    got = ws.out_bf16(2).double().cpu().numpy()
+    check_attention(got, ws.lse[:2].double().cpu().numpy(),
+                    prob.attention(0, q.cpu(), [n + 3 for n in lens]), "graph", BF16)
+    assert int(ws.err.item()) == 0
+
+
+# ------------------------------------------------------------ device errors ----
+def _bad_page(ws, prob, b, col, value):
+    ws.page_table[int(prob.p.req_pool_indices[b]), col] = value
+
+
+@pytest.mark.parametrize("page", [16, 8])
+@pytest.mark.parametrize("value", [-1, 1 << 30])
+@pytest.mark.parametrize("S", [1, 3])
+def test_attention_bad_page(cuda, page, value, S):
+    lens = [200, 150]
+    prob = _problem(lens, page=page, block=8)
+    ws, cache = prob.device(max_splits=S)
+    _bad_page(ws, prob, 0, 3, value)
+    q = W.normal_bf16((2, 8, 128), 23).cuda()
+    A.pkv_kv8_decode_layer(ws, cache, 2, 0, q, None, None, prob.p.scale, S, A.PKV_FLAG_WRITE_LSE)
+    torch.cuda.synchronize()
+    assert int(ws.err.item()) == A.PKV_DEVERR_PAGE
+    assert int(ws.split_counters.abs().sum()) == 0
+    got, lse = ws.out_bf16(2).double().cpu().numpy(), ws.lse[:2].double().cpu().numpy()
+    assert np.isfinite(got).all()
+    if S == 1:
+        assert (got[0] == 0).all() and np.isneginf(lse[0]).all()
+    ref = prob.attention(0, q.cpu(), lens)
+    check_attention(got[1:], lse[1:], tuple(x[1:] for x in ref), "the other request", BF16)
+
+
+@pytest.mark.parametrize("S", [1, 2])
+def test_attention_bad_lengths_and_rows(cuda, S):
+    prob = _problem([50, 60, 70, 80])
+    ws, cache = prob.device(max_splits=S)
+    ws.seq_lens[0] = -3
+    ws.seq_lens[1] = prob.p.max_pages_per_req * 16 + 1
+    ws.req_pool_indices[2] = prob.p.max_reqs
+    q = W.normal_bf16((4, 8, 128), 24).cuda()
+    A.pkv_kv8_decode_layer(ws, cache, 4, 0, q, None, None, prob.p.scale, S, A.PKV_FLAG_WRITE_LSE)
+    torch.cuda.synchronize()
+    assert int(ws.err.item()) == A.PKV_DEVERR_LEN | A.PKV_DEVERR_PAGE
+    got, lse = ws.out_bf16(4).double().cpu().numpy(), ws.lse[:4].double().cpu().numpy()
+    assert (got[:3] == 0).all() and np.isneginf(lse[:3]).all()
+    ref = prob.attention(0, q.cpu(), [0, 0, 0, 80])
+    check_attention(got, lse, ref, "the good request", BF16)
+
+
+def test_flat_bad_slot_and_total(cuda):
+    prob = _problem([30, 40, 50], page=1, block=1)
+    ws, cache = prob.device(max_splits=2)
+    ws.kv_indices[35] = prob.p.pool_slots  # token 5 of request 1
+    ws.struct.max_total_tokens = 100       # request 2 ends at 120
+    q = W.normal_bf16((3, 8, 128), 25).cuda()
+    A.pkv_kv8_decode_layer(ws, cache, 3, 0, q, None, None, prob.p.scale, 1, A.PKV_FLAG_WRITE_LSE)
+    torch.cuda.synchronize()
+    assert int(ws.err.item()) == A.PKV_DEVERR_SLOT | A.PKV_DEVERR_TOTAL
+    got, lse = ws.out_bf16(3).double().cpu().numpy(), ws.lse[:3].double().cpu().numpy()
+    assert (got[1:] == 0).all() and np.isneginf(lse[1:]).all()
+    ref = prob.attention(0, q.cpu(), [30, 0, 0])
+    check_attention(got, lse, ref, "the good request", BF16)
+
+
+def test_append_bad_slot(cuda):
+    prob = _problem([20, 30, 40])
+    ws, cache = prob.device()
+    ws.out_loc[0], ws.out_loc[2] = -1, prob.p.pool_slots
+    k, v = _rows((1, 3, 2, 128), 26), _rows((1, 3, 2, 128), 27)
+    A.pkv_kv8_append(ws, cache, 3, 0, 1, k.cuda(), v.cuda())
+    prob.k.append(0, prob.slots(1, 29, 30), K8_values(k[0, 1:2]))
+    prob.v.append(0, prob.slots(1, 29, 30), K8_values(v[0, 1:2]))
+    _same(cache, prob)
+    assert int(ws.err.item()) == A.PKV_DEVERR_SLOT
+
+
+def test_chunk_bad_requests(cuda):
+    lens, new = [20, 30, 40, 50], [4, 40, 5, 20]  # request 1: more new tokens than it has
+    prob = _problem(lens)
+    ws, cache = prob.device()
+    _bad_page(ws, prob, 3, 2, -5)  # tokens 32 .. 47; new ones are 30 .. 49
+    qo = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    k, v = _rows((69, 2, 128), 28), _rows((69, 2, 128), 29)
+    A.pkv_kv8_extend_append(ws, cache, 4, 0, torch.from_numpy(qo).cuda(), 40, k.cuda(), v.cuda())
+    for b, a, n, at in ((0, 16, 4, 0), (2, 35, 5, 44), (3, 30, 2, 49), (3, 48, 2, 67)):
+        s = prob.slots(b, a, a + n)
+        prob.k.append(0, s, K8_values(k[at:at + n]))
+        prob.v.append(0, s, K8_values(v[at:at + n]))
+    _same(cache, prob)
+    assert int(ws.err.item()) == A.PKV_DEVERR_LEN | A.PKV_DEVERR_PAGE
+
+
+def test_read_bad_requests(cuda):
+    lens = [20, 30, 40, 17, 9]
+    prob = _problem(lens)
+    ws, cache = prob.device()
+    _bad_page(ws, prob, 1, 1, 1 << 20)      # tokens 16 .. 29
+    ws.req_pool_indices[3] = -1
+    starts = torch.tensor([-1, 0, 0, 0, 3], dtype=torch.int32).cuda()
+    dst = torch.tensor([0, 20, 62, 50, 67], dtype=torch.int32).cuda()  # request 2 past the end
+    k = torch.full((80, 2, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, 3.0)
+    A.pkv_kv8_read(ws, cache, 5, 0, starts, dst, 80, k, v)
+    torch.cuda.synchronize()
+    want = np.full((80, 2, 128), 3.0)
+    want[20:36] = prob.k.rows(0, prob.slots(1, 0, 16))
+    want[36:50] = 0
+    want[50:67] = 0
+    want[67:73] = prob.k.rows(0, prob.slots(4, 3, 9))
+    assert np.array_equal(k.double().cpu().numpy(), want)
+    assert int(ws.err.item()) == A.PKV_DEVERR_LEN | A.PKV_DEVERR_TOTAL | A.PKV_DEVERR_PAGE
+
+
+def test_offsets_past_32_bits(cuda):
+    # 3 layers of 2^21 slots x 8 heads x 128 bytes: layer 2 starts at 2^32 bytes
+    from paged_kv_decode_bind_gb300 import Kv8Cache, Workspace
+    slots = 1 << 21
+    ws = Workspace(n_layers=3, pool_slots=slots, n_q_heads=8, n_kv_heads=8, head_dim=128,
+                   page_size=16, max_batch=1, max_reqs=1, max_pages_per_req=2, pools=False)
+    cache = Kv8Cache(ws, dtype="int8", scale_block=16)
+    ws.page_table[0] = torch.tensor([slots // 16 - 1, slots // 16 - 2], dtype=torch.int32)
+    ws.seq_lens[0] = 19
+    A.pkv_bind_step(ws, 1, A.PKV_BIND_REBUILD)
+    k, v = _rows((19, 8, 128), 30, 0.1), _rows((19, 8, 128), 31, 0.1)
+    qo = torch.tensor([0, 19], dtype=torch.int32).cuda()
+    A.pkv_kv8_extend_append(ws, cache, 1, 2, qo, 19, k.cuda(), v.cuda())
+    rk = torch.zeros((19, 8, 128), dtype=torch.bfloat16, device="cuda")
+    rv = torch.zeros_like(rk)
+    A.pkv_kv8_read(ws, cache, 1, 2, None, ws.kv_indptr, 19, rk, rv)
+    q = W.normal_bf16((1, 8, 128), 32)
+    A.pkv_kv8_decode_layer(ws, cache, 1, 2, q.cuda(), None, None, 0.1, 1, A.PKV_FLAG_OUT_F32)
+    torch.cuda.synchronize()
+    # every written element is within half an int8 step of its block's scale
+    for x, y in ((k, rk), (v, rv)):
+        x, y = x.double().numpy(), y.double().cpu().numpy()
+        for a, e in ((0, 16), (16, 19)):
+            amax = np.abs(x[a:e]).max(axis=(0, 2), keepdims=True)
+            s = np.vectorize(lambda m: K8.need(m, "int8"))(amax)
+            assert np.all(np.abs(x[a:e] - y[a:e]) <= s / 2)
+    o, _, mass, _ = K8.attention(K8_values(q)[0], rk.double().cpu().numpy(),
+                                 rv.double().cpu().numpy(), float(np.float32(0.1)))
+    got = ws.out_f32(1).double().cpu().numpy()[0]
+    assert np.all(np.abs(got - o) <= 2.0 ** -10 * mass + 1e-6)
+    # nothing outside the two pages of layer 2
+    lo = int(torch.count_nonzero(cache.k_pool[:2])) + int(torch.count_nonzero(
+        cache.k_pool[2, :slots - 32]))
+    assert lo == 0 and int(ws.err.item()) == 0
