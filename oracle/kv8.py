@@ -98,21 +98,26 @@ class Cache:
                 self.scales[layer, page, h, sub] = s
             i += n
 
-    def rows(self, layer, slots):
-        """Dequantised rows [n, H, D] in float64."""
+    def scale_of(self, layer, slots):
+        """Scales [n, H] of slots, in float64."""
         slots = np.asarray(slots, dtype=np.int64)
         page, inside = slots // self.P, slots % self.P
-        s = self.scales[layer, page, :, inside // self.block].astype(np.float64)
-        return TABLE[self.dtype][self.codes[layer, slots]] * s[..., None]
+        return self.scales[layer, page, :, inside // self.block].astype(np.float64)
+
+    def rows(self, layer, slots):
+        """Dequantised rows [n, H, D] in float64."""
+        return TABLE[self.dtype][self.codes[layer, np.asarray(slots, dtype=np.int64)]] * \
+            self.scale_of(layer, slots)[..., None]
 
 
-def attention(q, k, v, scale):
-    """q [Hq, D], k and v [n, H, D] -> out [Hq, D], lse [Hq], sum_t p_t |v_t| [Hq, D]
-    and max_t sum_d |q_d k_td| * scale [Hq] (both for error bounds)."""
+def attention(q, k, v, scale, v_scale=None):
+    """q [Hq, D], k and v [n, H, D] -> out [Hq, D], lse [Hq] and, for error bounds,
+    sum_t p_t |v_t| [Hq, D], max_t sum_d |q_d k_td| * scale [Hq] and, given v's
+    scales [n, H], max_t(p_t v_scale_t) sum_t |code_t| [Hq, D] (else zeros)."""
     Hq, D = q.shape
     n, H, _ = k.shape
     out, lse = np.zeros((Hq, D)), np.full(Hq, -np.inf)
-    mass, size = np.zeros((Hq, D)), np.zeros(Hq)
+    mass, size, floor = np.zeros((Hq, D)), np.zeros(Hq), np.zeros((Hq, D))
     for h in range(Hq if n else 0):
         g = h // (Hq // H)
         s = k[:, g] @ q[h] * scale
@@ -122,7 +127,10 @@ def attention(q, k, v, scale):
         mass[h] = p @ np.abs(v[:, g]) / p.sum()
         lse[h] = m + math.log(p.sum())
         size[h] = (np.abs(k[:, g]) @ np.abs(q[h])).max() * abs(scale)
-    return out, lse, mass, size
+        if v_scale is not None:
+            vs = v_scale[:, g]
+            floor[h] = (p / p.sum() * vs).max() * np.abs(v[:, g] / vs[:, None]).sum(0)
+    return out, lse, mass, size, floor
 
 
 def norm_rope(x, weight, cos, sin, eps, interleaved):

@@ -163,10 +163,17 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_has_cuda = None
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        # asked once: torch's check costs microseconds, as long as a small launch
+        global _has_cuda
+        if _has_cuda is None:
+            import torch
+            _has_cuda = torch.cuda.current_stream if torch.cuda.is_available() else False
+        return _has_cuda().cuda_stream if _has_cuda else None
     if isinstance(s, int):
         return s
     return s.cuda_stream

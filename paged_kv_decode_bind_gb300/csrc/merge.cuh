@@ -78,7 +78,10 @@ template <int D>
 __device__ __forceinline__ void merge_store(const pkv_workspace &ws, long long row, int flags,
                                             int lane, float M, float den, float4 acc) {
   constexpr int NV = D / 4;
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  // no keys: zeros and lse = -inf; a NaN weight (the 8-bit cache passes NaN
+  // scores on) makes the row NaN
+  const bool nan = den != den;
+  const float inv = den > 0.f ? 1.f / den : (nan ? den : 0.f);
   if (lane < NV) {
     const float4 r = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (flags & PKV_FLAG_OUT_F32) {
@@ -91,7 +94,7 @@ __device__ __forceinline__ void merge_store(const pkv_workspace &ws, long long r
     }
   }
   if (lane == 0 && (flags & PKV_FLAG_WRITE_LSE) && ws.lse)
-    ws.lse[row] = den > 0.f ? M + logf(den) : -INFINITY;
+    ws.lse[row] = den > 0.f ? M + logf(den) : (nan ? den : -INFINITY);
 }
 
 // Merge of the n split partials of NH query-head rows (row0 + j * rstep,

@@ -70,8 +70,9 @@ class Problem:
         outs, lses, bo, bl = [], [], [], []
         for b, n in enumerate(lens):
             s = self.slots(b, 0, n)
-            o, lse, mass, size = K8.attention(q[b], self.k.rows(layer, s), self.v.rows(layer, s),
-                                              self.p.scale)
+            o, lse, mass, size, floor = K8.attention(
+                q[b], self.k.rows(layer, s), self.v.rows(layer, s), self.p.scale,
+                self.v.scale_of(layer, s))
             # score: D products and sums in fp32 plus the two scalings; weight: the
             # exponential of a score off by that (and by a few fp32 steps of its
             # own argument, at most |score|), then one rounding to fp16
@@ -79,8 +80,12 @@ class Problem:
             dw = 2.0 ** -11 + 2 * ds + 2.0 ** -20
             outs.append(o)
             lses.append(lse)
-            # numerator and denominator both carry the weights' error
-            bo.append(2 * dw[:, None] * mass)
+            # numerator and denominator both carry the weights' error.  A weight
+            # p_t v_scale_t below fp16's normal range is off by half its smallest
+            # step, 2^-25, in a unit in which the largest weight of the warp is at
+            # least 2^7 (so at most 2^-32 of the request's largest weight): over all
+            # tokens that is 2^-32 max_t(p_t v_scale_t) sum_t |code_t|
+            bo.append(2 * dw[:, None] * mass + 2.0 ** -32 * floor)
             bl.append(2 * ds + 2.0 ** -20 + 4 * EPS32 * np.abs(np.where(np.isfinite(lse), lse, 0)))
         return np.stack(outs), np.stack(lses), np.stack(bo), np.stack(bl)
 

@@ -283,8 +283,9 @@ def test_attention_ignores_what_no_token_holds(cuda):
         _attend(prob, ws, cache, q, S, lens, what=f"S={S}")
 
 
-def test_attention_nan_reaches_its_own_request_only(cuda):
-    lens = [40, 40]
+@pytest.mark.parametrize("n", [40, 600])
+def test_attention_nan_reaches_its_own_request_only(cuda, n):
+    lens = [n, n]  # 600: over two splits, of which one holds the NaN
     prob = _problem(lens)
     prob.k.codes[0, prob.slots(0, 7, 8)[0], 1, 3] = 0x7f
     ws, cache = prob.device(max_splits=2)
@@ -292,6 +293,7 @@ def test_attention_nan_reaches_its_own_request_only(cuda):
     A.pkv_kv8_decode_layer(ws, cache, 2, 0, q, None, None, prob.p.scale, 2)
     got = ws.out_bf16(2).double().cpu().numpy()
     assert np.isnan(got[0, 4:]).all()  # the heads of KV head 1
+    assert np.isfinite(got[0, :4]).all()
     got[0, 4:] = 0
     o, _, bo, _ = prob.attention(0, q.cpu(), lens)
     o[0, 4:] = 0
@@ -534,7 +536,7 @@ def test_offsets_past_32_bits(cuda):
             amax = np.abs(x[a:e]).max(axis=(0, 2), keepdims=True)
             s = np.vectorize(lambda m: K8.need(m, "int8"))(amax)
             assert np.all(np.abs(x[a:e] - y[a:e]) <= s / 2)
-    o, _, mass, _ = K8.attention(K8_values(q)[0], rk.double().cpu().numpy(),
+    o, _, mass, _, _ = K8.attention(K8_values(q)[0], rk.double().cpu().numpy(),
                                  rv.double().cpu().numpy(), float(np.float32(0.1)))
     got = ws.out_f32(1).double().cpu().numpy()[0]
     assert np.all(np.abs(got - o) <= 2.0 ** -10 * mass + 1e-6)

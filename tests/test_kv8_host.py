@@ -274,7 +274,7 @@ def test_oracle_append_grows_a_block():
 def test_oracle_attention_and_rope():
     k = np.array([[[0.0, 0.0]], [[2.0, 0.0]]])
     v = np.array([[[1.0, 0.0]], [[0.0, 1.0]]])
-    out, lse, mass, size = K8.attention(np.array([[math.log(3.0), 0.0]]), k, v, 0.5)
+    out, lse, mass, size, _ = K8.attention(np.array([[math.log(3.0), 0.0]]), k, v, 0.5)
     assert np.allclose(out, [[0.25, 0.75]]) and np.allclose(lse, [math.log(4.0)])
     y = K8.norm_rope(np.array([[3.0, 4.0, 5.0, 0.0]]), None, np.array([0.0]), np.array([1.0]), 0,
                      False)
