@@ -431,7 +431,8 @@ pkv_status pkv_kv8_decode_layer(const pkv_workspace *ws, const pkv_kv8 *c, int b
   if (st != PKV_OK) return st;
   if ((st = check_index(ws)) != PKV_OK) return st;
   if (batch < 0 || layer < 0 || num_splits < 1 ||
-      (flags & ~(PKV_FLAG_OUT_F32 | PKV_FLAG_WRITE_LSE | PKV_FLAG_PLAN_EARLY)))
+      (flags & ~(PKV_FLAG_OUT_F32 | PKV_FLAG_WRITE_LSE | PKV_FLAG_PLAN_EARLY |
+                 PKV_FLAG_TEST_SKIP_FIRST_TILE)))
     return PKV_ERR_INVALID;
   if (batch > ws->max_batch || layer >= ws->n_layers || num_splits > ws->max_splits)
     return PKV_ERR_CAPACITY;

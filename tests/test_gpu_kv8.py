@@ -461,6 +461,47 @@ def test_flat_bad_slot_and_total(cuda):
     check_attention(got, lse, ref, "the good request", BF16)
 
 
+@pytest.mark.parametrize("S", [1, 2])
+def test_bounded_wait_runs_out(cuda, S):
+    # the hook leaves every warp's first copy unissued: the waits run out (~1 s),
+    # the outputs are empty, and the next launch is as it should be
+    lens = [300, 40]
+    prob = _problem(lens)
+    ws, cache = prob.device(max_splits=S)
+    q = W.normal_bf16((2, 8, 128), 33).cuda()
+    A.pkv_kv8_decode_layer(ws, cache, 2, 0, q, None, None, prob.p.scale, S,
+                           A.PKV_FLAG_TEST_SKIP_FIRST_TILE | A.PKV_FLAG_WRITE_LSE)
+    torch.cuda.synchronize()
+    assert int(ws.err.item()) == A.PKV_DEVERR_TIMEOUT
+    assert torch.all(ws.out_bf16(2) == 0) and torch.all(torch.isneginf(ws.lse[:2]))
+    assert int(ws.split_counters.abs().sum()) == 0
+    ws.err.zero_()
+    _attend(prob, ws, cache, q, S, lens, what="after a timeout")
+
+
+@pytest.mark.parametrize("page", [16, 8])
+def test_early_start(cuda, page):
+    # layers after the first of a step may start before the previous ends: the
+    # same results as without the flag, over several steps
+    lens, layers = [700, 45, 0], 3
+    prob = _problem(lens, page=page, block=8, layers=layers)
+    ws, cache = prob.device(max_splits=4)
+    q = W.normal_bf16((layers, 3, 8, 128), 34).cuda()
+    for rep in range(3):
+        for flag in (0, A.PKV_FLAG_PLAN_EARLY):
+            outs = []
+            A.pkv_bind_step(ws, 3, A.PKV_BIND_REBUILD)
+            for layer in range(layers):
+                A.pkv_kv8_decode_layer(ws, cache, 3, layer, q[layer], None, None, prob.p.scale, 4,
+                                       A.PKV_FLAG_WRITE_LSE | (flag if layer else 0))
+                outs.append((ws.out_bf16(3).clone(), ws.lse[:3].clone()))
+            torch.cuda.synchronize()
+            for layer, (o, l) in enumerate(outs):
+                check_attention(o.double().cpu().numpy(), l.double().cpu().numpy(),
+                                prob.attention(layer, q[layer].cpu(), lens), "early", BF16)
+    assert int(ws.err.item()) == 0
+
+
 def test_append_bad_slot(cuda):
     prob = _problem([20, 30, 40])
     ws, cache = prob.device()
