@@ -207,16 +207,32 @@ __global__ void __launch_bounds__(kKXWarps * 32)
 
 constexpr int kKRThreads = 256;
 constexpr int kKRTokens = 8;  // tokens per tile
+constexpr int kKRUnroll = 4;  // rows whose loads a thread has in flight
 
-// gx CTAs per request walk its tiles of kKRTokens tokens: the tile's slots are
-// resolved once, then each thread turns 8 codes at a time into 8 values
-// (16-byte stores, consecutive threads on consecutive words of a token's row).
+// 32 bytes: one store where the address allows it.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// gx CTAs per request walk its tiles of kKRTokens tokens.  The tile's slots and
+// scale rows are resolved once; then 2^tshift threads share a row of K or V,
+// 16 codes (32 or 64 bytes of values) at a time, with kKRUnroll rows' loads
+// issued before any is used.
 template <int D, int DT, bool F32>
 __global__ void __launch_bounds__(kKRThreads)
     kv8_read_kernel(const __grid_constant__ pkv_workspace ws, const __grid_constant__ pkv_kv8 c,
-                    int layer, int gx, const int *__restrict__ starts,
-                    const int *__restrict__ dst_indptr, int n_rows, void *k_out, void *v_out) {
-  __shared__ int s_slot[kKRTokens];
+                    int layer, int gx, int tshift, const int *__restrict__ starts,
+                    const int *__restrict__ dst_indptr, int n_rows, uint8_t *k_out,
+                    uint8_t *v_out) {
+  __shared__ int s_slot[kKRTokens];         // -1: a bad index entry
+  __shared__ long long s_scale[kKRTokens];  // index of head 0's scale in the layer
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / gx, x = blockIdx.x - b * gx;
@@ -242,7 +258,16 @@ __global__ void __launch_bounds__(kKRThreads)
     if (lead) atomicOr(ws.err, kind);
     return;
   }
-  const int H = ws.n_kv_heads, W = H * (D / 8);  // 8-code words of a token's row
+  const int H = ws.n_kv_heads, W = H * (D / 16);  // 16-code words of a token's row
+  const int per_page = ws.page_size / c.scale_block, n_pages = ws.pool_slots / ws.page_size;
+  const uint4 *kp = static_cast<const uint4 *>(c.k_pool) + (long long)layer * ws.pool_slots * W;
+  const uint4 *vp = static_cast<const uint4 *>(c.v_pool) + (long long)layer * ws.pool_slots * W;
+  const long long srow = (long long)layer * n_pages * H * per_page;
+  const float *ks = c.k_scale + srow, *vs = c.v_scale + srow;
+  constexpr int OB = F32 ? 64 : 32;  // bytes of 16 values
+  const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
+  const int col = threadIdx.x & ((1 << tshift) - 1), rr = threadIdx.x >> tshift;
+  const int rows = kKRThreads >> tshift;  // rows side by side
   for (int t0 = x * kKRTokens; t0 < n; t0 += gx * kKRTokens) {
     const int m = min(kKRTokens, n - t0);
     __syncthreads();  // the last tile's slots are no longer read
@@ -252,36 +277,60 @@ __global__ void __launch_bounds__(kKRThreads)
       else bad = PKV_DEVERR_PAGE;
       if (bad) atomicOr(ws.err, bad);
       s_slot[threadIdx.x] = slot;
+      const int page = slot >= 0 ? slot / ws.page_size : 0;
+      s_scale[threadIdx.x] = (long long)page * H * per_page +
+                             (slot >= 0 ? (slot - page * ws.page_size) / c.scale_block : 0);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < m * 2 * W; i += kKRThreads) {
-      const int r = i / W, w = i - r * W, t = r >> 1, side = r & 1;
-      const int slot = s_slot[t], g = w / (D / 8);
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (slot >= 0) {
-        const uint2 code = reinterpret_cast<const uint2 *>(
-            side ? c.v_pool : c.k_pool)[((long long)layer * ws.pool_slots + slot) * W + w];
-        const float s =
-            (side ? c.v_scale : c.k_scale)[scale_index(ws, c.scale_block, layer, slot, g)];
-        float a[4], e[4];
-        decode4<DT>(code.x, a);
-        decode4<DT>(code.y, e);
+    for (int w = col; w < W; w += 1 << tshift) {
+      const int g = w / (D / 16);
+      // row i of the tile: K of token i, then V of token i - m
+      for (int i0 = rr; i0 < 2 * m; i0 += kKRUnroll * rows) {
+        uint4 code[kKRUnroll];
+        float s[kKRUnroll];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[k] = a[k] * s;
-          f[4 + k] = e[k] * s;
+        for (int k = 0; k < kKRUnroll; ++k) {
+          const int i = i0 + k * rows;
+          const bool isv = i >= m;
+          const int t = isv ? i - m : i;
+          code[k] = make_uint4(0, 0, 0, 0);
+          s[k] = 0.f;
+          if (i < 2 * m && s_slot[t] >= 0) {
+            code[k] = ldg_nc_v4((isv ? vp : kp) + (long long)s_slot[t] * W + w);
+            s[k] = (isv ? vs : ks)[s_scale[t] + (long long)g * per_page];
+          }
         }
-      }
-      const long long o = (row0 + t0 + t) * W + w;
-      void *out = side ? v_out : k_out;
-      if constexpr (F32) {
-        float4 *p = static_cast<float4 *>(out) + 2 * o;
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
-      } else {
-        static_cast<uint4 *>(out)[o] =
-            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                       pack_bf16x2(f[6], f[7]));
+#pragma unroll
+        for (int k = 0; k < kKRUnroll; ++k) {
+          const int i = i0 + k * rows;
+          if (i >= 2 * m) break;
+          const bool isv = i >= m;
+          const int t = isv ? i - m : i;
+          const uint32_t cw[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+          float f[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float a[4];
+            decode4<DT>(cw[e], a);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) f[4 * e + y] = a[y] * s[k];
+          }
+          uint8_t *p = (isv ? v_out : k_out) + ((row0 + t0 + t) * W + w) * OB;
+          if constexpr (F32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t o[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(f[8 * h + e]);
+              store32(p + 32 * h, o, wide);
+            }
+          } else {
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+            store32(p, o, wide);
+          }
+        }
       }
     }
   }
@@ -352,12 +401,17 @@ struct ReadLaunch {
     if (gx > share) gx = share;
     if (gx < 1) gx = 1;
     if (gx * batch > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    // threads per row: the power of two that covers its 16-code words, 256 at most
+    int tshift = 0;
+    while (tshift < 8 && (1 << tshift) < ws.n_kv_heads * (D / 16)) ++tshift;
     const dim3 grid((unsigned)(gx * batch));
     if (flags & PKV_FLAG_OUT_F32)
       return launch_pdl(kv8_read_kernel<D, DT, true>, grid, dim3(kKRThreads), 0, st, ws, c, layer,
-                        (int)gx, starts, dst_indptr, n_rows, k, v);
+                        (int)gx, tshift, starts, dst_indptr, n_rows, static_cast<uint8_t *>(k),
+                        static_cast<uint8_t *>(v));
     return launch_pdl(kv8_read_kernel<D, DT, false>, grid, dim3(kKRThreads), 0, st, ws, c, layer,
-                      (int)gx, starts, dst_indptr, n_rows, k, v);
+                      (int)gx, tshift, starts, dst_indptr, n_rows, static_cast<uint8_t *>(k),
+                      static_cast<uint8_t *>(v));
   }
 };
 

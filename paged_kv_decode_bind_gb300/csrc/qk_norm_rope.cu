@@ -8,6 +8,8 @@
 // of 16 products per lane and a butterfly over the head's lanes, in fp32.  The
 // cosines and sines a lane needs do not depend on the head, so a warp loads
 // them once for all the heads of its token that it handles.
+#include <algorithm>
+
 #include "kernels.cuh"
 
 namespace pkv {
@@ -66,67 +68,78 @@ __global__ void __launch_bounds__(kRWarps * 32) qk_norm_rope_kernel(const __grid
     }
   }
   const int groups = (heads + HPW - 1) / HPW;
-  for (int i = part; i < groups; i += a.per_token) {
-    const int hh = i * HPW + sub;
-    const bool live = hh < heads;
-    const bool isk = hh >= p.n_q_heads;
-    const int h = isk ? hh - p.n_q_heads : hh;
-    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-    if (live) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          isk ? a.k + tok * a.k_stride + (long long)h * D : a.q + tok * a.q_stride + (long long)h * D);
-      x0 = src[c0];
-      x1 = src[c1];
-    }
-    float u[8], v[8];
-    unpack8(x0, u);
-    unpack8(x1, v);
-    float ss = 0.f;
+  constexpr int UN = 2;  // groups whose loads are in flight together
+  for (int i0 = part; i0 < groups; i0 += UN * a.per_token) {
+    uint4 x[UN][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
-#pragma unroll
-    for (int d = LG / 2; d >= 1; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    if (!live) continue;
-    const uint4 *w = static_cast<const uint4 *>(isk ? p.k_weight : p.q_weight);
-    if (w) {
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      float wu[8], wv[8];
-      unpack8(w[c0], wu);
-      unpack8(w[c1], wv);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        u[e] *= r * wu[e];
-        v[e] *= r * wv[e];
+    for (int k = 0; k < UN; ++k) {
+      const int hh = (i0 + k * a.per_token) * HPW + sub;
+      x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
+      if (i0 + k * a.per_token < groups && hh < heads) {
+        const bool isk = hh >= p.n_q_heads;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            isk ? a.k + tok * a.k_stride + (long long)(hh - p.n_q_heads) * D
+                : a.q + tok * a.q_stride + (long long)hh * D);
+        x[k][0] = src[c0];
+        x[k][1] = src[c1];
       }
     }
-    if (turns) {
-      if (p.interleaved) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a0 = u[2 * e], b0 = u[2 * e + 1], a1 = v[2 * e], b1 = v[2 * e + 1];
-          u[2 * e] = a0 * cs[e] - b0 * sn[e];
-          u[2 * e + 1] = b0 * cs[e] + a0 * sn[e];
-          v[2 * e] = a1 * cs[4 + e] - b1 * sn[4 + e];
-          v[2 * e + 1] = b1 * cs[4 + e] + a1 * sn[4 + e];
-        }
-      } else {
+    for (int k = 0; k < UN; ++k) {
+      if (i0 + k * a.per_token >= groups) break;  // warp-uniform
+      const int hh = (i0 + k * a.per_token) * HPW + sub;
+      const bool isk = hh >= p.n_q_heads;
+      const int h = isk ? hh - p.n_q_heads : hh;
+      float u[8], v[8];
+      unpack8(x[k][0], u);
+      unpack8(x[k][1], v);
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
+#pragma unroll
+      for (int d = LG / 2; d >= 1; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+      if (hh >= heads) continue;
+      const uint4 *w = static_cast<const uint4 *>(isk ? p.k_weight : p.q_weight);
+      if (w) {
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        float wu[8], wv[8];
+        unpack8(w[c0], wu);
+        unpack8(w[c1], wv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float x = u[e], y = v[e];
-          u[e] = x * cs[e] - y * sn[e];
-          v[e] = y * cs[e] + x * sn[e];
+          u[e] *= r * wu[e];
+          v[e] *= r * wv[e];
         }
       }
+      if (turns) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a0 = u[2 * e], b0 = u[2 * e + 1], a1 = v[2 * e], b1 = v[2 * e + 1];
+            u[2 * e] = a0 * cs[e] - b0 * sn[e];
+            u[2 * e + 1] = b0 * cs[e] + a0 * sn[e];
+            v[2 * e] = a1 * cs[4 + e] - b1 * sn[4 + e];
+            v[2 * e + 1] = b1 * cs[4 + e] + a1 * sn[4 + e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float y0 = u[e], y1 = v[e];
+            u[e] = y0 * cs[e] - y1 * sn[e];
+            v[e] = y1 * cs[e] + y0 * sn[e];
+          }
+        }
+      }
+      uint4 *dst = reinterpret_cast<uint4 *>(isk ? a.k_out + tok * a.k_out_stride + (long long)h * D
+                                                 : a.q_out + tok * a.q_out_stride + (long long)h * D);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      dst[c0] = bad ? zero
+                    : make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]),
+                                 pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+      dst[c1] = bad ? zero
+                    : make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(isk ? a.k_out + tok * a.k_out_stride + (long long)h * D
-                                               : a.q_out + tok * a.q_out_stride + (long long)h * D);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    dst[c0] = bad ? zero
-                  : make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]),
-                               pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
-    dst[c1] = bad ? zero
-                  : make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 }
 
@@ -134,7 +147,11 @@ template <int D>
 cudaError_t launch_one(RopeArgs a, cudaStream_t st) {
   const int per_warp = 32 / (D / 16);
   const int groups = (a.p.n_q_heads + a.p.n_kv_heads + per_warp - 1) / per_warp;
-  a.per_token = groups;
+  // Warps per token: one per group of heads while that fits about one wave
+  // (decode: latency counts), else as few as still give that many warps, so
+  // that a token's cosines and sines are loaded once for many heads.
+  const long long wave = 152 * 32;
+  a.per_token = (int)std::min<long long>(groups, std::max<long long>(1, wave / a.n_tokens));
   const long long blocks = ((long long)a.n_tokens * a.per_token + kRWarps - 1) / kRWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   return launch_pdl(qk_norm_rope_kernel<D>, dim3((unsigned)blocks), dim3(kRWarps * 32), 0, st, a);
