@@ -163,17 +163,30 @@ def _ptr(x):
     return x.data_ptr()
 
 
-_has_cuda = None
+_current = None
+
+
+def _current_stream():
+    """Handle of the current device's current stream, None without CUDA.  Building
+    torch's Stream object takes microseconds, as long as a small launch, so its
+    raw handle is asked for where torch has a call for that."""
+    global _current
+    if _current is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if not torch.cuda.is_available():
+            _current = lambda: None  # noqa: E731
+        elif raw is not None:
+            dev = torch.cuda.current_device
+            _current = lambda: raw(dev())  # noqa: E731
+        else:
+            _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current()
 
 
 def _stream(s):
     if s is None:
-        # asked once: torch's check costs microseconds, as long as a small launch
-        global _has_cuda
-        if _has_cuda is None:
-            import torch
-            _has_cuda = torch.cuda.current_stream if torch.cuda.is_available() else False
-        return _has_cuda().cuda_stream if _has_cuda else None
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -335,9 +348,10 @@ def _stride(x, width, head_dim):
     [tokens, width] or [tokens, heads, head_dim] with dense heads."""
     if x is None or isinstance(x, int):
         return width
-    if x.stride(-1) != 1 or x.dim() not in (2, 3) or (x.dim() == 3 and x.stride(1) != head_dim):
+    st = x.stride()
+    if st[-1] != 1 or len(st) not in (2, 3) or (len(st) == 3 and st[1] != head_dim):
         raise ValueError("heads must be dense: [tokens, width] or [tokens, heads, head_dim]")
-    return x.stride(0)
+    return st[0]
 
 
 def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None, check=True):

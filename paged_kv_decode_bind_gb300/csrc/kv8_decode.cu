@@ -27,7 +27,7 @@
 // the 16-byte chunks swizzled (TMA's 128- or 64-byte pattern).  Pages of whole
 // pieces come as one TMA box for K and one for V, completing on the stage's
 // mbarrier; other page sizes and flat indices as 16-byte cp.async copies of
-// the rows (whole rows per 8 or 4 lanes).  Fragments are read with plain
+// the rows (whole rows per 8 or 4 lanes), the index entries NS pieces ahead.  Fragments are read with plain
 // 16-byte loads: which token a row of S^T is, and which head_dim an index of
 // the contraction is, is free as long as V and Q agree.  K: lane (r = lane / 4,
 // c = lane % 4) takes 16 bytes of token perm(r); V: 16 (8 at D = 64) bytes of
@@ -57,11 +57,10 @@ struct KCfg {
   static constexpr int THREADS = W * 32;
   static constexpr int KB = 16 * D;                // K (or V) bytes of a piece
   static constexpr int STAGE = 2 * KB;
-  static constexpr int NS = W == 8 ? (D == 128 ? 3 : 4) : (D == 128 ? 6 : 8);  // ring stages
+  static constexpr int NS = W == 8 ? (D == 128 ? 2 : 2) : (D == 128 ? 3 : 4);  // ring stages
   static constexpr int VB = D / 8;                 // V bytes of a row per lane
-  static constexpr int RS = D + 4;                 // row stride of a warp's O (floats)
   static constexpr int SMEM = W * NS * STAGE + 1024;  // + alignment slack
-  static_assert(NS * STAGE >= G * RS * 4, "a warp's O fits its ring");
+  static_assert(STAGE == 8 * D * 4, "a stage holds a warp's O for 8 heads");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
@@ -136,6 +135,34 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi
   }
 }
 
+// A unit of work: tokens [t0, t1) of (request b, KV head g), split c of n.
+struct KUnit {
+  int b, g, c, n, t0, t1;
+  int bad;         // error bits
+  long long base;  // where the request's index entries start
+};
+
+// A block's units in order.
+//
+// Shared out (S > 1, batches of up to kMaxCompactBatch): the requests, one
+// after the other, make a line of 16-token pieces.  The blocks form groups of
+// Hkv, one block per KV head, and each group takes a run of q pieces, so every
+// block has the same number whatever the lengths are; a run that crosses the
+// end of a request becomes two units.  The heads of a token lie side by side in
+// the pool, so the blocks of a group read whole DRAM pages between them (with
+// runs over one head after the other, 4 x 65536 tokens took 138 us, not TIMED).
+// Each request counts kUnitCost pieces more than it has, in front: what a block
+// spends on starting and finishing a unit (2 us against 0.2 us for a piece).
+// q = ceil(line / groups), at least 8 (one piece per warp) and at least
+// ceil(longest request / (S - 1)), so that none lies in more than S runs.
+// Whole pairs (S == 1), or fixed chunks (larger batches): unit u = (split,
+// request, head), every gridDim.x-th one from blockIdx.x.
+constexpr int kUnitCost = 14;
+
+struct KUnits {
+  int q, pos, end, b, chunk;  // pos, end: of the line, or unit numbers
+};
+
 // PAGED: pages hold whole 16-token pieces, loaded as TMA boxes.
 template <int D, int G, int DT, bool PAGED>
 __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
@@ -150,56 +177,191 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   __shared__ int s_pref[kMaxCompactBatch + 1];
   __shared__ int s_len[kMaxCompactBatch];
   __shared__ int s_base[kMaxCompactBatch];
-  __shared__ int s_chunk[kMaxCompactBatch];
   __shared__ float s_scale[W][NS][32];  // K scales of a piece's tokens, then V scales
   __shared__ int s_idx[PAGED ? 1 : W][PAGED ? 1 : 2 * NS][16];
-  __shared__ float s_ml[W][16][2];
-  __shared__ float s_hml[16][2];
+  __shared__ float2 s_ml[W][16];
+  __shared__ int s_slot[W];  // ring slot holding a warp's O, -1: it had no piece
   __shared__ int s_bad[W];
-  __shared__ int s_tmp[32];
-  __shared__ int s_max_len, s_last;
+  __shared__ KUnits s_us;
+  __shared__ KUnit s_unit[3];  // the current unit, the next, the one after
+  __shared__ int s_plan;       // most pieces of a pair / longest length
+  __shared__ int s_merge[2][3];  // splits to merge (0: not by this block), request, head
+  __shared__ int s_seen[PAGED ? 1 : W][NS];  // index entries fetched by a stage's fill
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const pkv_workspace &ws = a.ws;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int Hq = ws.n_q_heads, H = ws.n_kv_heads;
-  const bool early = (a.flags & PKV_FLAG_PLAN_EARLY) != 0;
-  if (!early) {
-    pdl_wait();
-    pdl_trigger();
-  }
   if constexpr (PAGED) {
     // a warp is the only user of its barriers
     if (lane < NS) mbar_init(&s_bar[warp][lane], 1);
     fence_barrier_init();
     __syncwarp();
   }
+  bool waited = false;
+  auto wait_previous = [&]() {
+    if (!waited) {
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+    }
+  };
+  if (!(a.flags & PKV_FLAG_PLAN_EARLY)) wait_previous();
 
+  // ---- the block's share ----
   Plan pl;
   pl.set_pages(ws);
-  pl.batch = a.batch;
-  pl.hkv = H;
-  pl.S = a.num_splits;
-  const bool direct = pl.S == 1;
-  if (a.batch <= kMaxCompactBatch) {
-    const int budget = a.apportion ? (int)gridDim.x : 0;
-    const int pairs = batch_plan_compact(ws, a.batch, pl.S, budget, s_len, s_base, s_pref, s_chunk,
-                                         s_tmp, &s_max_len, &pl.chunk);
-    pl.pref = s_pref;
-    pl.lens = s_len;
-    pl.chunks = budget > 0 ? s_chunk : nullptr;
-    pl.n_units = pairs * H;
-  } else {
-    pl.chunk = split_chunk(batch_max_len(ws, a.batch, &s_max_len), pl.S, ws.page_size);
-    pl.n_units = pl.S * pl.batch * H;
+  const bool compact = a.batch <= kMaxCompactBatch;
+  if (compact) {
+    if (warp == 0) {
+      // lane i holds requests i, i + 32, ...: all loads in flight at once
+      constexpr int PER = kMaxCompactBatch / 32;
+      int len[PER], base[PER];
+      const long long cap = len_cap(ws);
+      const bool flat = ws.index_mode == PKV_IDX_FLAT;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int b = lane + 32 * i;
+        len[i] = b < a.batch ? ws.seq_lens[b] : 0;
+        base[i] = b < a.batch ? (flat ? ws.kv_indptr[b] : ws.req_pool_indices[b]) : 0;
+      }
+      int run = 0, most = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (32 * i >= a.batch) break;
+        const int b = lane + 32 * i;
+        int err = 0;
+        if (len[i] < 0 || (long long)len[i] > cap) err = PKV_DEVERR_LEN;
+        else if (flat && len[i] > 0 &&
+                 (base[i] < 0 || (long long)base[i] + len[i] > ws.max_total_tokens))
+          err = PKV_DEVERR_TOTAL;
+        if (err) {
+          if (blockIdx.x == 0) atomicOr(ws.err, err);
+          len[i] = 0;
+        }
+        const int pcs = len[i] > 0 ? kUnitCost + ((len[i] + 15) >> 4) : 0;
+        most = max(most, pcs);
+        int incl = pcs;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        if (b < a.batch) {
+          s_pref[b] = run + incl - pcs;
+          s_len[b] = len[i];
+          s_base[b] = base[i];
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) s_pref[a.batch] = run;
+      __syncwarp();
+      if (lane == 0 && a.apportion) {
+        const int groups = (int)gridDim.x / H, group = (int)blockIdx.x / H;
+        KUnits us;
+        us.q = max(max((run + groups - 1) / groups, 8),
+                   (most - kUnitCost + a.num_splits - 2) / (a.num_splits - 1));
+        const long long first = group < groups ? (long long)group * us.q : run;
+        us.pos = (int)min(first, (long long)run);
+        us.end = (int)min(first + us.q, (long long)run);
+        us.b = 0;
+        int hi = a.batch - 1;  // last b with pref[b] <= pos
+        while (us.b < hi) {
+          const int mid = (us.b + hi + 1) >> 1;
+          if (s_pref[mid] <= us.pos) us.b = mid;
+          else hi = mid - 1;
+        }
+        s_us = us;
+      }
+    }
+  }
+  if (!a.apportion) {
+    if (a.num_splits > 1) batch_max_len(ws, a.batch, &s_plan);
+    if (tid == 0) {
+      KUnits us;
+      us.q = 0;
+      us.chunk = a.num_splits == 1 ? 0x7ffffff0  // whole requests
+                                   : split_chunk(s_plan, a.num_splits, ws.page_size);
+      us.pos = blockIdx.x;
+      us.end = a.num_splits * a.batch * H;
+      us.b = 0;
+      s_us = us;
+    }
+  }
+
+  // The next unit into *dst by thread 0 (t0 == t1: past the last one).
+  auto next_unit = [&](KUnit *dst) {
+    KUnits us = s_us;
+    KUnit u;
+    u.b = u.g = u.c = u.n = u.t0 = u.t1 = u.bad = 0;
+    u.base = 0;
+    while (us.pos < us.end) {
+      ReqIndex ri;
+      if (a.apportion) {
+        while (s_pref[us.b + 1] <= us.pos) ++us.b;
+        const int real = s_pref[us.b] + kUnitCost, last = s_pref[us.b + 1];  // its pieces
+        const int from = max(us.pos, real), stop = min(us.end, last);
+        us.pos = stop;
+        if (from >= stop) continue;  // the run ends in what the request counts in front
+        const int first = real / us.q;
+        u.b = us.b;
+        u.g = (int)blockIdx.x % H;
+        u.c = (int)blockIdx.x / H - first;
+        u.n = (last - 1) / us.q - first + 1;
+        u.t0 = 16 * (from - real);
+        u.t1 = min(16 * (stop - real), s_len[us.b]);
+        ri = req_index_cached(ws, s_base, us.b);
+      } else {
+        const int hb = a.batch * H;
+        u.c = us.pos / hb;
+        const int x = us.pos - u.c * hb;
+        u.b = x / H;
+        u.g = x - u.b * H;
+        us.pos += gridDim.x;
+        const int L = compact                  ? s_len[u.b]
+                      : u.c == 0 && u.g == 0 ? checked_len(ws, u.b, ws.err)
+                                             : usable_len(ws, u.b);
+        const bool whole = a.num_splits == 1;
+        if (u.c * (long long)us.chunk >= L) continue;  // past the request's end
+        u.t0 = whole ? 0 : u.c * us.chunk;
+        u.t1 = whole ? L : min(u.t0 + us.chunk, L);
+        u.n = whole ? 1 : (L + us.chunk - 1) / us.chunk;
+        ri = compact ? req_index_cached(ws, s_base, u.b) : req_index(ws, u.b);
+      }
+      u.base = ri.base;
+      u.bad = ri.ok ? 0 : PKV_DEVERR_PAGE;
+      s_us = us;
+      *dst = u;
+      return;
+    }
+    s_us = us;
+    u.t0 = u.t1 = 0;
+    *dst = u;
+  };
+  if (tid == 0) {  // in warp 0, which has the arrays
+    next_unit(&s_unit[0]);
+    next_unit(&s_unit[1]);
+  }
+  __syncthreads();
+  // Requests with no usable token have no unit: zero their outputs here.
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    if ((compact ? s_len[b] : usable_len(ws, b)) > 0) continue;
+    wait_previous();
+    for (int i = tid; i < Hq * D; i += C::THREADS) {
+      const long long o = (long long)b * Hq * D + i;
+      if (a.flags & PKV_FLAG_OUT_F32) static_cast<float *>(ws.out)[o] = 0.f;
+      else static_cast<uint16_t *>(ws.out)[o] = 0;
+    }
+    if (a.flags & PKV_FLAG_WRITE_LSE)
+      for (int h = tid; h < Hq; h += C::THREADS) ws.lse[(long long)b * Hq + h] = -INFINITY;
   }
 
   uint8_t *const wring = smem + warp * (NS * C::STAGE);
   const uint32_t ring = smem_addr(wring);
-  float *obuf = reinterpret_cast<float *>(wring);
   const int SB = a.c.scale_block, per_page = ws.page_size / SB;
   const int sshift = (SB & (SB - 1)) == 0 ? __ffs(SB) - 1 : -1;
-  const long long layer_slot = (long long)a.layer * ws.pool_slots;
+  const int layer_slot = a.layer * ws.pool_slots;  // PAGED only: fits (checked by the host)
   // fragment offsets in a stage (rows + 8 are 8 D bytes on)
   const int tk = perm<D>(r);
   const int koff = swz<D>(tk, c);
@@ -209,183 +371,200 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   int st_in = 0, st_out = 0, ph_out = 0;  // ring positions: next to fill, next to read
   bool dead = false;                      // a wait of this warp ran out
 
-  bool waited = !early;
-  auto wait_previous = [&]() {
-    if (!waited) {
-      pdl_wait();
-      pdl_trigger();
-      waited = true;
+  int cu = 0;  // s_unit[cu]: the current unit, then (cu + 1) % 3 the next
+  auto after = [](int i) { return i == 2 ? 0 : i + 1; };
+  // pieces of a unit that are this warp's: every W-th from its own
+  auto count = [&](const KUnit &u) {
+    return dead ? 0 : (((u.t1 - u.t0 + 15) >> 4) - warp + W - 1) / W;
+  };
+  int np = count(s_unit[0]), nn = count(s_unit[1]);
+  // Positions count this warp's pieces from the start of the current unit and
+  // go on into the next unit.
+  int done_idx = 0, done_kv = 0;  // next index entries / rows to copy
+  int landed_idx = 0;             // index entries before this one have landed
+  int base_pos = 0;               // position 0, counted from the block's first
+
+  // PAGED: lane i holds the page of piece 32 m + i of the unit, pg_next the
+  // next 32, pg_unit the first 32 of the next unit.
+  auto load_pages = [&](const KUnit &u, int j0, int n) {
+    const int j = j0 + lane;
+    return PAGED && !(u.bad & PKV_DEVERR_PAGE) && j < n ? ws.page_table[u.base + pl.page_of(u.t0 + 16 * (warp + W * j))]
+                                    : -1;
+  };
+  int pg = load_pages(s_unit[0], 0, np), pg_next = load_pages(s_unit[0], 32, np);
+  int pg_unit = load_pages(s_unit[1], 0, nn);
+
+  // Else: the 16 index entries of position p into the index ring.
+  auto copy_idx = [&](int p) {
+    const bool in_next = p >= np;
+    const KUnit &u = s_unit[in_next ? after(cu) : cu];
+    if (lane < 16) {
+      const int tok = u.t0 + 16 * (warp + W * (in_next ? p - np : p)) + lane;
+      int *dst = &s_idx[warp][(base_pos + p) % (2 * NS)][lane];
+      if (tok < u.t1 && !(u.bad & PKV_DEVERR_PAGE)) {
+        const int *src = ws.index_mode == PKV_IDX_FLAT ? ws.kv_indices + u.base + tok
+                                                       : ws.page_table + u.base + pl.page_of(tok);
+        cp4(smem_addr(dst), src, 4);
+      } else {
+        *dst = -1;
+      }
     }
   };
-  if (pl.pref) {
-    // Requests with no usable token have no unit: zero their outputs here.
-    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-      if (s_pref[b + 1] != s_pref[b]) continue;
-      wait_previous();
-      for (int i = tid; i < Hq * D; i += C::THREADS) {
-        const long long o = (long long)b * Hq * D + i;
-        if (a.flags & PKV_FLAG_OUT_F32) static_cast<float *>(ws.out)[o] = 0.f;
-        else static_cast<uint16_t *>(ws.out)[o] = 0;
+  // The copies of position p into the next stage.  Rows past the unit's end may
+  // hold anything (TMA) or are zeros (cp.async).
+  const int tt = lane & 15;  // lanes 0-15: K scale of token tt, 16-31: V scale
+  auto copy_kv = [&](int p) {
+    const bool in_next = p >= np;
+    const int j = in_next ? p - np : p;
+    KUnit &u = s_unit[in_next ? after(cu) : cu];
+    const int tok0 = u.t0 + 16 * (warp + W * j);
+    const int g = u.g;
+    const float *sbase = (lane < 16 ? a.c.k_scale : a.c.v_scale) +
+                         ((long long)a.layer * pl.n_pages * H + g) * per_page;
+    const uint32_t dst = ring + st_in * C::STAGE;
+    const uint32_t sd = smem_addr(&s_scale[warp][st_in][lane]);
+    int bad = 0;
+    if constexpr (PAGED) {
+      uint64_t *bar = &s_bar[warp][st_in];
+      int page = __shfl_sync(0xffffffffu, in_next ? pg_unit : pg, j & 31);
+      if (page < 0 || page >= pl.n_pages) {
+        bad = PKV_DEVERR_PAGE;
+        page = 0;  // an in-range stand-in: the unit is written empty
       }
-      if (a.flags & PKV_FLAG_WRITE_LSE)
-        for (int h = tid; h < Hq; h += C::THREADS) ws.lse[(long long)b * Hq + h] = -INFINITY;
+      const int in0 = pl.in_page(tok0);
+      if (lane == 0) {
+        const int row = layer_slot + page * pl.P + in0;
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        tma_load_3d(dst, &tmk, 0, row, g, bar);
+        tma_load_3d(dst + C::KB, &tmv, 0, row, g, bar);
+      }
+      const int sub = sshift >= 0 ? (in0 + tt) >> sshift : (in0 + tt) / SB;
+      cp4(sd, sbase + ((long long)page * (H * per_page) + sub), 4);
+      if (!in_next && (j & 31) == 31) {
+        pg = pg_next;
+        pg_next = load_pages(u, j + 33, np);
+      }
+    } else {
+      constexpr int CH = D / 16, RPI = 32 / CH;  // chunks per row, rows per copy
+      const int nv = u.t1 - tok0;
+      const int *raw = s_idx[warp][(base_pos + p) % (2 * NS)];
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int row = i * RPI + lane / CH, ch = lane % CH;
+        int kind = 0;
+        const int s = row < nv ? (int)slot_from_raw(ws, pl, raw[row], tok0 + row, kind) : -1;
+        bad |= kind;
+        const long long off =
+            s >= 0 ? (((long long)a.layer * ws.pool_slots + s) * H + g) * (long long)D + ch * 16 : 0;
+        const uint32_t d = dst + swz<D>(row, ch);
+        cp16(d, static_cast<const uint8_t *>(a.c.k_pool) + off, s >= 0 ? 16 : 0);
+        cp16(d + C::KB, static_cast<const uint8_t *>(a.c.v_pool) + off, s >= 0 ? 16 : 0);
+      }
+      int kind = 0;
+      const int s = tt < nv ? (int)slot_from_raw(ws, pl, raw[tt], tok0 + tt, kind) : -1;
+      long long si = 0;
+      if (s >= 0) {
+        const int page = pl.P == 1 ? s : s / pl.P;
+        si = (long long)page * (H * per_page) + (pl.P == 1 ? 0 : (s - page * pl.P) / SB);
+      }
+      cp4(sd, sbase + si, s >= 0 ? 4 : 0);
+    }
+    if (bad) atomicOr(&u.bad, bad);
+  };
+  // Everything up to position p whose stage is free (p is at most NS past the
+  // last piece read): rows, and index entries NS further.
+  auto fill = [&](int p) {
+    if (dead) return;
+    const int most = min(p + 1, np + nn);
+    while (done_kv < most) {
+      if constexpr (!PAGED) {
+        // Entries NS ahead land before their turn: the wait for the rows of
+        // position p covers what was fetched with them.  The first pieces of
+        // a block, and those of a unit that follows very short ones, are
+        // known too late for that and wait here.
+        if (done_idx <= done_kv) {
+          const int to = min(done_kv + NS, np + nn);
+          for (; done_idx < to; ++done_idx) copy_idx(done_idx);
+        }
+        if (landed_idx <= done_kv) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+          landed_idx = done_idx;
+        }
+      }
+      copy_kv(done_kv);
+      if constexpr (!PAGED) {
+        const int to = min(done_kv + NS + 1, np + nn);
+        for (; done_idx < to; ++done_idx) copy_idx(done_idx);
+        if (lane == 0) s_seen[warp][st_in] = base_pos + done_idx;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");  // one group per position
+      st_in = st_in + 1 == NS ? 0 : st_in + 1;
+      ++done_kv;
+    }
+  };
+  if (PAGED && (a.flags & PKV_FLAG_TEST_SKIP_FIRST_TILE)) {
+    // test hook: the first stage is never armed, the wait for it runs out
+    if (np + nn > 0) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      st_in = 1;
+      done_kv = 1;
     }
   }
+  fill(NS - 2);  // the last stage follows in the unit's first step
 
-  UnitIter ui;
-  for (ui.first(ws, pl); !ui.done; ui.next(ws, pl)) {
-    const Unit un = ui.un;
-    const int hq0 = un.g * G;
-    if (un.t0 >= un.t1) {  // dense enumeration only: past the request's end
-      if (un.c == 0) {
-        wait_previous();
-        for (int i = tid; i < G * D; i += C::THREADS) {
-          const long long o = ((long long)un.b * Hq + hq0) * D + i;
-          if (a.flags & PKV_FLAG_OUT_F32) static_cast<float *>(ws.out)[o] = 0.f;
-          else static_cast<uint16_t *>(ws.out)[o] = 0;
-        }
-        if ((a.flags & PKV_FLAG_WRITE_LSE) && tid < G)
-          ws.lse[(long long)un.b * Hq + hq0 + tid] = -INFINITY;
-      }
-      continue;
-    }
-    const int pieces = (un.t1 - un.t0 + 15) / 16;
-    const int np = dead ? 0 : (pieces - warp + W - 1) / W;  // this warp's
-    const ReqIndex ri = pl.pref ? req_index_cached(ws, s_base, un.b) : req_index(ws, un.b);
-    int bad = (ri.ok ? 0 : PKV_DEVERR_PAGE) | (dead ? PKV_DEVERR_TIMEOUT : 0);
-    auto piece_tok = [&](int j) { return un.t0 + 16 * (warp + W * j); };
-
-    // Index entries.  PAGED: lane i holds the page of piece 32 m + i, the next
-    // 32 follow in pg_next.  Else the 16 entries of a piece are copied, one
-    // group ahead of its rows, into a ring of 2 NS pieces.
-    int pg = -1, pg_next = -1;
-    auto load_pages = [&](int j0) {
-      const int j = j0 + lane;
-      return PAGED && ri.ok && j < np ? *index_src(ws, pl, ri, piece_tok(j)) : -1;
-    };
-    auto fetch_idx = [&](int j) {
-      if constexpr (!PAGED) {
-        if (j < np && lane < 16) {
-          const int tok = piece_tok(j) + lane;
-          int *dst = &s_idx[warp][j % (2 * NS)][lane];
-          if (ri.ok && tok < un.t1) cp4(smem_addr(dst), index_src(ws, pl, ri, tok), 4);
-          else *dst = -1;
-        }
-      }
-    };
-    // The copies of piece j into the next stage; their small ones (scales and
-    // index entries) are a commit group each piece.  Rows past the unit's end
-    // may hold anything (TMA) or are zeros (cp.async).
-    const long long srow = ((long long)a.layer * pl.n_pages * H + un.g) * per_page;
-    const float *sbase = (lane < 16 ? a.c.k_scale : a.c.v_scale) + srow;
-    const int tt = lane & 15;  // lanes 0-15: K scale of token tt, 16-31: V scale
-    auto issue = [&](int j) {
-      const int tok0 = piece_tok(j);
-      const uint32_t dst = ring + st_in * C::STAGE;
-      const uint32_t sd = smem_addr(&s_scale[warp][st_in][lane]);
-      if constexpr (PAGED) {
-        int page = __shfl_sync(0xffffffffu, pg, j & 31);
-        if (page < 0 || page >= pl.n_pages) {
-          bad |= PKV_DEVERR_PAGE;
-          page = 0;  // an in-range stand-in: the unit is written empty
-        }
-        const int in0 = pl.in_page(tok0);
-        if (lane == 0) {
-          uint64_t *bar = &s_bar[warp][st_in];
-          const int row = (int)layer_slot + page * pl.P + in0;
-          mbar_arrive_expect_tx(bar, C::STAGE);
-          tma_load_3d(dst, &tmk, 0, row, un.g, bar);
-          tma_load_3d(dst + C::KB, &tmv, 0, row, un.g, bar);
-        }
-        const int sub = sshift >= 0 ? (in0 + tt) >> sshift : (in0 + tt) / SB;
-        cp4(sd, sbase + ((long long)page * (H * per_page) + sub), 4);
-        if ((j & 31) == 31) {
-          pg = pg_next;
-          pg_next = load_pages(j + 33);
-        }
-      } else {
-        constexpr int CH = D / 16, RPI = 32 / CH;  // chunks per row, rows per copy
-        const int nv = un.t1 - tok0;
-        const int *raw = s_idx[warp][j % (2 * NS)];
+  // Q^T as the B operand: lane r is head r (+ 8), its 16 elements 64 x + 16 c ..
+  // 64 x + 16 c + 15 of each half x match the K bytes the lane reads.
+  uint4 qraw[NH][D / 32];
+  auto load_q = [&](const KUnit &u) {
 #pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
-          const int row = i * RPI + lane / CH, ch = lane % CH;
-          int kind = 0;
-          const int s = row < nv ? (int)slot_from_raw(ws, pl, raw[row], tok0 + row, kind) : -1;
-          bad |= kind;
-          const long long off =
-              s >= 0 ? ((layer_slot + s) * H + un.g) * (long long)D + ch * 16 : 0;
-          const uint32_t d = dst + swz<D>(row, ch);
-          cp16(d, static_cast<const uint8_t *>(a.c.k_pool) + off, s >= 0 ? 16 : 0);
-          cp16(d + C::KB, static_cast<const uint8_t *>(a.c.v_pool) + off, s >= 0 ? 16 : 0);
-        }
-        int kind = 0;
-        const int s = tt < nv ? (int)slot_from_raw(ws, pl, raw[tt], tok0 + tt, kind) : -1;
-        long long si = 0;
-        if (s >= 0) {
-          const int page = pl.P == 1 ? s : s / pl.P;
-          si = (long long)page * (H * per_page) + (pl.P == 1 ? 0 : (s - page * pl.P) / SB);
-        }
-        cp4(sd, sbase + si, s >= 0 ? 4 : 0);
-      }
-      st_in = st_in + 1 == NS ? 0 : st_in + 1;
-    };
+    for (int n = 0; n < NH; ++n) {
+      const int h = r + 8 * n;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        qraw[n][i] = h < G ? reinterpret_cast<const uint4 *>(
+                                 a.q)[((long long)u.b * Hq + u.g * G + h) * (D / 8) +
+                                      8 * (i >> 1) + 2 * c + (i & 1)]
+                           : make_uint4(0, 0, 0, 0);
+    }
+  };
+  wait_previous();  // q comes from the previous kernel
+  if (s_unit[0].t0 < s_unit[0].t1) load_q(s_unit[0]);
 
-    // Q^T as the B operand: lane r is head r (+ 8), its 16 elements 64 x + 16 c
-    // .. 64 x + 16 c + 15 of each half x match the K bytes the lane reads.
+  int n_part = 0;  // tickets taken and not looked at
+  while (s_unit[cu].t0 < s_unit[cu].t1) {  // the same in every thread
+    const int nv0 = s_unit[cu].t1 - s_unit[cu].t0 - 16 * warp;  // tokens from piece 0 on
     uint32_t qb[NH][D / 16][2];
     float qs[NH][2];  // scale of heads 2 c and 2 c + 1, log2 units
-    auto load_q = [&]() {
 #pragma unroll
-      for (int n = 0; n < NH; ++n) {
-        const int h = r + 8 * n;
-        uint4 raw[D / 32];
+    for (int n = 0; n < NH; ++n) {
+      float m = 0.f;
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x)
+      for (int i = 0; i < D / 32; ++i) {
+        float f[8];
+        unpack8(qraw[n][i], f);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            raw[2 * x + i] =
-                h < G ? reinterpret_cast<const uint4 *>(a.q)[((long long)un.b * Hq + hq0 + h) *
-                                                                 (D / 8) + 8 * x + 2 * c + i]
-                      : make_uint4(0, 0, 0, 0);
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          float f[8];
-          unpack8(raw[i], f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        // 2^k brings m into [2^14, 2^15) (k <= 126: a smaller row keeps all it has)
-        const int k = m > 0.f ? min(126, 141 - (__float_as_int(m) >> 23)) : 0;
-        const float up = pow2i(k);
-        const float down = a.scale * kLog2e * pow2i(-k);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          float f[8];
-          unpack8(raw[i], f);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            qb[n][2 * i + e][0] = pack_f16x2(f[4 * e] * up, f[4 * e + 1] * up);
-            qb[n][2 * i + e][1] = pack_f16x2(f[4 * e + 2] * up, f[4 * e + 3] * up);
-          }
-        }
-        qs[n][0] = __shfl_sync(0xffffffffu, down, 8 * c);
-        qs[n][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
       }
-    };
-
-    if constexpr (PAGED) {
-      pg = load_pages(0);
-      pg_next = load_pages(32);
-    } else {
-      for (int j = 0; j < NS; ++j) fetch_idx(j);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncwarp();
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      // 2^k brings m into [2^14, 2^15) (k <= 126: a smaller row keeps all it has)
+      const int k = m > 0.f ? min(126, 141 - (__float_as_int(m) >> 23)) : 0;
+      const float up = pow2i(k);
+      const float down = a.scale * kLog2e * pow2i(-k);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        float f[8];
+        unpack8(qraw[n][i], f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          qb[n][2 * i + e][0] = pack_f16x2(f[4 * e] * up, f[4 * e + 1] * up);
+          qb[n][2 * i + e][1] = pack_f16x2(f[4 * e + 2] * up, f[4 * e + 3] * up);
+        }
+      }
+      qs[n][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+      qs[n][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
     }
-
     // acc[n][j] = O of heads 8 n + 2 c + {0, 1} at dims VB r + 2 j (elements 0, 1)
     // and VB r + 2 j + 1 (elements 2, 3)
     float acc[NH][D / 16][4];
@@ -398,33 +577,35 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       l_run[n][0] = l_run[n][1] = 0.f;
     }
 
-    // Iteration j: consume piece j (from 0 on), then fill its stage with piece
-    // j + NS; the NS iterations before the first only fill.
+    // Step j reads piece j and refills the ring behind it; step -1 only fills.
+    // After the last piece its stage stays free: it takes the warp's O.
 #pragma unroll 1
-    for (int j = -NS; j < np; ++j) {
+    for (int j = -1; j < np; ++j) {
       if (j >= 0) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
-        if constexpr (PAGED) {
-          const bool ok = mbar_wait_bounded(&s_bar[warp][st_out], ph_out);
-          if (__any_sync(0xffffffffu, !ok)) {
-            // The copies still in flight (bounded too) end before anything
-            // else uses their stages; the warp copies nothing from here on.
-            for (int i = j; i < min(j + NS, np); ++i) {
-              mbar_wait_bounded(&s_bar[warp][st_out], ph_out);
-              if (++st_out == NS) {
-                st_out = 0;
-                ph_out ^= 1;
-              }
+        // this position's group: the groups of the newer positions may pend
+        const int newer = done_kv - 1 - j;
+        if (newer >= NS - 1) asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+        else if (newer == NS - 2) asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+        else if (newer >= 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (PAGED && __any_sync(0xffffffffu, !mbar_wait_bounded(&s_bar[warp][st_out], ph_out))) {
+          // The copies still in flight (bounded too) end before anything else
+          // uses their stages; the warp copies nothing from here on.
+          for (int i = j; i < done_kv; ++i) {
+            mbar_wait_bounded(&s_bar[warp][st_out], ph_out);
+            if (++st_out == NS) {
+              st_out = 0;
+              ph_out ^= 1;
             }
-            dead = true;
-            bad |= PKV_DEVERR_TIMEOUT;
-            break;
           }
+          dead = true;
+          break;
         }
         __syncwarp();  // the other lanes' copies too
+        if constexpr (!PAGED) landed_idx = max(landed_idx, s_seen[warp][st_out] - base_pos);
         const uint8_t *stage = wring + st_out * C::STAGE;
         const float *ss = s_scale[warp][st_out];
-        const int nv = un.t1 - piece_tok(j);
+        const int nv = nv0 - 16 * W * j;
         // ---- S^T = K Q^T, in two chains ----
         float sc[NH][4], sc2[NH][4];
 #pragma unroll
@@ -545,27 +726,17 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
           ph_out ^= 1;
         }
         __syncwarp();  // every lane is done with the stage
+        if (j == np - 1) break;
       }
-      if (j + NS < np) {
-        if (PAGED && j == -NS && (a.flags & PKV_FLAG_TEST_SKIP_FIRST_TILE)) {
-          // test hook: the stage is never armed, its wait runs out
-          st_in = st_in + 1 == NS ? 0 : st_in + 1;
-        } else {
-          issue(j + NS);
-        }
-      }
-      fetch_idx(j + 2 * NS);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (j == -1) {
-        wait_previous();  // q comes from the previous kernel
-        load_q();
-      }
+      fill(j + NS);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    bad = __reduce_or_sync(0xffffffffu, (unsigned)bad);
-    if (bad && lane == 0) atomicOr(ws.err, bad);
 
     // ---- the warps' states meet ----
+    const int at = np > 0 && !dead ? (st_out == 0 ? NS - 1 : st_out - 1) : -1;
+    if (lane == 0) {
+      s_slot[warp] = at;
+      s_bad[warp] = dead ? PKV_DEVERR_TIMEOUT : 0;
+    }
 #pragma unroll
     for (int n = 0; n < NH; ++n)
 #pragma unroll
@@ -574,106 +745,133 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (r == 0) {
-          s_ml[warp][8 * n + 2 * c + e][0] = m_run[n][e];
-          s_ml[warp][8 * n + 2 * c + e][1] = l;
-        }
+        if (r == 0) s_ml[warp][8 * n + 2 * c + e] = make_float2(m_run[n][e], l);
       }
-    if (lane == 0) s_bad[warp] = bad;
-    __syncthreads();
+    const bool has_next = s_unit[after(cu)].t0 < s_unit[after(cu)].t1;
+    if (has_next) load_q(s_unit[after(cu)]);  // on its way while the block meets
+    const int split = s_unit[cu].c;
+    const bool final_out = s_unit[cu].n == 1;
+    const long long q0 = (long long)s_unit[cu].b * Hq + s_unit[cu].g * G;
 #pragma unroll
-    for (int n = 0; n < NH; ++n)
+    for (int n = 0; n < NH; ++n) {
+      // 8 heads x D floats in the free stage; word d of row h sits at d ^ its
+      // lanes' (r, c) bits, so the 8-byte stores of half a warp take every bank
+      if (at >= 0) {
+        float *o = reinterpret_cast<float *>(wring + at * C::STAGE);
+        const int x = D == 128 ? (((r >> 1) & 1) << 1) | (c << 2) : c << 1;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = 8 * n + 2 * c + e;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, s_ml[w][h][0]);
-        float L = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const float mw = s_ml[w][h][0], lw = s_ml[w][h][1];
-          // a warp without pieces has nothing; one whose scores are all NaN
-          // never moved its reference and passes its NaN on
-          L += mw == -INFINITY ? (lw == 0.f ? 0.f : lw) : fast_exp2(mw - M) * lw;
-        }
-        if (warp == 0 && r == 0 && h < G) {
-          s_hml[h][0] = M;
-          s_hml[h][1] = L;
-        }
-        const float f = m_run[n][e] == -INFINITY ? 1.f : fast_exp2(m_run[n][e] - M);
-        if (h < G) {
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
-            *reinterpret_cast<float2 *>(obuf + h * C::RS + C::VB * r + 2 * i) =
-                make_float2(acc[n][i][e] * f, acc[n][i][2 + e] * f);
-        }
+            *reinterpret_cast<float2 *>(o + (2 * c + e) * D + ((C::VB * r + 2 * i) ^ x)) =
+                make_float2(acc[n][i][e], acc[n][i][2 + e]);
       }
-    int unit_bad = 0;
+      __syncthreads();
+      int unit_bad = s_unit[cu].bad;
 #pragma unroll
-    for (int w = 0; w < W; ++w) unit_bad |= s_bad[w];
-    __syncthreads();
-
-    // ---- write: final row, or a partial (and maybe merge them all) ----
-    const bool final_out = direct || un.n == 1;
-    for (int i = tid * 4; i < G * D; i += C::THREADS * 4) {
-      const int h = i / D, d = i - h * D;
-      const float L = s_hml[h][1];
-      const float inv = 1.f / L;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!unit_bad) {
+      for (int w = 0; w < W; ++w) unit_bad |= s_bad[w];
+      if (n == 0 && tid == C::THREADS - 1) {
+        if (unit_bad) atomicOr(ws.err, unit_bad);
+      }
+      for (int i = tid * 4; i < min(8, G - 8 * n) * D; i += C::THREADS * 4) {
+        const int h8 = i / D, h = h8 + 8 * n, d = i - h8 * D;
+        float M = -INFINITY, L = 0.f;
+        float2 ml[W];
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float4 y = *reinterpret_cast<const float4 *>(
-              smem + w * (NS * C::STAGE) + (h * C::RS + d) * 4);
-          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          ml[w] = s_ml[w][h];
+          M = fmaxf(M, ml[w].x);
         }
-        x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int sx = D == 128 ? (((d >> 5) & 1) << 1) | ((h8 >> 1) << 2) : (h8 >> 1) << 1;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int slot = s_slot[w];
+          if (slot < 0) continue;
+          // a warp whose scores are all NaN never placed its reference: it
+          // passes its NaN on
+          const float f = ml[w].x == -INFINITY ? 1.f : fast_exp2(ml[w].x - M);
+          L += f * ml[w].y;
+          const float4 y = *reinterpret_cast<const float4 *>(
+              smem + (w * NS + slot) * C::STAGE + (h8 * D + (d ^ (sx & ~3))) * 4);
+          const bool sw = sx & 2;
+          x.x = fmaf(f, sw ? y.z : y.x, x.x);
+          x.y = fmaf(f, sw ? y.w : y.y, x.y);
+          x.z = fmaf(f, sw ? y.x : y.z, x.z);
+          x.w = fmaf(f, sw ? y.y : y.w, x.w);
+        }
+        const float inv = 1.f / L;
+        x = unit_bad ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        const long long qrow = q0 + h;
+        if (!final_out) {
+          *reinterpret_cast<float4 *>(ws.o_part + (qrow * a.num_splits + split) * D + d) = x;
+        } else if (a.flags & PKV_FLAG_OUT_F32) {
+          *reinterpret_cast<float4 *>(static_cast<float *>(ws.out) + qrow * D + d) = x;
+        } else {
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(ws.out) + qrow * D + d) =
+              make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+        }
+        if (d == 0) {
+          const float lse = unit_bad ? -INFINITY : M * kLn2 + logf(L);
+          if (!final_out)
+            *reinterpret_cast<float2 *>(ws.ml_part + (qrow * a.num_splits + split) * 2) =
+                make_float2(lse, unit_bad ? 0.f : 1.f);
+          else if (a.flags & PKV_FLAG_WRITE_LSE)
+            ws.lse[qrow] = lse;
+        }
       }
-      const long long qrow = (long long)un.b * Hq + hq0 + h;
-      if (!final_out) {
-        *reinterpret_cast<float4 *>(ws.o_part + (qrow * pl.S + un.c) * D + d) = x;
-      } else if (a.flags & PKV_FLAG_OUT_F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(ws.out) + qrow * D + d) = x;
-      } else {
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(ws.out) + qrow * D + d) =
-            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-      }
+      // the unit after the next one, in the place of the one before this
+      if (n == 0 && tid == 0) next_unit(&s_unit[after(after(cu))]);
+      // the stages go back to copies of the async proxy
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();
     }
-    if (tid < G) {
-      const float lse = unit_bad ? -INFINITY : s_hml[tid][0] * kLn2 + logf(s_hml[tid][1]);
-      const long long qrow = (long long)un.b * Hq + hq0 + tid;
-      if (final_out) {
-        if (a.flags & PKV_FLAG_WRITE_LSE) ws.lse[qrow] = lse;
-      } else {
-        const long long o = (qrow * pl.S + un.c) * 2;
-        ws.ml_part[o] = lse;
-        ws.ml_part[o + 1] = unit_bad ? 0.f : 1.f;
-      }
-    }
+    // Ticket: the block that completes a pair's partials merges them, after
+    // its last unit.  The barrier above orders the block's partial before the
+    // ticket; the last taker acquires every other block's.
     if (!final_out) {
-      __syncthreads();
       if (tid == 0) {
-        // the block's partial (ordered by the barrier) is released with the
-        // ticket; the last taker acquires every other block's
-        int *ctr = ws.split_counters + (long long)un.b * H + un.g;
-        const int last = atomic_add_acq_rel_gpu(ctr, 1) == un.n - 1;
+        const KUnit &u = s_unit[cu];
+        int *ctr = ws.split_counters + (long long)u.b * H + u.g;
+        const int last = atomic_add_acq_rel_gpu(ctr, 1) == u.n - 1;
         if (last) *ctr = 0;  // ready for the next launch
-        s_last = last;
+        s_merge[n_part][0] = last ? u.n : 0;
+        s_merge[n_part][1] = u.b;
+        s_merge[n_part][2] = u.g;
       }
-      __syncthreads();
-      if (s_last && warp < G) {
-        constexpr int RPW = G >= W ? G / W : 1;
-        merge_rows_batched<D, RPW>(ws, (long long)un.b * Hq + hq0 + warp, W, pl.S, un.n, a.flags,
-                                   lane);
-      }
+      ++n_part;
     }
-    // the rings, s_ml and the ticket serve the next unit, the rings by copies of
-    // the async proxy
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
+
+    // ---- on to the next unit ----
+    done_idx -= np;
+    done_kv -= np;
+    landed_idx -= np;
+    base_pos += np;
+    cu = after(cu);
+    np = dead ? 0 : nn;
+    pg = pg_unit;
+    pg_next = load_pages(s_unit[cu], 32, np);
+    nn = count(s_unit[after(cu)]);
+    pg_unit = load_pages(s_unit[after(cu)], 0, nn);
+
+    // A run has at most two partials (its first and its last unit); blocks of
+    // fixed chunks (larger batches) merge as they go.
+    if (n_part == 2 || (n_part > 0 && !has_next)) {
+      __syncthreads();
+#pragma unroll 1
+      for (int i = 0; i < n_part; ++i) {
+        const int n = s_merge[i][0];
+        if (n > 0 && warp < G) {
+          constexpr int RPW = G >= W ? G / W : 1;
+          merge_rows_batched<D, RPW>(ws, (long long)s_merge[i][1] * Hq + s_merge[i][2] * G + warp, W,
+                                     a.num_splits, n, a.flags, lane);
+        }
+      }
+      __syncthreads();  // s_merge
+      n_part = 0;
+    }
   }
-  wait_previous();
 }
 
 using TmapEncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -732,9 +930,10 @@ cudaError_t launch_one(Kv8Args a, const CUtensorMap &tmk, const CUtensorMap &tmv
   const long long units = (long long)a.num_splits * a.batch * ws.n_kv_heads;
   const long long cap = (long long)sms_cache[di] * occ_cache[di];
   const int grid = (int)(units < cap ? units : cap);
-  // splits shared out by length need the compact plan and a sum that fits an int
-  a.apportion = a.num_splits > 1 && a.batch <= kMaxCompactBatch &&
-                (long long)a.batch * ws.max_pages_per_req * ws.page_size < 0x7fffffffll;
+  // sharing out by length needs the compact plan, a block per head and a line
+  // whose length fits an int
+  a.apportion = a.num_splits > 1 && a.batch <= kMaxCompactBatch && grid >= ws.n_kv_heads &&
+                (long long)a.batch * (len_cap(ws) / 16 + 1 + kUnitCost) < 0x7fffffffll;
   return launch_pdl(kern, dim3(grid), dim3(C::THREADS), (size_t)C::SMEM, st, a, tmk, tmv);
 }
 
