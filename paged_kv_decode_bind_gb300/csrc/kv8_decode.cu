@@ -82,7 +82,7 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void *src, int bytes) {
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -140,6 +140,7 @@ struct KUnit {
   int b, g, c, n, t0, t1;
   int bad;         // error bits
   long long base;  // where the request's index entries start
+  long long srow;  // scale index of (layer, page 0, head g)
 };
 
 // A block's units in order.
@@ -170,8 +171,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
                       const __grid_constant__ CUtensorMap tmv) {
   using C = KCfg<D, G>;
   constexpr int W = C::W, NS = C::NS, NH = C::NH;
-  // log2 of the largest weight where r is placed, and where it has to move
-  constexpr float kPlace = 7.f, kMove = 15.f;
+  // log2 of the largest weight where r is placed, and the weight at which it moves
+  constexpr float kPlace = 7.f, kMove = 32768.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[PAGED ? W : 1][NS];
   __shared__ int s_pref[kMaxCompactBatch + 1];
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     KUnits us = s_us;
     KUnit u;
     u.b = u.g = u.c = u.n = u.t0 = u.t1 = u.bad = 0;
-    u.base = 0;
+    u.base = u.srow = 0;
     while (us.pos < us.end) {
       ReqIndex ri;
       if (a.apportion) {
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       }
       u.base = ri.base;
       u.bad = ri.ok ? 0 : PKV_DEVERR_PAGE;
+      u.srow = ((long long)a.layer * pl.n_pages * H + u.g) * (ws.page_size / a.c.scale_block);
       s_us = us;
       *dst = u;
       return;
@@ -413,14 +415,15 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   // The copies of position p into the next stage.  Rows past the unit's end may
   // hold anything (TMA) or are zeros (cp.async).
   const int tt = lane & 15;  // lanes 0-15: K scale of token tt, 16-31: V scale
+  const float *const scales = lane < 16 ? a.c.k_scale : a.c.v_scale;
+  const int page_row = H * per_page;  // scales of a page
   auto copy_kv = [&](int p) {
     const bool in_next = p >= np;
     const int j = in_next ? p - np : p;
     KUnit &u = s_unit[in_next ? after(cu) : cu];
     const int tok0 = u.t0 + 16 * (warp + W * j);
     const int g = u.g;
-    const float *sbase = (lane < 16 ? a.c.k_scale : a.c.v_scale) +
-                         ((long long)a.layer * pl.n_pages * H + g) * per_page;
+    const float *sbase = scales + u.srow;
     const uint32_t dst = ring + st_in * C::STAGE;
     const uint32_t sd = smem_addr(&s_scale[warp][st_in][lane]);
     int bad = 0;
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
         tma_load_3d(dst + C::KB, &tmv, 0, row, g, bar);
       }
       const int sub = sshift >= 0 ? (in0 + tt) >> sshift : (in0 + tt) / SB;
-      cp4(sd, sbase + ((long long)page * (H * per_page) + sub), 4);
+      cp4(sd, sbase + ((long long)page * page_row + sub), 4);
       if (!in_next && (j & 31) == 31) {
         pg = pg_next;
         pg_next = load_pages(u, j + 33, np);
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       long long si = 0;
       if (s >= 0) {
         const int page = pl.P == 1 ? s : s / pl.P;
-        si = (long long)page * (H * per_page) + (pl.P == 1 ? 0 : (s - page * pl.P) / SB);
+        si = (long long)page * page_row + (pl.P == 1 ? 0 : (s - page * pl.P) / SB);
       }
       cp4(sd, sbase + si, s >= 0 ? 4 : 0);
     }
@@ -585,8 +588,6 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
         // this position's group: the groups of the newer positions may pend
         const int newer = done_kv - 1 - j;
         if (newer >= NS - 1) asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
-        else if (newer == NS - 2) asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
-        else if (newer >= 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
         else asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (PAGED && __any_sync(0xffffffffu, !mbar_wait_bounded(&s_bar[warp][st_out], ph_out))) {
           // The copies still in flight (bounded too) end before anything else
@@ -631,28 +632,33 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
         // ---- weights: tokens tk and tk + 8, heads 2 c and 2 c + 1 ----
         const float ks[2] = {ss[tk], ss[tk + 8]};
         float vs[2] = {ss[16 + tk], ss[24 + tk]};
-        if (nv < 16) {  // rows past the end: any scale, no weight
-          if (tk >= nv) vs[0] = 1.f;
-          if (tk + 8 >= nv) vs[1] = 1.f;
-        }
-        const float lv[2] = {fast_log2(vs[0]), fast_log2(vs[1])};
-        bool move = false;
 #pragma unroll
         for (int n = 0; n < NH; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[n][i] = (sc[n][i] + sc2[n][i]) * ks[i >> 1] * qs[n][i & 1];
-        if (nv < 16) {
+          for (int i = 0; i < 4; ++i) sc[n][i] = (sc[n][i] + sc2[n][i]) * (ks[i >> 1] * qs[n][i & 1]);
+        if (nv < 16) {  // rows past the end: any score and scale, no weight
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (tk + 8 * t >= nv) {
+              vs[t] = 1.f;
+#pragma unroll
+              for (int n = 0; n < NH; ++n) sc[n][2 * t] = sc[n][2 * t + 1] = -INFINITY;
+            }
+        }
+        float p[NH][4];  // exp(x - r); element 2 t + e
+        auto weigh = [&]() {
+          bool big = false;
 #pragma unroll
           for (int n = 0; n < NH; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (tk + 8 * (i >> 1) >= nv) sc[n][i] = -INFINITY;
-        }
-#pragma unroll
-        for (int n = 0; n < NH; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) move |= sc[n][i] + lv[i >> 1] > m_run[n][i & 1] + kMove;
-        if (__any_sync(0xffffffffu, move)) {
+            for (int i = 0; i < 4; ++i) {
+              p[n][i] = fast_exp2(sc[n][i] - m_run[n][i & 1]);
+              big |= p[n][i] * vs[i >> 1] > kMove;
+            }
+          return big;
+        };
+        if (__any_sync(0xffffffffu, weigh())) {
+          const float lv[2] = {fast_log2(vs[0]), fast_log2(vs[1])};
 #pragma unroll
           for (int n = 0; n < NH; ++n) {
             float al[2];
@@ -675,17 +681,16 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
               acc[n][i][3] *= al[1];
             }
           }
+          weigh();
         }
         uint32_t wb[NH][2];  // W^T as B: tokens of rows 0-7 / 8-15
 #pragma unroll
         for (int n = 0; n < NH; ++n)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const float p0 = fast_exp2(sc[n][2 * t] - m_run[n][0]);
-            const float p1 = fast_exp2(sc[n][2 * t + 1] - m_run[n][1]);
-            l_run[n][0] += p0;
-            l_run[n][1] += p1;
-            wb[n][t] = movmatrix_t(pack_f16x2(p0 * vs[t], p1 * vs[t]));
+            l_run[n][0] += p[n][2 * t];
+            l_run[n][1] += p[n][2 * t + 1];
+            wb[n][t] = movmatrix_t(pack_f16x2(p[n][2 * t] * vs[t], p[n][2 * t + 1] * vs[t]));
           }
         // ---- O^T += V^T W^T ----
         uint32_t v[4][C::VB / 4];
