@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   __shared__ int s_pref[kMaxCompactBatch + 1];
   __shared__ int s_len[kMaxCompactBatch];
   __shared__ int s_base[kMaxCompactBatch];
-  __shared__ float s_scale[W][NS][32];  // K scales of a piece's tokens, then V scales
+  // scales of tokens t and t + 8 of a piece: (K, K, V, V) at [4 t]
+  __shared__ __align__(16) float s_scale[W][NS][32];
   __shared__ int s_idx[PAGED ? 1 : W][PAGED ? 1 : 2 * NS][16];
   __shared__ float2 s_ml[W][16];
   __shared__ int s_slot[W];  // ring slot holding a warp's O, -1: it had no piece
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   const uint32_t ring = smem_addr(wring);
   const int SB = a.c.scale_block, per_page = ws.page_size / SB;
   const int sshift = (SB & (SB - 1)) == 0 ? __ffs(SB) - 1 : -1;
+  const int page_row = H * per_page;  // scales of a page
   const int layer_slot = a.layer * ws.pool_slots;  // PAGED only: fits (checked by the host)
   // fragment offsets in a stage (rows + 8 are 8 D bytes on)
   const int tk = perm<D>(r);
@@ -386,15 +388,28 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   int landed_idx = 0;             // index entries before this one have landed
   int base_pos = 0;               // position 0, counted from the block's first
 
-  // PAGED: lane i holds the page of piece 32 m + i of the unit, pg_next the
-  // next 32, pg_unit the first 32 of the next unit.
+  // PAGED: lane i holds, for piece 32 m + i of the unit, its page id and, from
+  // the first of those pieces on, the row of its TMA box instead, and its offset
+  // among the head's scales; *_unit the same for the first 32 of the next unit.
   auto load_pages = [&](const KUnit &u, int j0, int n) {
     const int j = j0 + lane;
-    return PAGED && !(u.bad & PKV_DEVERR_PAGE) && j < n ? ws.page_table[u.base + pl.page_of(u.t0 + 16 * (warp + W * j))]
-                                    : -1;
+    return PAGED && j < n && !(u.bad & PKV_DEVERR_PAGE)
+               ? ws.page_table[u.base + pl.page_of(u.t0 + 16 * (warp + W * j))]
+               : -1;
   };
-  int pg = load_pages(s_unit[0], 0, np), pg_next = load_pages(s_unit[0], 32, np);
-  int pg_unit = load_pages(s_unit[1], 0, nn);
+  // A bad page id becomes page 0, an in-range stand-in: the unit is written empty.
+  auto to_row = [&](KUnit &u, int j0, int n, int &row, unsigned &off) {
+    const int j = j0 + lane, in0 = pl.in_page(u.t0 + 16 * (warp + W * j));
+    int page = row;
+    if (page < 0 || page >= pl.n_pages) {
+      if (j < n) atomicOr(&u.bad, PKV_DEVERR_PAGE);
+      page = 0;
+    }
+    row = layer_slot + page * pl.P + in0;
+    off = (unsigned)page * page_row + (sshift >= 0 ? in0 >> sshift : in0 / SB);
+  };
+  int row = load_pages(s_unit[0], 0, np), row_unit = load_pages(s_unit[1], 0, nn);
+  unsigned off = 0, off_unit = 0;
 
   // Else: the 16 index entries of position p into the index ring.
   auto copy_idx = [&](int p) {
@@ -416,40 +431,36 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   // hold anything (TMA) or are zeros (cp.async).
   const int tt = lane & 15;  // lanes 0-15: K scale of token tt, 16-31: V scale
   const float *const scales = lane < 16 ? a.c.k_scale : a.c.v_scale;
-  const int page_row = H * per_page;  // scales of a page
+  // block of token tt after the piece's first (PAGED: a piece is whole blocks,
+  // or inside one)
+  const unsigned tok_block = tt / SB;
   auto copy_kv = [&](int p) {
     const bool in_next = p >= np;
     const int j = in_next ? p - np : p;
     KUnit &u = s_unit[in_next ? after(cu) : cu];
-    const int tok0 = u.t0 + 16 * (warp + W * j);
     const int g = u.g;
     const float *sbase = scales + u.srow;
     const uint32_t dst = ring + st_in * C::STAGE;
-    const uint32_t sd = smem_addr(&s_scale[warp][st_in][lane]);
+    const uint32_t sd = smem_addr(&s_scale[warp][st_in][4 * (tt & 7) + 2 * (lane >> 4) + (tt >> 3)]);
     int bad = 0;
     if constexpr (PAGED) {
-      uint64_t *bar = &s_bar[warp][st_in];
-      int page = __shfl_sync(0xffffffffu, in_next ? pg_unit : pg, j & 31);
-      if (page < 0 || page >= pl.n_pages) {
-        bad = PKV_DEVERR_PAGE;
-        page = 0;  // an in-range stand-in: the unit is written empty
+      if ((j & 31) == 0) {
+        if (in_next) to_row(u, j, nn, row_unit, off_unit);
+        else to_row(u, j, np, row, off);
       }
-      const int in0 = pl.in_page(tok0);
+      const int at = __shfl_sync(0xffffffffu, in_next ? row_unit : row, j & 31);
+      const unsigned so = __shfl_sync(0xffffffffu, in_next ? off_unit : off, j & 31);
       if (lane == 0) {
-        const int row = layer_slot + page * pl.P + in0;
+        uint64_t *bar = &s_bar[warp][st_in];
         mbar_arrive_expect_tx(bar, C::STAGE);
-        tma_load_3d(dst, &tmk, 0, row, g, bar);
-        tma_load_3d(dst + C::KB, &tmv, 0, row, g, bar);
+        tma_load_3d(dst, &tmk, 0, at, g, bar);
+        tma_load_3d(dst + C::KB, &tmv, 0, at, g, bar);
       }
-      const int sub = sshift >= 0 ? (in0 + tt) >> sshift : (in0 + tt) / SB;
-      cp4(sd, sbase + ((long long)page * page_row + sub), 4);
-      if (!in_next && (j & 31) == 31) {
-        pg = pg_next;
-        pg_next = load_pages(u, j + 33, np);
-      }
+      cp4(sd, sbase + (so + tok_block), 4);
+      if (!in_next && (j & 31) == 31) row = load_pages(u, j + 1, np);
     } else {
       constexpr int CH = D / 16, RPI = 32 / CH;  // chunks per row, rows per copy
-      const int nv = u.t1 - tok0;
+      const int tok0 = u.t0 + 16 * (warp + W * j), nv = u.t1 - tok0;
       const int *raw = s_idx[warp][(base_pos + p) % (2 * NS)];
 #pragma unroll
       for (int i = 0; i < 16 / RPI; ++i) {
@@ -630,8 +641,9 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
           }
         }
         // ---- weights: tokens tk and tk + 8, heads 2 c and 2 c + 1 ----
-        const float ks[2] = {ss[tk], ss[tk + 8]};
-        float vs[2] = {ss[16 + tk], ss[24 + tk]};
+        const float4 scl = *reinterpret_cast<const float4 *>(ss + 4 * tk);
+        const float ks[2] = {scl.x, scl.y};
+        float vs[2] = {scl.z, scl.w};
 #pragma unroll
         for (int n = 0; n < NH; ++n)
 #pragma unroll
@@ -855,10 +867,10 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     base_pos += np;
     cu = after(cu);
     np = dead ? 0 : nn;
-    pg = pg_unit;
-    pg_next = load_pages(s_unit[cu], 32, np);
+    row = row_unit;
+    off = off_unit;
     nn = count(s_unit[after(cu)]);
-    pg_unit = load_pages(s_unit[after(cu)], 0, nn);
+    row_unit = load_pages(s_unit[after(cu)], 0, nn);
 
     // A run has at most two partials (its first and its last unit); blocks of
     // fixed chunks (larger batches) merge as they go.
@@ -949,6 +961,8 @@ cudaError_t launch_shape(const Kv8Args &a, cudaStream_t st) {
   memset(&tmv, 0, sizeof(tmv));
   const bool paged = a.ws.index_mode == PKV_IDX_PAGE_TABLE && a.ws.page_size % 16 == 0 &&
                      (long long)a.ws.n_layers * a.ws.pool_slots < 0x7fffffffll &&
+                     (16 % a.c.scale_block == 0 || a.c.scale_block % 16 == 0) &&
+                     (long long)a.ws.pool_slots / a.c.scale_block * a.ws.n_kv_heads < 0xffffffffll &&
                      encode_codes_map(&tmk, a.c.k_pool, a.ws) &&
                      encode_codes_map(&tmv, a.c.v_pool, a.ws);
   if (a.c.dtype == PKV_KV8_E4M3)
