@@ -141,6 +141,7 @@ struct KUnit {
   int bad;         // error bits
   long long base;  // where the request's index entries start
   long long srow;  // scale index of (layer, page 0, head g)
+  long long row0;  // byte of (layer, slot 0, head g) in a code pool
 };
 
 // A block's units in order.
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     KUnits us = s_us;
     KUnit u;
     u.b = u.g = u.c = u.n = u.t0 = u.t1 = u.bad = 0;
-    u.base = u.srow = 0;
+    u.base = u.srow = u.row0 = 0;
     while (us.pos < us.end) {
       ReqIndex ri;
       if (a.apportion) {
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       u.base = ri.base;
       u.bad = ri.ok ? 0 : PKV_DEVERR_PAGE;
       u.srow = ((long long)a.layer * pl.n_pages * H + u.g) * (ws.page_size / a.c.scale_block);
+      u.row0 = ((long long)a.layer * ws.pool_slots * H + u.g) * D;
       s_us = us;
       *dst = u;
       return;
@@ -365,6 +367,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   const int SB = a.c.scale_block, per_page = ws.page_size / SB;
   const int sshift = (SB & (SB - 1)) == 0 ? __ffs(SB) - 1 : -1;
   const int page_row = H * per_page;  // scales of a page
+  const int rs = H * D;               // bytes between the rows of consecutive slots
   const int layer_slot = a.layer * ws.pool_slots;  // PAGED only: fits (checked by the host)
   // fragment offsets in a stage (rows + 8 are 8 D bytes on)
   const int tk = perm<D>(r);
@@ -461,21 +464,20 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     } else {
       constexpr int CH = D / 16, RPI = 32 / CH;  // chunks per row, rows per copy
       const int tok0 = u.t0 + 16 * (warp + W * j), nv = u.t1 - tok0;
-      const int *raw = s_idx[warp][(base_pos + p) % (2 * NS)];
+      // lanes t and t + 16 resolve token t's slot (-1: none), the others ask them
+      int s = -1;
+      if (tt < nv) s = (int)slot_from_raw(ws, pl, s_idx[warp][(base_pos + p) % (2 * NS)][tt],
+                                          tok0 + tt, bad);
+      const uint8_t *kp = static_cast<const uint8_t *>(a.c.k_pool) + u.row0 + (lane % CH) * 16;
+      const uint8_t *vp = static_cast<const uint8_t *>(a.c.v_pool) + u.row0 + (lane % CH) * 16;
 #pragma unroll
       for (int i = 0; i < 16 / RPI; ++i) {
-        const int row = i * RPI + lane / CH, ch = lane % CH;
-        int kind = 0;
-        const int s = row < nv ? (int)slot_from_raw(ws, pl, raw[row], tok0 + row, kind) : -1;
-        bad |= kind;
-        const long long off =
-            s >= 0 ? (((long long)a.layer * ws.pool_slots + s) * H + g) * (long long)D + ch * 16 : 0;
-        const uint32_t d = dst + swz<D>(row, ch);
-        cp16(d, static_cast<const uint8_t *>(a.c.k_pool) + off, s >= 0 ? 16 : 0);
-        cp16(d + C::KB, static_cast<const uint8_t *>(a.c.v_pool) + off, s >= 0 ? 16 : 0);
+        const int row = i * RPI + lane / CH, sr = __shfl_sync(0xffffffffu, s, row);
+        const long long at = (long long)max(sr, 0) * rs;
+        const uint32_t d = dst + swz<D>(row, lane % CH);
+        cp16(d, kp + at, sr >= 0 ? 16 : 0);
+        cp16(d + C::KB, vp + at, sr >= 0 ? 16 : 0);
       }
-      int kind = 0;
-      const int s = tt < nv ? (int)slot_from_raw(ws, pl, raw[tt], tok0 + tt, kind) : -1;
       long long si = 0;
       if (s >= 0) {
         const int page = pl.P == 1 ? s : s / pl.P;
