@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kKXWarps * 32)
 }
 
 constexpr int kKRThreads = 256;
-constexpr int kKRTokens = 8;  // tokens per tile
+constexpr int kKRTokens = 16;  // tokens per tile
 constexpr int kKRUnroll = 4;  // rows whose loads a thread has in flight
 
 // 32 bytes: one store where the address allows it.
@@ -221,117 +221,186 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool wi
   }
 }
 
-// gx CTAs per request walk its tiles of kKRTokens tokens.  The tile's slots and
-// scale rows are resolved once; then 2^tshift threads share a row of K or V,
-// 16 codes (32 or 64 bytes of values) at a time, with kKRUnroll rows' loads
-// issued before any is used.
+constexpr int kKRBatch = 256;  // requests whose tiles are laid out at a time
+
+// The tiles of kKRTokens tokens of all requests, one after the other, go round
+// the CTAs (one request's tiles over a share of the CTAs each left a batch of 16
+// requests of 1 to 8192 tokens waiting for its longest: 35 us, against 29).
+// A tile's slots and scale rows are resolved while the tile before it is read;
+// then 2^tshift threads share a row of K or V, 16 codes (32 or 64 bytes of
+// values) at a time, with kKRUnroll rows' loads issued before any is used.
 template <int D, int DT, bool F32>
 __global__ void __launch_bounds__(kKRThreads)
     kv8_read_kernel(const __grid_constant__ pkv_workspace ws, const __grid_constant__ pkv_kv8 c,
-                    int layer, int gx, int tshift, const int *__restrict__ starts,
+                    int batch, int layer, int tshift, const int *__restrict__ starts,
                     const int *__restrict__ dst_indptr, int n_rows, uint8_t *k_out,
                     uint8_t *v_out) {
-  __shared__ int s_slot[kKRTokens];         // -1: a bad index entry
-  __shared__ long long s_scale[kKRTokens];  // index of head 0's scale in the layer
+  __shared__ int s_pref[kKRBatch + 1], s_n[kKRBatch], s_start[kKRBatch], s_row[kKRBatch];
+  __shared__ long long s_base[kKRBatch];  // its index entries; -1: no row of the table
+  __shared__ int s_slot[2][kKRTokens];         // -1: a bad index entry
+  __shared__ long long s_scale[2][kKRTokens];  // index of head 0's scale in the layer
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x / gx, x = blockIdx.x - b * gx;
-  const bool lead = x == 0 && threadIdx.x == 0;
-  const int L = ws.seq_lens[b], start = starts ? starts[b] : 0;
-  const long long row0 = dst_indptr[b];
-  bool ok = L >= 0 && (long long)L <= len_cap(ws) && start >= 0;
-  long long base = 0;
-  int kind = ok ? 0 : PKV_DEVERR_LEN;
-  const int n = ok ? L - start : 0;
-  if (ok && n > 0) {
-    if (row0 < 0 || row0 + n > n_rows) kind = PKV_DEVERR_TOTAL;
-    if (ws.index_mode == PKV_IDX_FLAT) {
-      base = ws.kv_indptr[b];
-      if (base < 0 || base + L > ws.max_total_tokens) kind = PKV_DEVERR_TOTAL;
-    } else {
-      const int row = ws.req_pool_indices[b];
-      // no row of the table: every token is bad (written as zeros below)
-      base = row >= 0 && row < ws.max_reqs ? (long long)row * ws.max_pages_per_req : -1;
-    }
-  }
-  if (kind) {
-    if (lead) atomicOr(ws.err, kind);
-    return;
-  }
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool flat = ws.index_mode == PKV_IDX_FLAT;
   const int H = ws.n_kv_heads, W = H * (D / 16);  // 16-code words of a token's row
-  const int per_page = ws.page_size / c.scale_block, n_pages = ws.pool_slots / ws.page_size;
+  const int P = ws.page_size, per_page = P / c.scale_block, n_pages = ws.pool_slots / P;
   const uint4 *kp = static_cast<const uint4 *>(c.k_pool) + (long long)layer * ws.pool_slots * W;
   const uint4 *vp = static_cast<const uint4 *>(c.v_pool) + (long long)layer * ws.pool_slots * W;
   const long long srow = (long long)layer * n_pages * H * per_page;
   const float *ks = c.k_scale + srow, *vs = c.v_scale + srow;
   constexpr int OB = F32 ? 64 : 32;  // bytes of 16 values
-  const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
-  const int col = threadIdx.x & ((1 << tshift) - 1), rr = threadIdx.x >> tshift;
+  const bool wide =
+      ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
+  const int col = tid & ((1 << tshift) - 1), rr = tid >> tshift;
   const int rows = kKRThreads >> tshift;  // rows side by side
-  for (int t0 = x * kKRTokens; t0 < n; t0 += gx * kKRTokens) {
-    const int m = min(kKRTokens, n - t0);
-    __syncthreads();  // the last tile's slots are no longer read
-    if (threadIdx.x < m) {
-      int bad = 0, slot = -1;
-      if (base >= 0) slot = token_slot(ws, base, start + t0 + threadIdx.x, &bad);
-      else bad = PKV_DEVERR_PAGE;
-      if (bad) atomicOr(ws.err, bad);
-      s_slot[threadIdx.x] = slot;
-      const int page = slot >= 0 ? slot / ws.page_size : 0;
-      s_scale[threadIdx.x] = (long long)page * H * per_page +
-                             (slot >= 0 ? (slot - page * ws.page_size) / c.scale_block : 0);
-    }
-    __syncthreads();
-    for (int w = col; w < W; w += 1 << tshift) {
-      const int g = w / (D / 16);
-      // row i of the tile: K of token i, then V of token i - m
-      for (int i0 = rr; i0 < 2 * m; i0 += kKRUnroll * rows) {
-        uint4 code[kKRUnroll];
-        float s[kKRUnroll];
-#pragma unroll
-        for (int k = 0; k < kKRUnroll; ++k) {
-          const int i = i0 + k * rows;
-          const bool isv = i >= m;
-          const int t = isv ? i - m : i;
-          code[k] = make_uint4(0, 0, 0, 0);
-          s[k] = 0.f;
-          if (i < 2 * m && s_slot[t] >= 0) {
-            code[k] = ldg_nc_v4((isv ? vp : kp) + (long long)s_slot[t] * W + w);
-            s[k] = (isv ? vs : ks)[s_scale[t] + (long long)g * per_page];
+
+  for (int g0 = 0; g0 < batch; g0 += kKRBatch) {
+    const int nb = min(kKRBatch, batch - g0);
+    __syncthreads();  // the last group is done with
+    if (tid < 32) {
+      int run = 0;
+      for (int i = lane; i < (nb + 31) / 32 * 32; i += 32) {
+        const int b = g0 + i;
+        int n = 0, kind = 0, start = 0, row0 = 0;
+        long long base = 0;
+        if (i < nb) {
+          const int L = ws.seq_lens[b];
+          start = starts ? starts[b] : 0;
+          row0 = dst_indptr[b];
+          base = flat ? ws.kv_indptr[b] : ws.req_pool_indices[b];
+          if (L < 0 || (long long)L > len_cap(ws) || start < 0) kind = PKV_DEVERR_LEN;
+          else n = max(L - start, 0);
+          if (n > 0 && (row0 < 0 || (long long)row0 + n > n_rows)) kind = PKV_DEVERR_TOTAL;
+          if (n > 0 && flat && (base < 0 || base + L > ws.max_total_tokens))
+            kind = PKV_DEVERR_TOTAL;
+          // no row of the table: every token is bad (written as zeros below)
+          if (!flat) base = base >= 0 && base < ws.max_reqs ? base * ws.max_pages_per_req : -1;
+          if (kind) {
+            if (blockIdx.x == 0) atomicOr(ws.err, kind);
+            n = 0;
           }
         }
+        const int tiles = (n + kKRTokens - 1) / kKRTokens;
+        int incl = tiles;
 #pragma unroll
-        for (int k = 0; k < kKRUnroll; ++k) {
-          const int i = i0 + k * rows;
-          if (i >= 2 * m) break;
-          const bool isv = i >= m;
-          const int t = isv ? i - m : i;
-          const uint32_t cw[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
-          float f[16];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a[4];
-            decode4<DT>(cw[e], a);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) f[4 * e + y] = a[y] * s[k];
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        if (i < nb) {
+          s_pref[i] = run + incl - tiles;
+          s_n[i] = n;
+          s_start[i] = start;
+          s_row[i] = row0;
+          s_base[i] = base;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (lane == 0) s_pref[nb] = run;
+    }
+    __syncthreads();
+    const int total = s_pref[nb];
+    // request (in the group) of a tile
+    auto find = [&](int tile) {
+      int lo = 0, hi = nb - 1;  // last one with pref <= tile
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_pref[mid] <= tile) lo = mid;
+        else hi = mid - 1;
+      }
+      return lo;
+    };
+    // threads 0 .. 15 resolve a tile's tokens: the raw entry early, the slot late
+    int raw = -1, tok = 0;
+    auto fetch = [&](int tile) {
+      raw = -1;
+      if (tid < kKRTokens && tile < total) {
+        const int q = find(tile), t = (tile - s_pref[q]) * kKRTokens + tid;
+        if (t < s_n[q] && s_base[q] >= 0) {
+          tok = s_start[q] + t;
+          raw = flat ? ws.kv_indices[s_base[q] + tok] : ws.page_table[s_base[q] + tok / P];
+        }
+      }
+    };
+    auto resolve = [&](int tile, int buf) {
+      if (tid < kKRTokens && tile < total) {
+        const int q = find(tile), t = (tile - s_pref[q]) * kKRTokens + tid;
+        if (t < s_n[q]) {
+          int slot = -1, page = 0;
+          if (raw >= 0 && raw < (flat ? ws.pool_slots : n_pages)) {
+            page = flat ? raw / P : raw;
+            slot = flat ? raw : raw * P + tok % P;
+          } else {
+            atomicOr(ws.err, flat ? PKV_DEVERR_SLOT : PKV_DEVERR_PAGE);
           }
-          uint8_t *p = (isv ? v_out : k_out) + ((row0 + t0 + t) * W + w) * OB;
-          if constexpr (F32) {
+          s_slot[buf][tid] = slot;
+          s_scale[buf][tid] = (long long)page * H * per_page +
+                              (slot >= 0 ? (slot - page * P) / c.scale_block : 0);
+        }
+      }
+    };
+    fetch(blockIdx.x);
+    resolve(blockIdx.x, 0);
+    int buf = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, buf ^= 1) {
+      __syncthreads();  // this tile's slots; and the other buffer is free
+      fetch(tile + gridDim.x);
+      const int q = find(tile), t0 = (tile - s_pref[q]) * kKRTokens;
+      const int m = min(kKRTokens, s_n[q] - t0);
+      const long long row0 = (long long)s_row[q] + t0;
+      for (int w = col; w < W; w += 1 << tshift) {
+        const long long head = (long long)(w / (D / 16)) * per_page;
+        // row i of the tile: K of token i, then V of token i - m
+        for (int i0 = rr; i0 < 2 * m; i0 += kKRUnroll * rows) {
+          uint4 code[kKRUnroll];
+          float s[kKRUnroll];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+          for (int k = 0; k < kKRUnroll; ++k) {
+            const int i = i0 + k * rows;
+            const bool isv = i >= m;
+            const int t = isv ? i - m : i;
+            code[k] = make_uint4(0, 0, 0, 0);
+            s[k] = 0.f;
+            if (i < 2 * m && s_slot[buf][t] >= 0) {
+              code[k] = ldg_nc_v4((isv ? vp : kp) + (long long)s_slot[buf][t] * W + w);
+              s[k] = (isv ? vs : ks)[s_scale[buf][t] + head];
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kKRUnroll; ++k) {
+            const int i = i0 + k * rows;
+            if (i >= 2 * m) break;
+            const bool isv = i >= m;
+            const int t = isv ? i - m : i;
+            const uint32_t cw[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a[4];
+              decode4<DT>(cw[e], a);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) f[4 * e + y] = a[y] * s[k];
+            }
+            uint8_t *p = (isv ? v_out : k_out) + ((row0 + t) * W + w) * OB;
+            if constexpr (F32) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(f[8 * h + e]);
+                store32(p + 32 * h, o, wide);
+              }
+            } else {
               uint32_t o[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(f[8 * h + e]);
-              store32(p + 32 * h, o, wide);
+              for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+              store32(p, o, wide);
             }
-          } else {
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-            store32(p, o, wide);
           }
         }
       }
+      resolve(tile + gridDim.x, buf ^ 1);
     }
   }
 }
@@ -393,24 +462,18 @@ struct ReadLaunch {
   cudaStream_t st;
   template <int D, int DT>
   cudaError_t operator()() {
-    // about 16 CTAs for each of 152 SMs over the batch, no more per request
-    // than it can have tiles
-    const long long most = len_cap(ws) < n_rows ? len_cap(ws) : n_rows;
-    long long gx = (most + kKRTokens - 1) / kKRTokens;
-    const long long share = (152 * 16 + batch - 1) / batch;
-    if (gx > share) gx = share;
-    if (gx < 1) gx = 1;
-    if (gx * batch > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    // as many CTAs as fit the GPU at once, no more than there can be tiles
+    const long long tiles = (long long)n_rows / kKRTokens + batch;
+    const unsigned grid = (unsigned)(tiles < 152 * 8 ? tiles : 152 * 8);
     // threads per row: the power of two that covers its 16-code words, 256 at most
     int tshift = 0;
     while (tshift < 8 && (1 << tshift) < ws.n_kv_heads * (D / 16)) ++tshift;
-    const dim3 grid((unsigned)(gx * batch));
     if (flags & PKV_FLAG_OUT_F32)
-      return launch_pdl(kv8_read_kernel<D, DT, true>, grid, dim3(kKRThreads), 0, st, ws, c, layer,
-                        (int)gx, tshift, starts, dst_indptr, n_rows, static_cast<uint8_t *>(k),
-                        static_cast<uint8_t *>(v));
-    return launch_pdl(kv8_read_kernel<D, DT, false>, grid, dim3(kKRThreads), 0, st, ws, c, layer,
-                      (int)gx, tshift, starts, dst_indptr, n_rows, static_cast<uint8_t *>(k),
+      return launch_pdl(kv8_read_kernel<D, DT, true>, dim3(grid), dim3(kKRThreads), 0, st, ws, c,
+                        batch, layer, tshift, starts, dst_indptr, n_rows,
+                        static_cast<uint8_t *>(k), static_cast<uint8_t *>(v));
+    return launch_pdl(kv8_read_kernel<D, DT, false>, dim3(grid), dim3(kKRThreads), 0, st, ws, c,
+                      batch, layer, tshift, starts, dst_indptr, n_rows, static_cast<uint8_t *>(k),
                       static_cast<uint8_t *>(v));
   }
 };
