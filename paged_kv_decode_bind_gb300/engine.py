@@ -34,7 +34,15 @@ class DecodeRunner:
 
     def __init__(self, ws: Workspace, batch: int, *, num_splits: int = 1, flags: int = 0,
                  scale: float | None = None, stream: torch.cuda.Stream | None = None,
-                 fused: bool = True, plan: bool = False, out_per_layer: bool = False):
+                 fused: bool = True, plan: bool = False, out_per_layer: bool = False,
+                 cache=None, norm_rope=None):
+        """cache: a Kv8Cache of this workspace; the layers then append to and
+        attend over it instead of the bf16 pools (flags: PKV_FLAG_OUT_F32 and
+        PKV_FLAG_WRITE_LSE).  norm_rope: a QkNormRope, or one per layer, applied
+        to the layer's q and k at ws.position_ids before they are used."""
+        if cache is not None and (not fused or plan):
+            raise ValueError("a step on the 8-bit cache has no unfused or planned form")
+        self.cache = cache
         self.ws = ws
         self.batch = batch
         sh = ws.shape
@@ -49,6 +57,17 @@ class DecodeRunner:
         self.k_in = torch.zeros((NL, B, sh["n_kv_heads"], sh["head_dim"]), dtype=torch.bfloat16,
                                 device=dev)
         self.v_in = torch.zeros_like(self.k_in)
+        self.norm_rope = None
+        if norm_rope is not None:
+            self.norm_rope = (list(norm_rope) if isinstance(norm_rope, (list, tuple))
+                              else [norm_rope] * NL)
+            if len(self.norm_rope) != NL or any(
+                    (r.struct.n_q_heads, r.struct.n_kv_heads, r.struct.head_dim) !=
+                    (sh["n_q_heads"], sh["n_kv_heads"], sh["head_dim"]) for r in self.norm_rope):
+                raise ValueError("norm_rope: one QkNormRope of the workspace's heads per layer")
+            # one layer's rows at a time: the next layer's kernel waits for this one's
+            self.q_use = torch.zeros_like(self.q_in[0])
+            self.k_use = torch.zeros_like(self.k_in[0])
         # out_per_layer: every layer writes its own output rows (layer l's into
         # outs[l], through a copy of the workspace struct whose `out` points
         # there), so a step leaves all its layers' results behind instead of
@@ -77,7 +96,11 @@ class DecodeRunner:
         # programmatic dependent launch the plan saves no time, and a one-layer
         # step pays for the extra launch.
         self.use_plan = plan and fused and mma and ws.work_plan is not None
-        per_layer = 1 if fused and mma else 2 + int(split)
+        if cache is not None:
+            per_layer = 2  # append, attention (with its merge)
+        else:
+            per_layer = 1 if fused and mma else 2 + int(split)
+        per_layer += int(self.norm_rope is not None)
         self.launches_per_step = (1 + int(flat) + int(self.use_plan and 0 < batch <= 256) +
                                   NL * per_layer)
 
@@ -92,8 +115,22 @@ class DecodeRunner:
 
     def layer(self, l, events=None):
         """Layer l: one fused launch (append + attention + merge), or the
-        three separate kernels when built with fused=False."""
+        three separate kernels when built with fused=False, or the 8-bit cache's
+        append and attention; the norm with rotation first where there is one."""
         s = self._s()
+        q, k = self.q_in[l], self.k_in[l]
+        if self.norm_rope is not None:
+            _abi.pkv_qk_norm_rope(self.norm_rope[l], self.batch, q, k, self.ws.position_ids,
+                                  self.q_use, self.k_use, s)
+            q, k = self.q_use, self.k_use
+        if self.cache is not None:
+            if events is not None:
+                events[0].record(s)
+            _abi.pkv_kv8_decode_layer(self._wsl(l), self.cache, self.batch, l, q, k, self.v_in[l],
+                                      self.scale, self.num_splits, self.flags, s)
+            if events is not None:
+                events[1].record(s)
+            return
         if self.fused:
             if events is not None:
                 events[0].record(s)
@@ -101,18 +138,16 @@ class DecodeRunner:
             # more launches earlier, so they may start before layer l-1 ends.
             early = _abi.PKV_FLAG_PLAN_EARLY if (l > 0 and events is None) else 0
             use = _abi.PKV_FLAG_USE_PLAN if self.use_plan else 0
-            _abi.pkv_decode_layer(self._wsl(l), self.batch, l, self.q_in[l], self.k_in[l],
-                                  self.v_in[l], self.scale, self.num_splits,
-                                  self.flags | early | use, s)
+            _abi.pkv_decode_layer(self._wsl(l), self.batch, l, q, k, self.v_in[l], self.scale,
+                                  self.num_splits, self.flags | early | use, s)
             if events is not None:
                 events[1].record(s)
             return
-        _abi.pkv_bind_step(self.ws, self.batch, _abi.PKV_BIND_APPEND_ONLY, l, 1, self.k_in[l],
-                           self.v_in[l], s)
+        _abi.pkv_bind_step(self.ws, self.batch, _abi.PKV_BIND_APPEND_ONLY, l, 1, k, self.v_in[l], s)
         if events is not None:
             events[0].record(s)
-        _abi.pkv_decode_attn(self._wsl(l), self.batch, l, self.q_in[l], self.scale,
-                             self.num_splits, self.flags, s)
+        _abi.pkv_decode_attn(self._wsl(l), self.batch, l, q, self.scale, self.num_splits,
+                             self.flags, s)
         if events is not None:
             events[1].record(s)
         if self.num_splits > 1:

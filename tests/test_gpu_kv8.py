@@ -370,6 +370,114 @@ def test_chunk_then_read_then_decode(cuda):
     _same(cache, prob)
 
 
+@pytest.mark.parametrize("dtype,page,block", [("e4m3", 16, 16), ("int8", 1, 1), ("e4m3", 8, 4)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_runner_steps(cuda, dtype, page, block, graph):
+    # whole steps as a program runs them: bind, then per layer the norm with
+    # rotation at the bind's positions, append and attention
+    from paged_kv_decode_bind_gb300 import DecodeRunner, QkNormRope, rope_table
+    lens, steps, layers, d = [3, 40, 129], 3, 2, 128
+    prob = _problem(lens, dtype, page, block, layers=layers, steps=steps)
+    ws, cache = prob.device(max_splits=3)
+    table = rope_table(200, d)
+    ropes = [QkNormRope(n_q_heads=8, n_kv_heads=2, head_dim=d, cos_sin=table,
+                        q_weight=W.normal_bf16((d,), 50 + l).cuda(),
+                        k_weight=W.normal_bf16((d,), 60 + l).cuda()) for l in range(layers)]
+    run = DecodeRunner(ws, 3, num_splits=3, scale=prob.p.scale, cache=cache, norm_rope=ropes,
+                       out_per_layer=True)
+    assert run.launches_per_step == 1 + (page == 1) + 3 * layers
+    if graph:
+        run.capture()
+    tab = table.double().cpu().numpy()
+    for step in range(steps):
+        q, k, v = W.step_inputs(prob.p, step)
+        for dst, src in ((run.q_in, q), (run.k_in, k), (run.v_in, v)):
+            dst.copy_(src)
+        run.replay() if graph else run.step()
+        torch.cuda.synchronize()
+        lens = [n + 1 for n in lens]
+        for l in range(layers):
+            # the rotated rows as the kernel rounds them (its own tests bound them)
+            qr = torch.zeros((3, 8, d), dtype=torch.bfloat16, device="cuda")
+            kr = torch.zeros((3, 2, d), dtype=torch.bfloat16, device="cuda")
+            A.pkv_qk_norm_rope(ropes[l], 3, run.q_in[l], run.k_in[l], ws.position_ids, qr, kr)
+            for b in range(3):
+                cos, sin = tab[lens[b] - 1, :d // 2], tab[lens[b] - 1, d // 2:]
+                want = K8.norm_rope(K8_values(k[l, b]), K8_values(ropes[l].k_weight.cpu()), cos,
+                                    sin, float(np.float32(1e-6)), False)
+                assert np.abs(kr[b].double().cpu().numpy() - want).max() <= 2.0 ** -7 * \
+                    np.abs(want).max()
+                s = prob.slots(b, lens[b] - 1, lens[b])
+                prob.k.append(l, s, K8_values(kr[b:b + 1].cpu()))
+                prob.v.append(l, s, K8_values(v[l, b:b + 1]))
+            check_attention(run.outs[l].double().cpu().numpy(), None,
+                            prob.attention(l, qr.cpu(), lens), f"step {step} layer {l}", BF16)
+    _same(cache, prob)
+    assert int(ws.err.item()) == 0 and int(ropes[0].err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype,page,block", [("e4m3", 16, 16), ("int8", 1, 1), ("int8", 12, 4)])
+@pytest.mark.parametrize("S", [1, 3])
+def test_extender(cuda, dtype, page, block, S):
+    from paged_kv_decode_bind_gb300 import Kv8Extender
+    before, new = [0, 130, 700], [90, 1, 33]
+    lens = [a + b for a, b in zip(before, new)]
+    prob = _problem(lens, dtype, page, block, layers=2)
+    ws, cache = prob.device()
+    ext = Kv8Extender(ws, cache, 3, max_new=96, max_context=740, scale=prob.p.scale, num_splits=S)
+    T = sum(new)
+    qo = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    for layer in range(2):
+        q, k, v = W.normal_bf16((T, 8, 128), 70), _rows((T, 2, 128), 71), _rows((T, 2, 128), 72)
+        out = torch.zeros((T, 8, 128), dtype=torch.float32, device="cuda")
+        ext.layer(layer, torch.from_numpy(qo).cuda(), 90, q.cuda(), k.cuda(), v.cuda(), out,
+                  A.PKV_FLAG_OUT_F32)
+        torch.cuda.synchronize()
+        got = out.double().cpu().numpy()
+        for b in range(3):
+            s = prob.slots(b, before[b], lens[b])
+            i = 0
+            while i < len(s):
+                n = min(len(s) - i, block - int(s[i]) % page % block)
+                prob.k.append(layer, s[i:i + n], K8_values(k[qo[b] + i:qo[b] + i + n]))
+                prob.v.append(layer, s[i:i + n], K8_values(v[qo[b] + i:qo[b] + i + n]))
+                i += n
+            kk, vv = (x.rows(layer, prob.slots(b, 0, lens[b])) for x in (prob.k, prob.v))
+            for t in range(new[b]):
+                n = before[b] + t + 1
+                o, _, _, _, _ = K8.attention(K8_values(q[qo[b] + t]), kk[:n], vv[:n], prob.p.scale)
+                # the bound of the extend kernel's own tests, relative to the
+                # values' size (P is applied as bf16 high and low parts)
+                assert np.abs(got[qo[b] + t] - o).max() <= 1e-3 * np.abs(vv[:n]).max()
+    _same(cache, prob)
+    assert int(ws.err.item()) == 0
+
+
+def test_extender_refuses_longer_contexts(cuda):
+    # a context past max_context: its request is skipped, its neighbour's rows
+    # are its own
+    from paged_kv_decode_bind_gb300 import Kv8Extender
+    lens = [60, 30]
+    prob = _problem(lens)
+    ws, cache = prob.device()
+    ext = Kv8Extender(ws, cache, 2, max_new=4, max_context=40, scale=prob.p.scale)
+    q, k, v = W.normal_bf16((4, 8, 128), 80), _rows((4, 2, 128), 81), _rows((4, 2, 128), 82)
+    out = torch.full((4, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    qo = torch.tensor([0, 2, 4], dtype=torch.int32).cuda()
+    ext.layer(0, qo, 2, q.cuda(), k.cuda(), v.cuda(), out)
+    torch.cuda.synchronize()
+    assert int(ws.err.item()) == A.PKV_DEVERR_LEN
+    s = prob.slots(1, 28, 30)
+    prob.k.append(0, s, K8_values(k[2:]))
+    prob.v.append(0, s, K8_values(v[2:]))
+    _same(cache, prob)
+    assert torch.all(out[:2] == 5.0)
+    kk, vv = (x.rows(0, prob.slots(1, 0, 30)) for x in (prob.k, prob.v))
+    o, _, _, _, _ = K8.attention(K8_values(q[3]), kk, vv, prob.p.scale)
+    got = out[3].double().cpu().numpy()
+    assert np.abs(got - o).max() <= 1e-3 * np.abs(vv).max() + BF16 * np.abs(o).max()
+
+
 def test_graph_replay_and_other_stream(cuda):
     lens = [33, 500]
     prob = _problem(lens, steps=4)

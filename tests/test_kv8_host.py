@@ -223,6 +223,37 @@ def test_cache_owner():
             Kv8Cache(ws, **kw)
 
 
+def test_runner_and_extender_arguments():
+    from paged_kv_decode_bind_gb300 import DecodeRunner, Kv8Extender
+    ws = _cpu_ws()
+    c = Kv8Cache(ws)
+    assert DecodeRunner(ws, 2, cache=c).launches_per_step == 1 + 2 * 2
+    for kw in (dict(fused=False), dict(plan=True)):
+        with pytest.raises(ValueError):
+            DecodeRunner(ws, 2, cache=c, **kw)
+    r = QkNormRope(n_q_heads=4, n_kv_heads=2, head_dim=64, cos_sin=rope_table(9, 64, device="cpu"))
+    assert DecodeRunner(ws, 2, norm_rope=r).launches_per_step == 1 + 2 * 2
+    other = QkNormRope(n_q_heads=2, n_kv_heads=2, head_dim=64,
+                       cos_sin=rope_table(9, 64, device="cpu"))
+    for bad in (other, [r], [r, other]):
+        with pytest.raises(ValueError):
+            DecodeRunner(ws, 2, norm_rope=bad)
+    e = Kv8Extender(ws, c, 2, max_new=3, max_context=20, scale=0.1, num_splits=2)
+    assert e.n_rows == 64 and e.first_row.tolist() == [0, 32]
+    assert e.table.tolist() == [[0, 1], [2, 3]]
+    assert e.read_view.max_seq_len == 20 and e.rows_view.max_seq_len == 20
+    assert e.rows_view.seq_lens == ws.struct.seq_lens and e.rows_view.err == ws.struct.err
+    assert e.part_o.numel() == 2 * 3 * 2 * 4 * 64
+    assert Kv8Extender(ws, c, 1, max_new=1, max_context=99, scale=0.1).read_view.max_seq_len == 32
+    with pytest.raises(ValueError):
+        e.layer(0, 0, 4, None, None, None, None)
+    for kw in (dict(batch=3), dict(max_new=0), dict(max_context=0), dict(num_splits=0)):
+        args = dict(batch=2, max_new=3, max_context=20, scale=0.1)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            Kv8Extender(ws, c, args.pop("batch"), **args)
+
+
 def test_rope_owner():
     t = rope_table(10, 32, device="cpu")
     w = torch.ones(64, dtype=torch.bfloat16)
