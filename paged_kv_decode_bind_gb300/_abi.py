@@ -343,15 +343,15 @@ def pkv_kv8_decode_layer(ws, cache, batch, layer, q, k_new, v_new, scale, num_sp
     return _check("pkv_kv8_decode_layer", s) if check else s
 
 
-def _stride(x, width, head_dim):
-    """Elements between the tokens of x: a pointer or None is dense; a tensor is
-    [tokens, width] or [tokens, heads, head_dim] with dense heads."""
+def _heads(x, width, head_dim):
+    """Pointer and elements between tokens of x: a pointer or None is dense; a
+    tensor is [tokens, width] or [tokens, heads, head_dim] with dense heads."""
     if x is None or isinstance(x, int):
-        return width
+        return x, width
     st = x.stride()
     if st[-1] != 1 or len(st) not in (2, 3) or (len(st) == 3 and st[1] != head_dim):
         raise ValueError("heads must be dense: [tokens, width] or [tokens, heads, head_dim]")
-    return st[0]
+    return x.data_ptr(), st[0]
 
 
 def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None, check=True):
@@ -361,9 +361,8 @@ def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None,
     st = args.struct if hasattr(args, "struct") else args
     D = st.head_dim
     qw, kw = st.n_q_heads * D, st.n_kv_heads * D
-    s = load().pkv_qk_norm_rope(ctypes.byref(st), int(n_tokens), _ptr(q), _stride(q, qw, D),
-                                _ptr(k), _stride(k, kw, D), _ptr(positions), _ptr(q_out),
-                                _stride(q_out, qw, D), _ptr(k_out), _stride(k_out, kw, D),
+    s = load().pkv_qk_norm_rope(st, n_tokens, *_heads(q, qw, D), *_heads(k, kw, D),
+                                _ptr(positions), *_heads(q_out, qw, D), *_heads(k_out, kw, D),
                                 _stream(stream))
     return _check("pkv_qk_norm_rope", s) if check else s
 

@@ -189,13 +189,13 @@ def test_rope_call_checks():
 
 def test_rope_strides_come_from_the_tensors():
     x = torch.zeros((3, 1024), dtype=torch.bfloat16)
-    assert A._stride(x[:, :512], 512, 128) == 1024
-    assert A._stride(x[:, :512].view(3, 4, 128), 512, 128) == 1024
-    assert A._stride(None, 256, 128) == 256
+    assert A._heads(x[:, :512], 512, 128) == (x.data_ptr(), 1024)
+    assert A._heads(x[:, 512:].view(3, 4, 128), 512, 128) == (x.data_ptr() + 1024, 1024)
+    assert A._heads(None, 256, 128) == (None, 256)
     with pytest.raises(ValueError):
-        A._stride(x[:, ::2], 512, 128)
+        A._heads(x[:, ::2], 512, 128)
     with pytest.raises(ValueError):
-        A._stride(x.view(3, 8, 128).transpose(0, 1), 1024, 128)
+        A._heads(x.view(3, 8, 128).transpose(0, 1), 1024, 128)
 
 
 def _cpu_ws(page=16):
