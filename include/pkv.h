@@ -545,9 +545,11 @@ pkv_status pkv_kv8_read(const pkv_workspace *ws, const pkv_kv8 *c, int batch, in
  *   s_t = scale * k_scale_t * (q . code_k,t),  o = sum_t softmax(s)_t v_scale_t code_v,t.
  *   num_splits  S in [1, max_splits]; S > 1 needs o_part, ml_part and
  *               split_counters (zeroed once, left zeroed).
- *   flags       PKV_FLAG_OUT_F32, PKV_FLAG_WRITE_LSE, PKV_FLAG_PLAN_EARLY (no
- *               effect in a call that appends), PKV_FLAG_TEST_SKIP_FIRST_TILE
- *               (no effect unless P % 16 == 0).
+ *   flags       PKV_FLAG_OUT_F32, PKV_FLAG_WRITE_LSE, PKV_FLAG_PLAN_EARLY (the
+ *               caller's guarantee also covers out_loc and this cache's codes and
+ *               scales; the block appended to waits for the append),
+ *               PKV_FLAG_TEST_SKIP_FIRST_TILE (no effect where TMA boxes do not
+ *               apply).
  * The partial of a split holds its (normalised output, log-sum-exp, 1).
  * Host errors: as pkv_decode_layer and pkv_kv8_append; PKV_ERR_INVALID for
  * another flag; PKV_ERR_UNSUPPORTED for G not in {1, 2, 4, 8, 16}.

@@ -65,10 +65,11 @@ constexpr int kKAThreads = 256;
 template <int D, int DT>
 __global__ void __launch_bounds__(kKAThreads)
     kv8_append_kernel(const __grid_constant__ pkv_workspace ws, const __grid_constant__ pkv_kv8 c,
-                      int batch, int layer_begin, const uint4 *__restrict__ k_new,
+                      int batch, int layer_begin, bool early, const uint4 *__restrict__ k_new,
                       const uint4 *__restrict__ v_new) {
+  if (early) pdl_trigger();  // the next kernel itself waits for what it must
   pdl_wait();
-  pdl_trigger();
+  if (!early) pdl_trigger();
   constexpr int LPR = D / 8;
   const int b = blockIdx.x, rel = blockIdx.y, layer = layer_begin + rel;
   const int loc = ws.out_loc[b];
@@ -421,11 +422,12 @@ struct AppendLaunch {
   const pkv_kv8 &c;
   int batch, layer_begin, layer_count;
   const void *k, *v;
+  bool early;
   cudaStream_t st;
   template <int D, int DT>
   cudaError_t operator()() {
     return launch_pdl(kv8_append_kernel<D, DT>, dim3(batch, layer_count), dim3(kKAThreads), 0, st,
-                      ws, c, batch, layer_begin, static_cast<const uint4 *>(k),
+                      ws, c, batch, layer_begin, early, static_cast<const uint4 *>(k),
                       static_cast<const uint4 *>(v));
   }
 };
@@ -482,8 +484,9 @@ struct ReadLaunch {
 
 cudaError_t launch_kv8_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,
                               int layer_begin, int layer_count, const void *k_new,
-                              const void *v_new, cudaStream_t st) {
-  return by_shape(ws, c, AppendLaunch{ws, c, batch, layer_begin, layer_count, k_new, v_new, st});
+                              const void *v_new, bool early, cudaStream_t st) {
+  return by_shape(ws, c,
+                  AppendLaunch{ws, c, batch, layer_begin, layer_count, k_new, v_new, early, st});
 }
 
 cudaError_t launch_kv8_extend_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,

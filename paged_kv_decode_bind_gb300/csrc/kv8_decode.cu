@@ -139,6 +139,7 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi
 struct KUnit {
   int b, g, c, n, t0, t1;
   int bad;         // error bits
+  int fresh;       // first token of the block that this call appends to
   long long base;  // where the request's index entries start
   long long srow;  // scale index of (layer, page 0, head g)
   long long row0;  // byte of (layer, slot 0, head g) in a code pool
@@ -152,7 +153,7 @@ struct KUnit {
 // block has the same number whatever the lengths are; a run that crosses the
 // end of a request becomes two units.  The heads of a token lie side by side in
 // the pool, so the blocks of a group read whole DRAM pages between them (with
-// runs over one head after the other, 4 x 65536 tokens took 138 us, not TIMED).
+// runs over one head after the other 4 x 65536 tokens took 138 us, not 96).
 // Each request counts kUnitCost pieces more than it has, in front: what a block
 // spends on starting and finishing a unit (2 us against 0.2 us for a piece).
 // q = ceil(line / groups), at least 8 (one piece per warp) and at least
@@ -299,8 +300,10 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     KUnit u;
     u.b = u.g = u.c = u.n = u.t0 = u.t1 = u.bad = 0;
     u.base = u.srow = u.row0 = 0;
+    u.fresh = 0x7fffffff;
     while (us.pos < us.end) {
       ReqIndex ri;
+      int L;
       if (a.apportion) {
         while (s_pref[us.b + 1] <= us.pos) ++us.b;
         const int real = s_pref[us.b] + kUnitCost, last = s_pref[us.b + 1];  // its pieces
@@ -313,7 +316,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
         u.c = (int)blockIdx.x / H - first;
         u.n = (last - 1) / us.q - first + 1;
         u.t0 = 16 * (from - real);
-        u.t1 = min(16 * (stop - real), s_len[us.b]);
+        L = s_len[us.b];
+        u.t1 = min(16 * (stop - real), L);
         ri = req_index_cached(ws, s_base, us.b);
       } else {
         const int hb = a.batch * H;
@@ -322,9 +326,9 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
         u.b = x / H;
         u.g = x - u.b * H;
         us.pos += gridDim.x;
-        const int L = compact                  ? s_len[u.b]
-                      : u.c == 0 && u.g == 0 ? checked_len(ws, u.b, ws.err)
-                                             : usable_len(ws, u.b);
+        L = compact                  ? s_len[u.b]
+            : u.c == 0 && u.g == 0 ? checked_len(ws, u.b, ws.err)
+                                   : usable_len(ws, u.b);
         const bool whole = a.num_splits == 1;
         if (u.c * (long long)us.chunk >= L) continue;  // past the request's end
         u.t0 = whole ? 0 : u.c * us.chunk;
@@ -335,6 +339,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       u.base = ri.base;
       u.bad = ri.ok ? 0 : PKV_DEVERR_PAGE;
       u.srow = ((long long)a.layer * pl.n_pages * H + u.g) * (ws.page_size / a.c.scale_block);
+      if (a.k_new) u.fresh = (L - 1) / a.c.scale_block * a.c.scale_block;
       u.row0 = ((long long)a.layer * ws.pool_slots * H + u.g) * D;
       s_us = us;
       *dst = u;
@@ -441,6 +446,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     const bool in_next = p >= np;
     const int j = in_next ? p - np : p;
     KUnit &u = s_unit[in_next ? after(cu) : cu];
+    // the append's kernel is the one before this: its block waits for it
+    if (u.t0 + 16 * (warp + W * j) + 16 > u.fresh) wait_previous();
     const int g = u.g;
     const float *sbase = scales + u.srow;
     const uint32_t dst = ring + st_in * C::STAGE;
@@ -984,10 +991,12 @@ bool kv8_decode_supported(int head_dim, int group) {
 cudaError_t launch_kv8_decode(const Kv8Args &args, cudaStream_t st) {
   Kv8Args a = args;
   if (a.k_new) {
-    const cudaError_t e =
-        launch_kv8_append(a.ws, a.c, a.batch, a.layer, 1, a.k_new, a.v_new, st);
+    // With PKV_FLAG_PLAN_EARLY the append lets this kernel start while the one
+    // before the append still runs: it plans and loads everything but the block
+    // appended to, and waits for the append (which waits for the rest) there.
+    const cudaError_t e = launch_kv8_append(a.ws, a.c, a.batch, a.layer, 1, a.k_new, a.v_new,
+                                            (a.flags & PKV_FLAG_PLAN_EARLY) != 0, st);
     if (e != cudaSuccess) return e;
-    a.flags &= ~PKV_FLAG_PLAN_EARLY;  // the append's rows are read
   }
   const int D = a.ws.head_dim, G = a.ws.n_q_heads / a.ws.n_kv_heads;
 #define PKV_KV8_CASE(DD, GG) \

@@ -390,7 +390,7 @@ pkv_status pkv_kv8_append(const pkv_workspace *ws, const pkv_kv8 *c, int batch, 
   if (batch == 0 || layer_count == 0) return PKV_OK;
   if (!ws->out_loc || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))
     return PKV_ERR_INVALID;
-  return from_cuda(launch_kv8_append(*ws, *c, batch, layer_begin, layer_count, k_new, v_new,
+  return from_cuda(launch_kv8_append(*ws, *c, batch, layer_begin, layer_count, k_new, v_new, false,
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 

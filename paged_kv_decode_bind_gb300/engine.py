@@ -126,8 +126,10 @@ class DecodeRunner:
         if self.cache is not None:
             if events is not None:
                 events[0].record(s)
+            # as below: what a layer after the first reads early is older
+            early = _abi.PKV_FLAG_PLAN_EARLY if (l > 0 and events is None) else 0
             _abi.pkv_kv8_decode_layer(self._wsl(l), self.cache, self.batch, l, q, k, self.v_in[l],
-                                      self.scale, self.num_splits, self.flags, s)
+                                      self.scale, self.num_splits, self.flags | early, s)
             if events is not None:
                 events[1].record(s)
             return

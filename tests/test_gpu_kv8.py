@@ -610,6 +610,36 @@ def test_early_start(cuda, page):
     assert int(ws.err.item()) == 0
 
 
+@pytest.mark.parametrize("page,block", [(16, 16), (64, 64), (16, 2), (1, 1), (12, 4)])
+def test_early_start_with_append(cuda, page, block):
+    # every layer appends and starts early: the appended block (its older rows
+    # rounded again) is the one that is attended, over many quick layers
+    lens, layers, steps = [700, 47, 0, 15], 6, 4
+    prob = _problem(lens, page=page, block=block, layers=layers, steps=steps)
+    ws, cache = prob.device(max_splits=4)
+    for step in range(steps):
+        q, k, v = (x.cuda() for x in W.step_inputs(prob.p, step))
+        k = k * (4.0 ** step)  # every step's rows make their block grow
+        outs = []
+        A.pkv_bind_step(ws, 4, A.PKV_BIND_STEADY)
+        for layer in range(layers):
+            A.pkv_kv8_decode_layer(ws, cache, 4, layer, q[layer], k[layer], v[layer],
+                                   prob.p.scale, 4, A.PKV_FLAG_WRITE_LSE |
+                                   (A.PKV_FLAG_PLAN_EARLY if layer else 0))
+            outs.append((ws.out_bf16(4).clone(), ws.lse[:4].clone()))
+        torch.cuda.synchronize()
+        lens = [n + 1 for n in lens]
+        for layer, (o, l) in enumerate(outs):
+            for b, n in enumerate(lens):
+                s = prob.slots(b, n - 1, n)
+                prob.k.append(layer, s, K8_values(k[layer, b:b + 1].cpu()))
+                prob.v.append(layer, s, K8_values(v[layer, b:b + 1].cpu()))
+            check_attention(o.double().cpu().numpy(), l.double().cpu().numpy(),
+                            prob.attention(layer, q[layer].cpu(), lens), "early", BF16)
+    _same(cache, prob)
+    assert int(ws.err.item()) == 0
+
+
 def test_append_bad_slot(cuda):
     prob = _problem([20, 30, 40])
     ws, cache = prob.device()
