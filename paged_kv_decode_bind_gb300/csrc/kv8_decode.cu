@@ -855,7 +855,9 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
           const float lse = unit_bad ? -INFINITY : M * kLn2 + logf(L);
           if (!final_out)
             *reinterpret_cast<float2 *>(ws.ml_part + (qrow * a.num_splits + split) * 2) =
-                make_float2(lse, unit_bad ? 0.f : 1.f);
+                // NaN as an infinite weight: the merge's difference of infinities
+                // makes the row NaN again
+                make_float2(lse == lse ? lse : INFINITY, unit_bad ? 0.f : 1.f);
           else if (a.flags & PKV_FLAG_WRITE_LSE)
             ws.lse[qrow] = lse;
         }

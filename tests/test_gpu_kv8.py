@@ -301,6 +301,46 @@ def test_attention_nan_reaches_its_own_request_only(cuda, n):
     check_attention(got, None, (o, None, bo, None), "others", BF16)
 
 
+def test_attention_queries_that_are_not_finite(cuda):
+    # a head whose query holds NaN or an infinity is NaN, the others are as they
+    # should be; a scale of zero averages the values
+    lens = [70, 300]
+    prob = _problem(lens)
+    ws, cache = prob.device(max_splits=3)
+    q = W.normal_bf16((2, 8, 128), 35)
+    bad = q.clone()
+    bad[0, 1, 5], bad[1, 6, 127] = float("nan"), float("inf")
+    A.pkv_kv8_decode_layer(ws, cache, 2, 0, bad.cuda(), None, None, prob.p.scale, 3)
+    torch.cuda.synchronize()
+    got = ws.out_bf16(2).double().cpu().numpy()
+    assert np.isnan(got[0, 1]).all() and np.isnan(got[1, 6]).all()
+    o, _, bo, _ = prob.attention(0, q, lens)
+    for x in (got, o, bo):
+        x[0, 1] = x[1, 6] = 0
+    check_attention(got, None, (o, None, bo, None), "finite heads", BF16)
+    prob.p.scale = 0.0
+    _attend(prob, ws, cache, q.cuda(), 3, lens, what="scale 0")
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_attention_random(cuda, seed):
+    # shapes, lengths, pages and splits drawn together
+    r = np.random.default_rng(900 + seed)
+    hkv = int(r.choice([1, 2, 3, 5]))
+    heads = (hkv * int(r.choice([1, 2, 4, 8, 16])), hkv)
+    page, block = PAGES[r.integers(len(PAGES))] if seed % 4 else [(48, 3), (80, 16)][seed // 4 % 2]
+    B = int(r.choice([1, 2, 5, 20, 40]))
+    top = int(r.choice([3, 40, 300, 1500 if B <= 5 else 200]))
+    lens = [int(x) for x in r.integers(0, top + 1, B)]
+    S = int(r.choice([1, 2, 3, 9, 40]))
+    d, dtype = int(r.choice([64, 128])), str(r.choice(["e4m3", "int8"]))
+    prob = _problem(lens, dtype, page, block, heads=heads, d=d, seed=seed + 1)
+    ws, cache = prob.device(max_splits=S, max_batch=B + 3)
+    q = W.normal_bf16((B, heads[0], d), 500 + seed).cuda()
+    flags = A.PKV_FLAG_OUT_F32 if seed % 3 == 0 else 0
+    _attend(prob, ws, cache, q, S, lens, flags, what=f"{heads} {page} {block} {lens} S={S} {d}")
+
+
 @pytest.mark.parametrize("batch", [1, 2])
 def test_rows_behind_the_batch_are_left(cuda, batch):
     prob = _problem([30, 40, 50])
@@ -416,20 +456,21 @@ def test_runner_steps(cuda, dtype, page, block, graph):
     assert int(ws.err.item()) == 0 and int(ropes[0].err.item()) == 0
 
 
-@pytest.mark.parametrize("dtype,page,block", [("e4m3", 16, 16), ("int8", 1, 1), ("int8", 12, 4)])
+@pytest.mark.parametrize("dtype,page,block,d", [("e4m3", 16, 16, 128), ("int8", 1, 1, 128),
+                                                ("int8", 12, 4, 64)])
 @pytest.mark.parametrize("S", [1, 3])
-def test_extender(cuda, dtype, page, block, S):
+def test_extender(cuda, dtype, page, block, d, S):
     from paged_kv_decode_bind_gb300 import Kv8Extender
     before, new = [0, 130, 700], [90, 1, 33]
     lens = [a + b for a, b in zip(before, new)]
-    prob = _problem(lens, dtype, page, block, layers=2)
+    prob = _problem(lens, dtype, page, block, d=d, layers=2)
     ws, cache = prob.device()
     ext = Kv8Extender(ws, cache, 3, max_new=96, max_context=740, scale=prob.p.scale, num_splits=S)
     T = sum(new)
     qo = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     for layer in range(2):
-        q, k, v = W.normal_bf16((T, 8, 128), 70), _rows((T, 2, 128), 71), _rows((T, 2, 128), 72)
-        out = torch.zeros((T, 8, 128), dtype=torch.float32, device="cuda")
+        q, k, v = W.normal_bf16((T, 8, d), 70), _rows((T, 2, d), 71), _rows((T, 2, d), 72)
+        out = torch.zeros((T, 8, d), dtype=torch.float32, device="cuda")
         ext.layer(layer, torch.from_numpy(qo).cuda(), 90, q.cuda(), k.cuda(), v.cuda(), out,
                   A.PKV_FLAG_OUT_F32)
         torch.cuda.synchronize()
@@ -687,6 +728,22 @@ def test_read_bad_requests(cuda):
     want[67:73] = prob.k.rows(0, prob.slots(4, 3, 9))
     assert np.array_equal(k.double().cpu().numpy(), want)
     assert int(ws.err.item()) == A.PKV_DEVERR_LEN | A.PKV_DEVERR_TOTAL | A.PKV_DEVERR_PAGE
+
+
+def test_read_many_requests(cuda):
+    # more requests than are laid out at a time, most of them short
+    lens = [(17 * i) % 41 for i in range(600)]
+    prob = _problem(lens, "int8", heads=(1, 1), d=64)
+    ws, cache = prob.device()
+    n = sum(lens)
+    k = torch.zeros((n, 1, 64), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    A.pkv_kv8_read(ws, cache, 600, 0, None, ws.kv_indptr, n, k, v)
+    torch.cuda.synchronize()
+    for got, side in ((k, prob.k), (v, prob.v)):
+        want = np.concatenate([side.rows(0, prob.slots(b, 0, m)) for b, m in enumerate(lens)])
+        assert np.array_equal(got.double().cpu().numpy(), want)
+    assert int(ws.err.item()) == 0
 
 
 def test_offsets_past_32_bits(cuda):

@@ -139,6 +139,38 @@ def test_strided_output_and_bad_positions(cuda):
            _expect(K8_values(k[good]), K8_values(args.k_weight.cpu()), tab, p, 32, eps, False), d)
 
 
+def test_norm_alone_needs_no_positions(cuda):
+    d = 128
+    q, w = _bf16((4, 3, d), 15), _bf16((d,), 16)
+    args = QkNormRope(n_q_heads=3, n_kv_heads=0, head_dim=d, rot_dim=0, q_weight=w.cuda())
+    out = torch.zeros((4, 3, d), dtype=torch.bfloat16, device="cuda")
+    A.pkv_qk_norm_rope(args, 4, q.cuda(), None, None, out, None)
+    torch.cuda.synchronize()
+    _check(out, _expect(K8_values(q), K8_values(w), None, [0] * 4, 0, float(np.float32(1e-6)),
+                        False), d)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_heads_that_are_not_finite(cuda, bad):
+    # a head with NaN or an infinity is its own affair
+    d = 64
+    q, w = _bf16((5, 4, d), 17), _bf16((d,), 18)
+    dirty = q.clone()
+    dirty[2, 1, 40] = bad
+    table = rope_table(8, d, device="cpu")
+    args = QkNormRope(n_q_heads=4, n_kv_heads=0, head_dim=d, cos_sin=table.cuda(), q_weight=w.cuda())
+    out = torch.zeros((5, 4, d), dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(5, dtype=torch.int32)
+    A.pkv_qk_norm_rope(args, 5, dirty.cuda(), None, pos.cuda(), out, None)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[2, 1]).any()
+    out[2, 1] = 0
+    o, size = _expect(K8_values(q), K8_values(w), table.double().numpy(), pos.tolist(), d,
+                      float(np.float32(1e-6)), False)
+    o[2, 1] = size[2, 1] = 0
+    _check(out, (o, size), d)
+
+
 def test_rows_behind_the_last_token_are_left(cuda):
     d = 128
     args = QkNormRope(n_q_heads=4, n_kv_heads=1, head_dim=d, cos_sin=rope_table(64, d))
