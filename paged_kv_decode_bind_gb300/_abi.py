@@ -174,10 +174,11 @@ def _current_stream():
     if _current is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        dev = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         if not torch.cuda.is_available():
             _current = lambda: None  # noqa: E731
         elif raw is not None:
-            dev = torch.cuda.current_device
+            torch.cuda.init()
             _current = lambda: raw(dev())  # noqa: E731
         else:
             _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
@@ -193,10 +194,7 @@ def _stream(s):
 
 
 def _ws(ws):
-    if ws is None:
-        return None
-    st = ws.struct if hasattr(ws, "struct") else ws
-    return ctypes.byref(st)
+    return getattr(ws, "struct", ws)  # passed by reference (see the argtypes)
 
 
 def _check(fn, status):
@@ -358,9 +356,9 @@ def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None,
     """RMS norm and rotation of every head of q and k into q_out and k_out
     (args: a QkNormRope or a PkvQkNormRopeArgs); q and k may be slices of one
     projection's rows."""
-    st = args.struct if hasattr(args, "struct") else args
-    D = st.head_dim
-    qw, kw = st.n_q_heads * D, st.n_kv_heads * D
+    st = getattr(args, "struct", args)
+    D, qw, kw = getattr(args, "widths", None) or \
+        (st.head_dim, st.n_q_heads * st.head_dim, st.n_kv_heads * st.head_dim)
     s = load().pkv_qk_norm_rope(st, n_tokens, *_heads(q, qw, D), *_heads(k, kw, D),
                                 _ptr(positions), *_heads(q_out, qw, D), *_heads(k_out, kw, D),
                                 _stream(stream))

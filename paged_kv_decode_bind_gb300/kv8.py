@@ -131,6 +131,7 @@ class QkNormRope:
         device = next((x.device for x in (cos_sin, q_weight, k_weight) if x is not None), "cuda")
         self.err = torch.zeros(1, dtype=torch.int32, device=device) if err is None else err
         self.cos_sin, self.q_weight, self.k_weight = cos_sin, q_weight, k_weight
+        self.widths = (head_dim, n_q_heads * head_dim, n_kv_heads * head_dim)  # of a token's rows
         self.struct = _abi.PkvQkNormRopeArgs(
             n_q_heads=n_q_heads, n_kv_heads=n_kv_heads, head_dim=head_dim, rot_dim=rot_dim,
             max_positions=0 if not rot_dim else cos_sin.shape[0], interleaved=int(interleaved),
