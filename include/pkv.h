@@ -118,7 +118,7 @@ enum {
   PKV_DEVERR_TOTAL = 4,    /* flat mode: kv_indptr[b] + seq_len > max_total_tokens */
   PKV_DEVERR_SLOT = 8,     /* a flat slot or out_loc outside [0, pool_slots)    */
   PKV_DEVERR_TIMEOUT = 16, /* a bounded wait on an async copy ran out (~1 s)    */
-  PKV_DEVERR_POSITION = 32 /* pkv_qk_norm_rope: position < 0 or >= max_positions */
+  PKV_DEVERR_POSITION = 32 /* pkv_qk_norm_rope: position < -1 or >= max_positions */
 };
 
 /*
@@ -523,7 +523,7 @@ pkv_status pkv_kv8_extend_append(const pkv_workspace *ws, const pkv_kv8 *c, int 
  *               whose start is its length or more has no rows.
  *   dst_indptr  device int32 [batch]: each request's first row (of at least
  *               [batch] entries; rows of two requests must not overlap).
- *   n_rows      rows that k_out and v_out hold.
+ *   n_rows      rows that k_out and v_out hold (0: they may be NULL).
  *   k_out, v_out device bf16 [n_rows, Hkv, D] (fp32 with PKV_FLAG_OUT_F32),
  *               16-byte aligned; rows that no token maps to are left as they
  *               were.  A value is code * scale rounded once, which is exact for
@@ -541,7 +541,7 @@ pkv_status pkv_kv8_read(const pkv_workspace *ws, const pkv_kv8 *c, int batch, in
  * One layer of a decode step on the 8-bit cache: the append (skipped when k_new
  * and v_new are both NULL), split-KV GQA decode attention and the split merge.
  * Arguments, workspace buffers and results are pkv_decode_layer's, with the
- * scores and values of the dequantised cache:
+ * scores and values of the dequantised cache (an empty request appends nothing):
  *   s_t = scale * k_scale_t * (q . code_k,t),  o = sum_t softmax(s)_t v_scale_t code_v,t.
  *   num_splits  S in [1, max_splits]; S > 1 needs o_part, ml_part and
  *               split_counters (zeroed once, left zeroed).
@@ -589,6 +589,8 @@ typedef struct pkv_qk_norm_rope_args {
  *               may be parts of one projection's rows).
  *   positions   device int32 [n_tokens] (ws->position_ids in a decode step).
  *   q_out, k_out as q and k; may be q and k themselves with the same strides.
+ * A token at position -1 (pkv_bind_step's for an empty request) is written as
+ * zeros (rot_dim > 0).
  * Device errors: PKV_DEVERR_POSITION (the token's heads are written as zeros).
  * Host errors: PKV_ERR_INVALID (null or misaligned pointer, bad size or
  * stride), PKV_ERR_UNSUPPORTED (head_dim, rot_dim).

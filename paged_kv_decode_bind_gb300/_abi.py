@@ -347,9 +347,11 @@ def _heads(x, width, head_dim):
     if x is None or isinstance(x, int):
         return x, width
     st = x.stride()
-    if st[-1] != 1 or len(st) not in (2, 3) or (len(st) == 3 and st[1] != head_dim):
+    if len(st) not in (2, 3) or st[-1] != 1 or \
+            (len(st) == 3 and st[1] != head_dim and x.shape[1] > 1):
         raise ValueError("heads must be dense: [tokens, width] or [tokens, heads, head_dim]")
-    return x.data_ptr(), st[0]
+    # the stride of a single token may be anything
+    return x.data_ptr(), width if st[0] < width and x.shape[0] <= 1 else st[0]
 
 
 def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None, check=True):

@@ -43,10 +43,12 @@ bool decode_mma_supported(int head_dim, int group);
 // 8-bit cache (kv8_cache.cu, kv8_decode.cu).
 struct Kv8Args;
 // early: the next kernel on the stream may start before this one's predecessor
-// has ended (it was launched to wait for this kernel where it must).
+// has ended (it was launched to wait for this kernel where it must).  lens:
+// requests without a usable length are passed over; NULL: every entry has a row.
 cudaError_t launch_kv8_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,
                               int layer_begin, int layer_count, const void *k_new,
-                              const void *v_new, bool early, cudaStream_t st);
+                              const void *v_new, bool early, const int *lens,
+                              cudaStream_t st);
 cudaError_t launch_kv8_extend_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,
                                      int layer, const int *qo_indptr, int max_qo_len,
                                      const void *k_new, const void *v_new, cudaStream_t st);

@@ -70,14 +70,15 @@ constexpr int kKAThreads = 256;
 template <int D, int DT>
 __global__ void __launch_bounds__(kKAThreads)
     kv8_append_kernel(const __grid_constant__ pkv_workspace ws, const __grid_constant__ pkv_kv8 c,
-                      int batch, int layer_begin, bool early, const uint4 *__restrict__ k_new,
-                      const uint4 *__restrict__ v_new) {
+                      int batch, int layer_begin, bool early, const int *__restrict__ lens,
+                      const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new) {
   if (early) pdl_trigger();  // the next kernel itself waits for what it must
   pdl_wait();
   if (!early) pdl_trigger();
   constexpr int LPR = D / 8;
   const int b = blockIdx.x, rel = blockIdx.y, layer = layer_begin + rel;
-  const int loc = ws.out_loc[b];
+  const int loc = ws.out_loc[b], L = lens ? lens[b] : 1;
+  if (L <= 0 || (long long)L > len_cap(ws)) return;  // no newest token, as in attention
   if (loc < 0 || loc >= ws.pool_slots) {
     if (threadIdx.x == 0) atomicOr(ws.err, PKV_DEVERR_SLOT);
     return;
@@ -428,11 +429,12 @@ struct AppendLaunch {
   int batch, layer_begin, layer_count;
   const void *k, *v;
   bool early;
+  const int *lens;
   cudaStream_t st;
   template <int D, int DT>
   cudaError_t operator()() {
     return launch_pdl(kv8_append_kernel<D, DT>, dim3(batch, layer_count), dim3(kKAThreads), 0, st,
-                      ws, c, batch, layer_begin, early, static_cast<const uint4 *>(k),
+                      ws, c, batch, layer_begin, early, lens, static_cast<const uint4 *>(k),
                       static_cast<const uint4 *>(v));
   }
 };
@@ -489,9 +491,10 @@ struct ReadLaunch {
 
 cudaError_t launch_kv8_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,
                               int layer_begin, int layer_count, const void *k_new,
-                              const void *v_new, bool early, cudaStream_t st) {
-  return by_shape(ws, c,
-                  AppendLaunch{ws, c, batch, layer_begin, layer_count, k_new, v_new, early, st});
+                              const void *v_new, bool early, const int *lens,
+                              cudaStream_t st) {
+  return by_shape(ws, c, AppendLaunch{ws, c, batch, layer_begin, layer_count, k_new, v_new, early,
+                                      lens, st});
 }
 
 cudaError_t launch_kv8_extend_append(const pkv_workspace &ws, const pkv_kv8 &c, int batch,

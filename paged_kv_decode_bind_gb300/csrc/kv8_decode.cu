@@ -923,17 +923,14 @@ using TmapEncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 // 3-D view of a code pool [NL * pool_slots, Hkv, D] as (byte, slot, head): a
 // box of D x 16 x 1 is one 16-token piece of one head.
 bool encode_codes_map(CUtensorMap *m, void *base, const pkv_workspace &ws) {
-  static TmapEncodeFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+  static const TmapEncodeFn fn = [] {  // looked up once, whichever thread is first
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<TmapEncodeFn>(p);
-  }
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                     cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<TmapEncodeFn>(p) : nullptr;
+  }();
   if (!fn) return false;
   const cuuint64_t D = (cuuint64_t)ws.head_dim, H = (cuuint64_t)ws.n_kv_heads;
   const cuuint64_t dims[3] = {D, (cuuint64_t)ws.n_layers * (cuuint64_t)ws.pool_slots, H};
@@ -1010,7 +1007,7 @@ cudaError_t launch_kv8_decode(const Kv8Args &args, cudaStream_t st) {
     // before the append still runs: it plans and loads everything but the block
     // appended to, and waits for the append (which waits for the rest) there.
     const cudaError_t e = launch_kv8_append(a.ws, a.c, a.batch, a.layer, 1, a.k_new, a.v_new,
-                                            (a.flags & PKV_FLAG_PLAN_EARLY) != 0, st);
+                                            (a.flags & PKV_FLAG_PLAN_EARLY) != 0, a.ws.seq_lens, st);
     if (e != cudaSuccess) return e;
   }
   const int D = a.ws.head_dim, G = a.ws.n_q_heads / a.ws.n_kv_heads;

@@ -390,7 +390,7 @@ pkv_status pkv_kv8_append(const pkv_workspace *ws, const pkv_kv8 *c, int batch, 
   if (batch == 0 || layer_count == 0) return PKV_OK;
   if (!ws->out_loc || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))
     return PKV_ERR_INVALID;
-  return from_cuda(launch_kv8_append(*ws, *c, batch, layer_begin, layer_count, k_new, v_new, false,
+  return from_cuda(launch_kv8_append(*ws, *c, batch, layer_begin, layer_count, k_new, v_new, false, nullptr,
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -417,7 +417,8 @@ pkv_status pkv_kv8_read(const pkv_workspace *ws, const pkv_kv8 *c, int batch, in
   if ((st = check_index(ws)) != PKV_OK) return st;
   if (batch < 0 || layer < 0 || n_rows < 0 || (flags & ~PKV_FLAG_OUT_F32)) return PKV_ERR_INVALID;
   if (batch > ws->max_batch || layer >= ws->n_layers) return PKV_ERR_CAPACITY;
-  if (!dst_indptr || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+  // no rows, no buffers: a request that has some raises PKV_DEVERR_TOTAL
+  if (!dst_indptr || (n_rows > 0 && (!k_out || !v_out)) || !aligned16(k_out) || !aligned16(v_out))
     return PKV_ERR_INVALID;
   if (batch == 0) return PKV_OK;
   return from_cuda(launch_kv8_read(*ws, *c, batch, layer, starts, dst_indptr, n_rows, k_out, v_out,
@@ -464,7 +465,9 @@ pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, con
   if (rot < 0 || rot > D || rot % 16 != 0) return PKV_ERR_UNSUPPORTED;
   if (!aligned16(args->q_weight) || !aligned16(args->k_weight) || !aligned16(args->cos_sin))
     return PKV_ERR_INVALID;
-  if (rot > 0 && (!args->cos_sin || !positions)) return PKV_ERR_INVALID;
+  if (rot > 0 && !args->cos_sin) return PKV_ERR_INVALID;
+  if (n_tokens == 0) return PKV_OK;  // the tensors may be empty
+  if (rot > 0 && !positions) return PKV_ERR_INVALID;
   const int64_t qw = (int64_t)args->n_q_heads * D, kw = (int64_t)args->n_kv_heads * D;
   if (!q || !q_out || !aligned16(q) || !aligned16(q_out) || q_stride % 8 || q_out_stride % 8 ||
       q_stride < qw || q_out_stride < qw)
@@ -472,7 +475,6 @@ pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, con
   if (kw > 0 && (!k || !k_out || !aligned16(k) || !aligned16(k_out) || k_stride % 8 ||
                  k_out_stride % 8 || k_stride < kw || k_out_stride < kw))
     return PKV_ERR_INVALID;
-  if (n_tokens == 0) return PKV_OK;
   return from_cuda(launch_qk_norm_rope(*args, n_tokens, q, q_stride, k, k_stride, positions, q_out,
                                        q_out_stride, k_out, k_out_stride,
                                        reinterpret_cast<cudaStream_t>(stream)));

@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kRWarps * 32) qk_norm_rope_kernel(const __grid
   if (rot > 0) {
     const int pos = a.positions[tok];
     bad = pos < 0 || pos >= p.max_positions;
-    if (bad && part == 0 && lane == 0) atomicOr(p.err, PKV_DEVERR_POSITION);
+    // -1 is an empty request of a padded batch
+    if (bad && pos != -1 && part == 0 && lane == 0) atomicOr(p.err, PKV_DEVERR_POSITION);
     if (turns && !bad) {
       const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (long long)pos * rot);
       *reinterpret_cast<float4 *>(cs) = row[2 * l];

@@ -19,8 +19,9 @@ class Kv8Cache:
     """Codes [NL, slots, Hkv, D] and scales [NL, slots / P, Hkv, P / scale_block].
 
     Existing uint8 and fp32 tensors of those shapes may be given (for example
-    a cache that was saved); new ones start as zeros.  A workspace built with
-    ``pools=False`` has no bf16 pools to pay for."""
+    a cache that was saved); new ones start as zeros under the
+    smallest scale, so that rows never written count as zeros.  A workspace built
+    with ``pools=False`` has no bf16 pools to pay for."""
 
     def __init__(self, ws, *, dtype="e4m3", scale_block=None, k_pool=None, v_pool=None,
                  k_scale=None, v_scale=None):
@@ -32,14 +33,16 @@ class Kv8Cache:
             scale_block = next(b for b in (16, 8, 4, 2, 1) if P % b == 0)
         if not 1 <= scale_block <= 128 or P % scale_block:
             raise ValueError("scale_block is 1 .. 128 and divides the page size")
+        home = torch.empty(0, device=ws.device).device  # "cuda" with its index
         codes = (sh["n_layers"], sh["pool_slots"], H, D)
         scales = (sh["n_layers"], sh["pool_slots"] // P, H, P // scale_block)
 
         def own(x, shape, dt):
             if x is None:
-                return torch.zeros(shape, dtype=dt, device=ws.device)
+                return torch.full(shape, 2.0 ** -100 if dt.is_floating_point else 0, dtype=dt,
+                                  device=ws.device)
             if tuple(x.shape) != shape or x.dtype != dt or not x.is_contiguous() or \
-                    x.device.type != ws.device.type:
+                    x.device != home:
                 raise ValueError(f"expected a dense {dt} tensor of {shape} on {ws.device}")
             return x
 
@@ -59,7 +62,8 @@ class Kv8Extender:
     tenth of the attention's time for chunks of 256 tokens on 512 to 2048.
 
     Contexts hold at most max_context tokens (longer ones raise PKV_DEVERR_LEN),
-    chunks at most max_new.  Every buffer is allocated here once."""
+    chunks at most max_new.  Every buffer is allocated here once, so calls of one
+    extender run one after the other (on one stream, or ordered by the caller)."""
 
     def __init__(self, ws, cache, batch, *, max_new, max_context, scale, num_splits=1):
         sh = ws.shape

@@ -681,6 +681,119 @@ def test_early_start_with_append(cuda, page, block):
     assert int(ws.err.item()) == 0
 
 
+@pytest.mark.parametrize("page,block", [(64, 16), (16, 16), (16, 2), (12, 4), (1, 1)])
+def test_early_start_behind_a_long_layer(cuda, page, block):
+    # a graph of layers in which request 0 keeps the previous layer running while
+    # the next one's blocks already load the short requests' older blocks, whose
+    # scales lie in the same sectors as the one that the append is about to change
+    lens, layers, steps = [20000, 47, 30, 250], 3, 3
+    p = W.make_problem(batch=4, n_layers=layers, n_q_heads=8, n_kv_heads=2, head_dim=128,
+                       page_size=page, seq_lens=lens, steps=steps, seed=11, pool_factor=1.1)
+    got = []
+    for flag in (0, A.PKV_FLAG_PLAN_EARLY):
+        from paged_kv_decode_bind_gb300 import Kv8Cache, Workspace
+        ws = Workspace(n_layers=layers, pool_slots=p.pool_slots, n_q_heads=8, n_kv_heads=2,
+                       head_dim=128, page_size=page, max_batch=4, max_reqs=p.max_reqs,
+                       max_pages_per_req=p.max_pages_per_req, max_splits=64,
+                       max_total_tokens=4 * p.max_pages_per_req if page == 1 else 0,
+                       index_mode=p.index_mode, pools=False)
+        ws.page_table.copy_(p.page_table)
+        ws.req_pool_indices[:4].copy_(p.req_pool_indices)
+        ws.seq_lens[:4].copy_(p.seq_lens)
+        g = torch.Generator(device="cuda").manual_seed(3)
+        shape = (layers, p.pool_slots, 2, 128)
+        pool = lambda: torch.randint(0, 120, shape, generator=g, dtype=torch.uint8,  # noqa: E731
+                                     device="cuda")
+        cache = Kv8Cache(ws, scale_block=block, k_pool=pool(), v_pool=pool())
+        cache.k_scale.fill_(2.0 ** -9), cache.v_scale.fill_(2.0 ** -9)
+        q, k, v = (torch.zeros_like(x.cuda()) for x in W.step_inputs(p, 0))
+        outs = [torch.zeros((4, 8, 128), dtype=torch.bfloat16, device="cuda")
+                for _ in range(layers)]
+
+        def step():
+            A.pkv_bind_step(ws, 4, A.PKV_BIND_STEADY)
+            for l in range(layers):
+                view = A.PkvWorkspace.from_buffer_copy(ws.struct)
+                view.out = outs[l].data_ptr()
+                A.pkv_kv8_decode_layer(view, cache, 4, l, q[l], k[l], v[l], p.scale, 64,
+                                       flag if l else 0)
+
+        graph = torch.cuda.CUDAGraph()
+        ws.seq_lens[:4] -= 1  # the call that loads the kernels appends nothing that stays
+        keep = [t.clone() for t in (cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale)]
+        step()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            step()
+        for t, was in zip((cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale), keep):
+            t.copy_(was)
+        ws.seq_lens[:4].copy_(p.seq_lens)
+        run = []
+        for i in range(steps):
+            for dst, src in zip((q, k, v), W.step_inputs(p, i)):
+                dst.copy_(src)
+            k.mul_(4.0 ** (i + 1))  # every step's rows make their block grow
+            v.mul_(4.0 ** (i + 1))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            run += [x.clone() for x in outs]
+        run += [cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale]
+        got.append(run)
+        assert int(ws.err.item()) == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("S", [1, 3])
+def test_padded_batch_raises_nothing(cuda, S):
+    # empty requests beside others: no row, no error, zeros
+    lens = [0, 39, 0, 130]
+    prob = _problem(lens, layers=1, steps=1)
+    ws, cache = prob.device(max_splits=S)
+    q, k, v = W.step_inputs(prob.p, 0)
+    for b in (1, 3):  # position lens - 1 again: the row of the newest token
+        s = prob.slots(b, lens[b] - 1, lens[b])
+        prob.k.append(0, s, K8_values(k[0, b:b + 1]))
+        prob.v.append(0, s, K8_values(v[0, b:b + 1]))
+    got = _attend(prob, ws, cache, q[0].cuda(), S, lens, new=(k[0].cuda(), v[0].cuda()))
+    assert (got[[0, 2]] == 0).all()
+    _same(cache, prob)
+    # the append on its own has a row for every entry
+    A.pkv_kv8_append(ws, cache, 4, 0, 1, k.cuda(), v.cuda())
+    assert int(ws.err.item()) == A.PKV_DEVERR_SLOT
+
+
+def test_rows_never_written_count_as_zeros(cuda):
+    # a new cache under lengths that nothing wrote (a program's first, empty run)
+    from paged_kv_decode_bind_gb300 import Kv8Cache
+    prob = _problem([5, 70, 333])
+    ws, _ = prob.device(max_splits=2)
+    q, k, v = (x.cuda() for x in W.step_inputs(_problem([5, 70, 333], steps=1).p, 0))
+    for dtype in ("e4m3", "int8"):
+        cache = Kv8Cache(ws, dtype=dtype)
+        A.pkv_kv8_decode_layer(ws, cache, 3, 0, q[0], None, None, 0.1, 2, A.PKV_FLAG_WRITE_LSE)
+        assert torch.all(ws.out_bf16(3) == 0)
+        n = torch.tensor([5.0, 70.0, 333.0], device="cuda").log()[:, None]
+        assert (ws.lse[:3] - n).abs().max() <= 1e-4  # log n; its terms of 74 .. 80 are in steps of 2^-17
+        # one row written: the others weigh in as zeros
+        A.pkv_kv8_decode_layer(ws, cache, 3, 0, q[0], k[0], v[0], 0.1, 2)
+        assert torch.all(torch.isfinite(ws.out_bf16(3))) and int(ws.err.item()) == 0
+
+
+def test_read_of_no_rows(cuda):
+    prob = _problem([0, 20])
+    ws, cache = prob.device()
+    dst = torch.zeros(2, dtype=torch.int32, device="cuda")
+    A.pkv_kv8_read(ws, cache, 1, 0, None, dst, 0, None, None)
+    assert int(ws.err.item()) == 0
+    starts = torch.full((2,), 20, dtype=torch.int32, device="cuda")
+    A.pkv_kv8_read(ws, cache, 2, 0, starts, dst, 0, None, None)
+    assert int(ws.err.item()) == 0
+    A.pkv_kv8_read(ws, cache, 2, 0, None, dst, 0, None, None)  # 20 rows, room for none
+    assert int(ws.err.item()) == A.PKV_DEVERR_TOTAL
+
+
 def test_append_bad_slot(cuda):
     prob = _problem([20, 30, 40])
     ws, cache = prob.device()

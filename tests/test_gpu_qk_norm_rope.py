@@ -139,6 +139,17 @@ def test_strided_output_and_bad_positions(cuda):
            _expect(K8_values(k[good]), K8_values(args.k_weight.cpu()), tab, p, 32, eps, False), d)
 
 
+def test_an_empty_request_is_no_error(cuda):
+    d, pos = 128, torch.tensor([4, -1, 0], dtype=torch.int32)
+    q, k = _bf16((3, 4, d), 21).cuda(), _bf16((3, 2, d), 22).cuda()
+    args = QkNormRope(n_q_heads=4, n_kv_heads=2, head_dim=d, cos_sin=rope_table(5, d))
+    A.pkv_qk_norm_rope(args, 3, q, k, pos.cuda(), q, k)
+    assert int(args.err.item()) == 0
+    assert torch.all(q[1] == 0) and torch.all(k[1] == 0) and q[0].any() and k[2].any()
+    A.pkv_qk_norm_rope(args, 3, q, k, (pos - 1).cuda(), q, k)
+    assert int(args.err.item()) == A.PKV_DEVERR_POSITION
+
+
 def test_norm_alone_needs_no_positions(cuda):
     d = 128
     q, w = _bf16((4, 3, d), 15), _bf16((d,), 16)

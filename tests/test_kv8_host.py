@@ -198,6 +198,25 @@ def test_rope_strides_come_from_the_tensors():
         A._heads(x.view(3, 8, 128).transpose(0, 1), 1024, 128)
 
 
+def test_rope_strides_of_one_head_or_token():
+    x = torch.zeros((6, 4, 64), dtype=torch.bfloat16)
+    one = x[:, :1].transpose(0, 1)[:1]  # [1, 6, 64]: dense heads are 256 apart
+    with pytest.raises(ValueError):
+        A._heads(one, 384, 64)
+    assert A._heads(torch.as_strided(x, (3, 1, 64), (256, 7, 1)), 64, 64)[1] == 256
+    assert A._heads(torch.as_strided(x, (1, 256), (1, 1)), 256, 64)[1] == 256
+    assert A._heads(torch.as_strided(x, (2, 256), (8, 1)), 256, 64)[1] == 8  # the call refuses it
+
+
+def test_empty_calls_need_no_buffers():
+    kw = dict(stream=0, check=False)
+    assert P.pkv_kv8_append(_ws(), _c(), 0, 0, 1, None, None, **kw) == P.PKV_OK
+    assert P.pkv_kv8_read(_ws(), _c(), 0, 0, None, F, 0, None, None, **kw) == P.PKV_OK
+    assert P.pkv_kv8_read(_ws(), _c(), 1, 0, None, F, 1, None, None, **kw) == P.PKV_ERR_INVALID
+    e = torch.zeros((0, 4, 128), dtype=torch.bfloat16)
+    assert P.pkv_qk_norm_rope(_rope(), 0, e, e[:, :2], None, e, e[:, :2], **kw) == P.PKV_OK
+
+
 def _cpu_ws(page=16):
     return Workspace(n_layers=2, pool_slots=4 * page, n_q_heads=4, n_kv_heads=2, head_dim=64,
                      page_size=page, max_batch=2, max_reqs=2, max_pages_per_req=2,
@@ -216,8 +235,9 @@ def test_cache_owner():
     assert Kv8Cache(_cpu_ws(1)).scale_block == 1 and Kv8Cache(_cpu_ws(24)).scale_block == 8
     keep = torch.zeros((2, 64, 2, 64), dtype=torch.uint8)
     assert Kv8Cache(ws, k_pool=keep).k_pool is keep
+    assert not c.k_pool.any() and torch.all(c.v_scale == 2.0 ** -100)
     for kw in (dict(dtype="fp4"), dict(scale_block=3), dict(scale_block=0), dict(scale_block=32),
-               dict(k_pool=keep.float()), dict(v_pool=keep[:1]),
+               dict(k_pool=keep.float()), dict(v_pool=keep[:1]), dict(v_pool=keep.to("meta")),
                dict(k_pool=keep.transpose(0, 1).contiguous().transpose(0, 1))):
         with pytest.raises(ValueError):
             Kv8Cache(ws, **kw)
