@@ -160,8 +160,7 @@ struct KUnit {
 
 // A block's units in order.
 //
-// Shared out (S > 1, batches of up to kMaxCompactBatch): the requests, one
-// after the other, make a line of 16-token pieces.  The blocks form groups of
+// Shared out (S > 1): the requests, one after the other, make a line of 16-token pieces.  The blocks form groups of
 // Hkv, one block per KV head, and each group takes a run of q pieces, so every
 // block has the same number whatever the lengths are; a run that crosses the
 // end of a request becomes two units.  The heads of a token lie side by side in
@@ -171,13 +170,25 @@ struct KUnit {
 // spends on starting and finishing a unit (2 us against 0.2 us for a piece).
 // q = ceil(line / groups), at least 8 (one piece per warp) and at least
 // ceil(longest request / (S - 1)), so that none lies in more than S runs.
-// Whole pairs (S == 1), or fixed chunks (larger batches): unit u = (split,
-// request, head), every gridDim.x-th one from blockIdx.x.
+// A block keeps the line of up to kMaxCompactBatch requests in shared memory.
+// Of more it keeps where each thread's few requests start, and walks on from
+// there (300 requests of 100-900 tokens 30 us, against 49 with fixed chunks;
+// tables for 1024 requests would cost the gathering form its L1: 16 flat
+// contexts 20.6 us, against 19.0).
+// Whole pairs (S == 1), or fixed chunks (fewer blocks than heads): unit u =
+// (split, request, head), every gridDim.x-th one from blockIdx.x.
 constexpr int kUnitCost = 14;
 
 struct KUnits {
   int q, pos, end, b, chunk;  // pos, end: of the line, or unit numbers
+  int at;                     // where request b starts (batches past the tables)
+  int group, head;            // the block's, where shared out
 };
+
+// Pieces of a request in the line.
+__device__ __forceinline__ int line_pieces(int len) {
+  return len > 0 ? kUnitCost + ((len + 15) >> 4) : 0;
+}
 
 // PAGED: pages hold whole 16-token pieces, loaded as TMA boxes.
 template <int D, int G, int DT, bool PAGED>
@@ -229,6 +240,29 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   Plan pl;
   pl.set_pages(ws);
   const bool compact = a.batch <= kMaxCompactBatch;
+  // a block's run of a line of `run` pieces, the longest request having `most`
+  auto share = [&](int run, int most) {
+    const int groups = (int)gridDim.x / H, group = (int)blockIdx.x / H;
+    KUnits us;
+    us.group = group;
+    us.head = (int)blockIdx.x - group * H;
+    us.q = max(max((run + groups - 1) / groups, 8),
+               (most - kUnitCost + a.num_splits - 2) / (a.num_splits - 1));
+    const long long first = group < groups ? (long long)group * us.q : run;
+    us.pos = (int)min(first, (long long)run);
+    us.end = (int)min(first + us.q, (long long)run);
+    return us;
+  };
+  // the last of n entries of s_pref that is not past pos
+  auto find = [&](int n, int pos) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_pref[mid] <= pos) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
   if (compact) {
     if (warp == 0) {
       // lane i holds requests i, i + 32, ...: all loads in flight at once
@@ -256,7 +290,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
           if (blockIdx.x == 0) atomicOr(ws.err, err);
           len[i] = 0;
         }
-        const int pcs = len[i] > 0 ? kUnitCost + ((len[i] + 15) >> 4) : 0;
+        const int pcs = line_pieces(len[i]);
         most = max(most, pcs);
         int incl = pcs;
 #pragma unroll
@@ -275,22 +309,43 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       if (lane == 0) s_pref[a.batch] = run;
       __syncwarp();
       if (lane == 0 && a.apportion) {
-        const int groups = (int)gridDim.x / H, group = (int)blockIdx.x / H;
-        KUnits us;
-        us.q = max(max((run + groups - 1) / groups, 8),
-                   (most - kUnitCost + a.num_splits - 2) / (a.num_splits - 1));
-        const long long first = group < groups ? (long long)group * us.q : run;
-        us.pos = (int)min(first, (long long)run);
-        us.end = (int)min(first + us.q, (long long)run);
-        us.b = 0;
-        int hi = a.batch - 1;  // last b with pref[b] <= pos
-        while (us.b < hi) {
-          const int mid = (us.b + hi + 1) >> 1;
-          if (s_pref[mid] <= us.pos) us.b = mid;
-          else hi = mid - 1;
-        }
+        KUnits us = share(run, most);
+        us.b = find(a.batch, us.pos);
         s_us = us;
       }
+    }
+  } else if (a.apportion) {
+    // thread t adds up requests t per .. t per + per - 1
+    const int per = (a.batch + C::THREADS - 1) / C::THREADS;
+    int sum = 0, most = 0;
+    for (int b = tid * per; b < min((tid + 1) * per, a.batch); ++b) {
+      const int pcs = line_pieces(blockIdx.x == 0 ? checked_len(ws, b, ws.err) : usable_len(ws, b));
+      sum += pcs;
+      most = max(most, pcs);
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) s_slot[warp] = incl;
+    if (lane == 0) s_bad[warp] = most;
+    __syncthreads();
+    int run = 0;
+    for (int w = 0; w < W; ++w) {
+      if (w == warp) s_pref[tid] = run + incl - sum;
+      run += s_slot[w];
+      most = max(most, s_bad[w]);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      KUnits us = share(run, most);
+      const int t = find(C::THREADS, us.pos);
+      us.b = t * per;
+      us.at = s_pref[t];
+      s_us = us;
     }
   }
   if (!a.apportion) {
@@ -307,6 +362,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     }
   }
 
+  const int SB = a.c.scale_block, per_page = ws.page_size / SB;
   // The next unit into *dst by thread 0 (t0 == t1: past the last one).
   auto next_unit = [&](KUnit *dst) {
     KUnits us = s_us;
@@ -318,20 +374,35 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       ReqIndex ri;
       int L;
       if (a.apportion) {
-        while (s_pref[us.b + 1] <= us.pos) ++us.b;
-        const int real = s_pref[us.b] + kUnitCost, last = s_pref[us.b + 1];  // its pieces
+        int start, last;  // the request's pieces in the line
+        if (compact) {
+          while (s_pref[us.b + 1] <= us.pos) ++us.b;
+          start = s_pref[us.b], last = s_pref[us.b + 1];
+          L = s_len[us.b];
+        } else {
+          for (;; ++us.b) {
+            L = us.b < a.batch ? usable_len(ws, us.b) : 0;
+            start = us.at, last = start + line_pieces(L);
+            if (last > us.pos || us.b >= a.batch) break;
+            us.at = last;
+          }
+          if (last <= us.pos) {  // lengths that changed since they were added up
+            us.pos = us.end;
+            continue;
+          }
+        }
+        const int real = start + kUnitCost;
         const int from = max(us.pos, real), stop = min(us.end, last);
         us.pos = stop;
         if (from >= stop) continue;  // the run ends in what the request counts in front
         const int first = real / us.q;
         u.b = us.b;
-        u.g = (int)blockIdx.x % H;
-        u.c = (int)blockIdx.x / H - first;
+        u.g = us.head;
+        u.c = us.group - first;
         u.n = (last - 1) / us.q - first + 1;
         u.t0 = 16 * (from - real);
-        L = s_len[us.b];
         u.t1 = min(16 * (stop - real), L);
-        ri = req_index_cached(ws, s_base, us.b);
+        ri = compact ? req_index_cached(ws, s_base, us.b) : req_index(ws, us.b);
       } else {
         const int hb = a.batch * H;
         u.c = us.pos / hb;
@@ -351,8 +422,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       }
       u.base = ri.base;
       u.bad = ri.ok ? 0 : PKV_DEVERR_PAGE;
-      u.srow = ((long long)a.layer * pl.n_pages * H + u.g) * (ws.page_size / a.c.scale_block);
-      if (a.k_new) u.fresh = (L - 1) / a.c.scale_block * a.c.scale_block;
+      u.srow = ((long long)a.layer * pl.n_pages * H + u.g) * per_page;
+      if (a.k_new) u.fresh = (L - 1) / SB * SB;
       u.row0 = ((long long)a.layer * ws.pool_slots * H + u.g) * D;
       s_us = us;
       *dst = u;
@@ -363,8 +434,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     *dst = u;
   };
   if (tid == 0) {  // in warp 0, which has the arrays
-    next_unit(&s_unit[0]);
-    next_unit(&s_unit[1]);
+#pragma unroll 1  // one copy of the code: the second pass has it at hand
+    for (int i = 0; i < 2; ++i) next_unit(&s_unit[i]);
   }
   __syncthreads();
   // Requests with no usable token have no unit: zero their outputs here.
@@ -382,7 +453,6 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
 
   uint8_t *const wring = smem + warp * (NS * C::STAGE);
   const uint32_t ring = smem_addr(wring);
-  const int SB = a.c.scale_block, per_page = ws.page_size / SB;
   const int sshift = (SB & (SB - 1)) == 0 ? __ffs(SB) - 1 : -1;
   const int page_row = H * per_page;  // scales of a page
   const int rs = H * D;               // bytes between the rows of consecutive slots
@@ -968,9 +1038,9 @@ cudaError_t launch_one(Kv8Args a, const CUtensorMap &tmk, const CUtensorMap &tmv
   const long long units = (long long)a.num_splits * a.batch * ws.n_kv_heads;
   const long long cap = (long long)sms_cache[di] * occ_cache[di];
   const int grid = (int)(units < cap ? units : cap);
-  // sharing out by length needs the compact plan, a block per head and a line
-  // whose length fits an int
-  a.apportion = a.num_splits > 1 && a.batch <= kMaxCompactBatch && grid >= ws.n_kv_heads &&
+  // sharing out by length needs a block per head and a line whose length fits
+  // an int
+  a.apportion = a.num_splits > 1 && grid >= ws.n_kv_heads &&
                 (long long)a.batch * (len_cap(ws) / 16 + 1 + kUnitCost) < 0x7fffffffll;
   return launch_pdl(kern, dim3(grid), dim3(C::THREADS), (size_t)C::SMEM, st, a, tmk, tmv);
 }

@@ -226,10 +226,11 @@ def test_attention_splits_long(cuda, S):
     _attend(prob, ws, cache, q, S, lens, A.PKV_FLAG_OUT_F32, what=f"S={S}")
 
 
-@pytest.mark.parametrize("B", [33, 200, 257, 300])
+@pytest.mark.parametrize("B", [33, 200, 257, 300, 1025])
 def test_attention_batches(cuda, B):
-    # past 32 and 256 requests the split plan is made another way
-    lens = [(37 * i) % 90 for i in range(B)]
+    # past 32 and past 256 requests the split plan is made another way
+    lens = [(37 * i) % 90 if i % 7 else 0 for i in range(B)]
+    lens[-1] = 0
     prob = _problem(lens, "int8", heads=(2, 1), d=64)
     ws, cache = prob.device(max_splits=2)
     q = W.normal_bf16((B, 2, 64), 14).cuda()
