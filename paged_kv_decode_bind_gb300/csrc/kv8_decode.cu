@@ -588,10 +588,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
         // position p covers what was fetched with them.  The first pieces of
         // a block, and those of a unit that follows very short ones, are
         // known too late for that and wait here.
-        if (done_idx <= done_kv) {
-          const int to = min(done_kv + NS, np + nn);
-          for (; done_idx < to; ++done_idx) copy_idx(done_idx);
-        }
+        const int to = min(done_kv + NS + 1, np + nn);
+        for (; done_idx < to; ++done_idx) copy_idx(done_idx);
         if (landed_idx <= done_kv) {
           asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
@@ -599,11 +597,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
         }
       }
       copy_kv(done_kv);
-      if constexpr (!PAGED) {
-        const int to = min(done_kv + NS + 1, np + nn);
-        for (; done_idx < to; ++done_idx) copy_idx(done_idx);
+      if constexpr (!PAGED)
         if (lane == 0) s_seen[warp][st_in] = base_pos + done_idx;
-      }
       asm volatile("cp.async.commit_group;" ::: "memory");  // one group per position
       st_in = st_in + 1 == NS ? 0 : st_in + 1;
       ++done_kv;
