@@ -528,6 +528,9 @@ pkv_status pkv_kv8_extend_append(const pkv_workspace *ws, const pkv_kv8 *c, int 
  *               16-byte aligned; rows that no token maps to are left as they
  *               were.  A value is code * scale rounded once, which is exact for
  *               power-of-two scales.
+ *   flags       PKV_FLAG_OUT_F32; PKV_FLAG_PLAN_EARLY (lengths, starts, dst_indptr
+ *               and index entries are as old as that flag asks; codes, scales and
+ *               the outputs wait for the previous launch).
  * Device errors: PKV_DEVERR_LEN (a length out of range or a negative start),
  * PKV_DEVERR_TOTAL (rows outside [0, n_rows)): the request is skipped;
  * PKV_DEVERR_PAGE, _SLOT: the row is written as zeros.

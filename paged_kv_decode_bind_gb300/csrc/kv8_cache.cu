@@ -239,15 +239,17 @@ constexpr int kKRBatch = 256;  // requests whose tiles are laid out at a time
 template <int D, int DT, bool F32>
 __global__ void __launch_bounds__(kKRThreads)
     kv8_read_kernel(const __grid_constant__ pkv_workspace ws, const __grid_constant__ pkv_kv8 c,
-                    int batch, int layer, int tshift, const int *__restrict__ starts,
+                    int batch, int layer, int tshift, bool early, const int *__restrict__ starts,
                     const int *__restrict__ dst_indptr, int n_rows, uint8_t *k_out,
                     uint8_t *v_out) {
   __shared__ int s_pref[kKRBatch + 1], s_n[kKRBatch], s_start[kKRBatch], s_row[kKRBatch];
   __shared__ long long s_base[kKRBatch];  // its index entries; -1: no row of the table
   __shared__ int s_slot[2][kKRTokens];         // -1: a bad index entry
   __shared__ long long s_scale[2][kKRTokens];  // index of head 0's scale in the layer
-  pdl_wait();
-  pdl_trigger();
+  if (!early) {
+    pdl_wait();
+    pdl_trigger();
+  }
   const int tid = threadIdx.x, lane = tid & 31;
   const bool flat = ws.index_mode == PKV_IDX_FLAT;
   const int H = ws.n_kv_heads, W = H * (D / 16);  // 16-code words of a token's row
@@ -349,6 +351,10 @@ __global__ void __launch_bounds__(kKRThreads)
     };
     fetch(blockIdx.x);
     resolve(blockIdx.x, 0);
+    if (early && g0 == 0) {  // codes, scales and the output's last readers
+      pdl_wait();
+      pdl_trigger();
+    }
     int buf = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, buf ^= 1) {
       __syncthreads();  // this tile's slots; and the other buffer is free
@@ -477,13 +483,14 @@ struct ReadLaunch {
     // threads per row: the power of two that covers its 16-code words, 256 at most
     int tshift = 0;
     while (tshift < 8 && (1 << tshift) < ws.n_kv_heads * (D / 16)) ++tshift;
+    const bool early = (flags & PKV_FLAG_PLAN_EARLY) != 0;
     if (flags & PKV_FLAG_OUT_F32)
       return launch_pdl(kv8_read_kernel<D, DT, true>, dim3(grid), dim3(kKRThreads), 0, st, ws, c,
-                        batch, layer, tshift, starts, dst_indptr, n_rows,
+                        batch, layer, tshift, early, starts, dst_indptr, n_rows,
                         static_cast<uint8_t *>(k), static_cast<uint8_t *>(v));
     return launch_pdl(kv8_read_kernel<D, DT, false>, dim3(grid), dim3(kKRThreads), 0, st, ws, c,
-                      batch, layer, tshift, starts, dst_indptr, n_rows, static_cast<uint8_t *>(k),
-                      static_cast<uint8_t *>(v));
+                      batch, layer, tshift, early, starts, dst_indptr, n_rows,
+                      static_cast<uint8_t *>(k), static_cast<uint8_t *>(v));
   }
 };
 

@@ -415,7 +415,9 @@ pkv_status pkv_kv8_read(const pkv_workspace *ws, const pkv_kv8 *c, int batch, in
   pkv_status st = check_kv8(ws, c);
   if (st != PKV_OK) return st;
   if ((st = check_index(ws)) != PKV_OK) return st;
-  if (batch < 0 || layer < 0 || n_rows < 0 || (flags & ~PKV_FLAG_OUT_F32)) return PKV_ERR_INVALID;
+  if (batch < 0 || layer < 0 || n_rows < 0 ||
+      (flags & ~(PKV_FLAG_OUT_F32 | PKV_FLAG_PLAN_EARLY)))
+    return PKV_ERR_INVALID;
   if (batch > ws->max_batch || layer >= ws->n_layers) return PKV_ERR_CAPACITY;
   // no rows, no buffers: a request that has some raises PKV_DEVERR_TOTAL
   if (!dst_indptr || (n_rows > 0 && (!k_out || !v_out)) || !aligned16(k_out) || !aligned16(v_out))

@@ -110,7 +110,9 @@ class Kv8Extender:
         _abi.pkv_kv8_extend_append(self.read_view, self.cache, self.batch, layer, qo_indptr,
                                    max_qo_len, k_new, v_new, stream)
         _abi.pkv_kv8_read(self.read_view, self.cache, self.batch, layer, None, self.first_row,
-                          self.n_rows, self.k_rows, self.v_rows, 0, stream)
+                          self.n_rows, self.k_rows, self.v_rows,
+                          # the append, if there is one, is the previous launch
+                          _abi.PKV_FLAG_PLAN_EARLY if max_qo_len else 0, stream)
         _abi.pkv_extend_attn(self.rows_view, self.batch, 0, qo_indptr, max_qo_len, q, out,
                              self.scale, self.num_splits, flags & _abi.PKV_FLAG_OUT_F32, stream)
 

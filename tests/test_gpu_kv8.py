@@ -782,6 +782,41 @@ def test_rows_never_written_count_as_zeros(cuda):
         assert torch.all(torch.isfinite(ws.out_bf16(3))) and int(ws.err.item()) == 0
 
 
+@pytest.mark.parametrize("page,block", [(16, 16), (64, 16), (1, 1), (12, 4)])
+def test_read_starts_early(cuda, page, block):
+    # a chunk's append and the read-back that starts while it runs, many times in
+    # a graph: as call by call without the flag
+    lens, new, times, most = [3000, 40, 0, 517], [64, 7, 0, 30], 6, 3100
+    prob = _problem(lens, page=page, block=block)
+    total = sum(new)
+    qo = torch.tensor([0, 64, 71, 71, 101], dtype=torch.int32, device="cuda")
+    rows = [(_rows((total, 2, 128), 70 + i) * 4.0 ** i).cuda() for i in range(times)]
+    dst = torch.arange(4, dtype=torch.int32, device="cuda") * most
+    got = []
+    for flag in (0, A.PKV_FLAG_PLAN_EARLY):
+        ws, cache = prob.device()
+        outs = torch.zeros((times, 2, 4 * most, 2, 128), dtype=torch.bfloat16, device="cuda")
+
+        def run():
+            for i in range(times):
+                A.pkv_kv8_extend_append(ws, cache, 4, 0, qo, 64, rows[i], rows[-1 - i])
+                A.pkv_kv8_read(ws, cache, 4, 0, None, dst, 4 * most, outs[i, 0], outs[i, 1], flag)
+
+        if flag:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                run()
+            graph.replay()
+        else:
+            run()
+        torch.cuda.synchronize()
+        assert int(ws.err.item()) == 0
+        got.append((outs, cache.k_pool, cache.k_scale, cache.v_scale))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert got[0][0][-1, 0, :3000].any() and not got[0][0][:, :, 3000:most].any()
+
+
 def test_read_of_no_rows(cuda):
     prob = _problem([0, 20])
     ws, cache = prob.device()
