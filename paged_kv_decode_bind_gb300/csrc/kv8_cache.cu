@@ -8,8 +8,8 @@
 // of any sum.
 //
 // Measured (GB300; a pass in a graph): 64 decode rows with the blocks they touch
-// read back 5.8 us; 4 x 256 rows with their 6500-row contexts read back 14.6 us;
-// 32832 tokens of 8 heads read back 34.5 us, 5.9 TB/s (87 % of the copy rate),
+// read back 5.8 us; 4 x 256 rows with their 6500-row contexts read back 14.8 us;
+// 32832 tokens of 8 heads read back 34.9 us, 5.8 TB/s (87 % of the copy rate),
 // the same from 1 KB rows at random slots 81 %.
 #include "kernels.cuh"
 #include "kv8.cuh"

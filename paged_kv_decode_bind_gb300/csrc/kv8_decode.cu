@@ -41,8 +41,8 @@
 // atomic ticket).
 //
 // Measured (GB300, 2070 MHz; a pass in a graph): 4 x 65536 tokens, 32/8 heads
-// 89 us, 6.0 TB/s, 91 % of the copy rate; 64 x 1024-4096, 16/2 heads 23.6 us,
-// 3.3 TB/s; 16 flat contexts of 1-8192, 18.9 us, 2.4 TB/s; 4 x 512-2048 9.0 us.
+// 89 us, 6.0 TB/s, 91 % of the copy rate; 64 x 1024-4096, 16/2 heads 23.7 us,
+// 3.3 TB/s; 16 flat contexts of 1-8192, 19.4 us, 2.3 TB/s; 4 x 512-2048 9.1 us.
 // The bound of the long case is the warps' own latency (356 instructions a
 // piece for e4m3, four warps a scheduler, IPC 2.2; they wait for data in 8 of
 // 86 us), that of the short ones the chain lengths - page ids - tile - meeting -
