@@ -58,8 +58,8 @@ class Kv8Cache:
 class Kv8Extender:
     """A chunk of new tokens per request on the 8-bit cache, layer by layer:
     append, the contexts read back as bf16 pages, causal attention over those
-    (``pkv_extend_attn``).  The reading moves three times the cache's bytes, a
-    tenth of the attention's time for chunks of 256 tokens on 512 to 2048.
+    (``pkv_extend_attn``).  The reading moves three times the cache's bytes:
+    with the append 13 of a layer's 58 us for 4 chunks of 256 tokens on 917 to 2270.
 
     Contexts hold at most max_context tokens (longer ones raise PKV_DEVERR_LEN),
     chunks at most max_new.  Every buffer is allocated here once, so calls of one
