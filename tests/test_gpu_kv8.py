@@ -238,6 +238,27 @@ def test_attention_batches(cuda, B):
         _attend(prob, ws, cache, q, S, lens, what=f"B={B} S={S}")
 
 
+@pytest.mark.parametrize("page", [16, 1])
+@pytest.mark.parametrize("S", [2, 9])
+def test_attention_large_batch(cuda, page, S):
+    # one request far longer than the others, empty ones, bad ones among them
+    B = 310
+    lens = [(53 * i) % 70 for i in range(B)]
+    lens[7], lens[200], lens[0] = 2500, 900, 0
+    prob = _problem(lens, page=page, block=page, heads=(4, 2), d=64)
+    ws, cache = prob.device(max_splits=S)
+    q = W.normal_bf16((B, 4, 64), 15).cuda()
+    _attend(prob, ws, cache, q, S, lens)
+    bad = {3: -1, 150: prob.p.max_pages_per_req * page + 1, 309: -(2 ** 31)}
+    for b, n in bad.items():
+        ws.seq_lens[b], lens[b] = n, 0
+    A.pkv_kv8_decode_layer(ws, cache, B, 0, q, None, None, prob.p.scale, S, A.PKV_FLAG_WRITE_LSE)
+    torch.cuda.synchronize()
+    assert int(ws.err.item()) == A.PKV_DEVERR_LEN and int(ws.split_counters.abs().sum()) == 0
+    check_attention(ws.out_bf16(B).double().cpu().numpy(), ws.lse[:B].double().cpu().numpy(),
+                    prob.attention(0, q.cpu(), lens), "the good requests", BF16)
+
+
 @pytest.mark.parametrize("dtype", ["e4m3", "int8"])
 def test_attention_scales_far_apart(cuda, dtype):
     # value blocks of very different sizes, zero blocks among them, and keys that
