@@ -12,14 +12,17 @@
 // The block scales stay out of the products.  A token's score is
 //   x_t = (q . code_k,t) * k_scale_t * scale,  and its weight in O
 //   w_t = exp(x_t - r) * v_scale_t,
-// with a reference r that follows max(x_t + ln v_scale_t): the largest w_t is
-// then 2^7 .. 2^15, which fp16 holds whatever the value scales are, while the
-// softmax sum  l = sum exp(x_t - r)  stays in fp32 (v_scale_t in [2^-100,
-// 2^100] keeps exp(x_t - r) in its range).  out = O / l.  Rounding w to fp16
-// costs 2^-11 of a weight, an eighth of what the bf16 output's own rounding
-// may cost (weights under 2^-21 of the largest: 2^-32 of the largest).
-// r moves only when a weight would pass 2^15, so most tokens need one vote
-// instead of a maximum over lanes and a rescaling of O.
+// with a reference r that follows max(x_t + ln max(v_scale_t, 2^-80)): the
+// largest w_t is then 2^7 .. 2^15, which fp16 holds whatever the value scales
+// are, while the softmax sum  l = sum exp(x_t - r)  stays in fp32.  out = O / l.
+// The floor of 2^-80 is for l: a block of zeros has v_scale = 2^-100, and terms
+// of 2^115 each would pass fp32's range from 8192 such tokens on; no term is
+// now above 2^95, so 2^31 tokens stay below 2^126.  Rounding w to fp16 costs
+// 2^-11 of a weight, an eighth of what the bf16 output's own rounding may cost
+// (weights under 2^-21 of the largest: 2^-32 of the largest; where all value
+// scales that count lie below 2^-80, that is 2^-12, at 2^-100).
+// r moves only when a weight (at the floored scale) would pass 2^15, so most
+// tokens need one vote instead of a maximum over lanes and a rescaling of O.
 //
 // Data.  Each warp takes every W-th piece of 16 tokens of the unit and fills
 // its own ring of stages, so no block barrier stands between a copy and its
@@ -199,6 +202,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   constexpr int W = C::W, NS = C::NS, NH = C::NH;
   // log2 of the largest weight where r is placed, and the weight at which it moves
   constexpr float kPlace = 7.f, kMove = 32768.f;
+  constexpr float kScaleFloor = 8.271806125530277e-25f;  // 2^-80
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[PAGED ? W : 1][NS];
   __shared__ int s_pref[kMaxCompactBatch + 1];
@@ -744,6 +748,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
               for (int n = 0; n < NH; ++n) sc[n][2 * t] = sc[n][2 * t + 1] = -INFINITY;
             }
         }
+        const float vt[2] = {fmaxf(vs[0], kScaleFloor), fmaxf(vs[1], kScaleFloor)};
         float p[NH][4];  // exp(x - r); element 2 t + e
         auto weigh = [&]() {
           bool big = false;
@@ -752,12 +757,12 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               p[n][i] = fast_exp2(sc[n][i] - m_run[n][i & 1]);
-              big |= p[n][i] * vs[i >> 1] > kMove;
+              big |= p[n][i] * vt[i >> 1] > kMove;
             }
           return big;
         };
         if (__any_sync(0xffffffffu, weigh())) {
-          const float lv[2] = {fast_log2(vs[0]), fast_log2(vs[1])};
+          const float lv[2] = {fast_log2(vt[0]), fast_log2(vt[1])};
 #pragma unroll
           for (int n = 0; n < NH; ++n) {
             float al[2];

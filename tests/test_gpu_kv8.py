@@ -950,3 +950,75 @@ def test_offsets_past_32_bits(cuda):
     lo = int(torch.count_nonzero(cache.k_pool[:2])) + int(torch.count_nonzero(
         cache.k_pool[2, :slots - 32]))
     assert lo == 0 and int(ws.err.item()) == 0
+
+
+def _rising_scores(lens, hq, tail, zero):
+    """Requests whose scores lie 5.5 (7.9 in powers of two, just under what moves the
+    reference) above those of their first 128 tokens, value scales `zero` (codes 0
+    there) but for ordinary values in the last block where `tail`.  One KV head,
+    D = 64, int8."""
+    prob = _problem(lens, "int8", heads=(hq, 1), d=64)
+    prob.k.codes[...] = 0
+    prob.k.scales[...] = 1.0
+    tail_codes, tail_scales = prob.v.codes.copy(), prob.v.scales.copy()
+    prob.v.codes[...] = 0
+    prob.v.scales[...] = zero
+    for b, n in enumerate(lens):
+        s = prob.slots(b, 0, n)
+        prob.k.codes[0, s[128:], 0, 0] = 127
+        if tail:
+            last = s[(n - 1) // 16 * 16:]
+            prob.v.codes[0, last] = tail_codes[0, last]
+            prob.v.scales[0, last[0] // 16] = tail_scales[0, last[0] // 16]
+    q = torch.zeros((len(lens), hq, 64), dtype=torch.bfloat16)
+    q[:, :, 0] = 5.5 / 127 / prob.p.scale
+    return prob, q
+
+
+@pytest.mark.parametrize("n,hq", [(20000, 2), (20000, 16), (150000, 2)])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("S", [1, 2, 5])
+def test_attention_long_runs_of_zero_values(cuda, n, hq, tail, S):
+    # rows of zeros carry the smallest scale: the sum of their weights stays finite
+    # within a warp (150000: over 9000 tokens each), a unit and a merge
+    prob, q = _rising_scores([n, 40], hq, tail, 2.0 ** -100)
+    ws, cache = prob.device(max_splits=S)
+    got = _attend(prob, ws, cache, q.cuda(), S, [n, 40], A.PKV_FLAG_OUT_F32, what=f"{n} S={S}")
+    assert got.any() == tail
+
+
+@pytest.mark.parametrize("zero", [2.0 ** -100, 2.0 ** -81, 2.0 ** -80, 2.0 ** -60, 2.0 ** 100])
+@pytest.mark.parametrize("S", [1, 3])
+def test_attention_values_at_the_scale_limits(cuda, zero, S):
+    # ordinary codes under the smallest and largest scales
+    lens = [3000, 50]
+    prob, q = _rising_scores(lens, 2, False, zero)
+    g = np.random.default_rng(8)
+    prob.v.codes[...] = g.integers(0, 256, prob.v.codes.shape)
+    prob.v.codes[prob.v.codes == 128] = 127  # -128 is no code
+    ws, cache = prob.device(max_splits=S)
+    A.pkv_kv8_decode_layer(ws, cache, 2, 0, q.cuda(), None, None, prob.p.scale, S,
+                           A.PKV_FLAG_WRITE_LSE | A.PKV_FLAG_OUT_F32)
+    torch.cuda.synchronize()
+    o, l, bo, bl = prob.attention(0, q, lens)
+    # the reference r is as large as far = 7 + |log2 scale| + 8 (place, scale, scores):
+    # the subtraction x - r rounds by half a step of that, and so do both terms of
+    # lse = r ln 2 + log(sum): ln 2 itself and the product (1.5 half steps), the
+    # logarithm (2 half steps)
+    far = 15 + abs(np.log2(max(zero, 2.0 ** -80)))
+    bl += 5 * F32 * far * np.log(2)
+    if zero < 2.0 ** -80:
+        # the reference counts these scales as 2^-80, so a warp's largest weight is at
+        # least 2^7 zero / 2^-80, and a weight below fp16's normal range is off by
+        # 2^-25: over all tokens 2^-25 / (2^87 zero) of the largest p_t v_scale_t, times
+        # sum_t |code_t| (2 %: the query is rounded, the scores rise by 5.5 / 2^8 more)
+        codes = [np.abs(prob.v.rows(0, prob.slots(b, 0, n)) / zero).sum(0) for b, n in
+                 enumerate(lens)]
+        for b, n in enumerate(lens):
+            x = np.where(np.arange(n) < 128, 0, 5.5)
+            top = zero / np.exp(x - x.max()).sum()  # the largest p_t v_scale_t
+            bo[b] += 2.0 ** -25 / (2.0 ** 87 * zero) * 1.02 * top * codes[b]
+    check_attention(ws.out_f32(2).double().cpu().numpy() / zero,
+                    ws.lse[:2].double().cpu().numpy(), (o / zero, l, bo / zero, bl),
+                    f"{zero} S={S}", F32)
+    assert int(ws.err.item()) == 0
