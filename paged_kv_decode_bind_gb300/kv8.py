@@ -65,6 +65,10 @@ class Kv8Extender:
     chunks at most max_new.  Every buffer is allocated here once, so calls of one
     extender run one after the other (on one stream, or ordered by the caller)."""
 
+    # Not PKV_FLAG_WRITE_LSE: ws.lse has a row per request, not per new token.
+    EXTEND_FLAGS = (_abi.PKV_FLAG_OUT_F32 | _abi.PKV_FLAG_EXTEND_FULL |
+                    _abi.PKV_FLAG_EXTEND_WARP_MMA)
+
     def __init__(self, ws, cache, batch, *, max_new, max_context, scale, num_splits=1):
         sh = ws.shape
         H, Hq, D = sh["n_kv_heads"], sh["n_q_heads"], sh["head_dim"]
@@ -104,9 +108,15 @@ class Kv8Extender:
     def layer(self, layer, qo_indptr, max_qo_len, q, k_new, v_new, out, flags=0, stream=None):
         """Rows q, k_new, v_new [total, heads, D] of the new tokens (offsets
         qo_indptr, as pkv_extend_attn) into out [total, Hq, D]; ws.seq_lens count
-        the new tokens, and flat indices are bound (PKV_BIND_REBUILD)."""
+        the new tokens, and flat indices are bound (PKV_BIND_REBUILD).
+        flags: those of EXTEND_FLAGS, with pkv_extend_attn's meaning; the permission
+        of PKV_FLAG_PLAN_EARLY is not used (the launch before the attention writes
+        the rows it reads)."""
         if max_qo_len > self.max_new:
             raise ValueError("max_qo_len exceeds max_new")
+        flags &= ~_abi.PKV_FLAG_PLAN_EARLY
+        if flags & ~self.EXTEND_FLAGS:
+            raise ValueError("flags: PKV_FLAG_OUT_F32, _EXTEND_FULL, _EXTEND_WARP_MMA")
         _abi.pkv_kv8_extend_append(self.read_view, self.cache, self.batch, layer, qo_indptr,
                                    max_qo_len, k_new, v_new, stream)
         _abi.pkv_kv8_read(self.read_view, self.cache, self.batch, layer, None, self.first_row,
@@ -114,7 +124,7 @@ class Kv8Extender:
                           # the append, if there is one, is the previous launch
                           _abi.PKV_FLAG_PLAN_EARLY if max_qo_len else 0, stream)
         _abi.pkv_extend_attn(self.rows_view, self.batch, 0, qo_indptr, max_qo_len, q, out,
-                             self.scale, self.num_splits, flags & _abi.PKV_FLAG_OUT_F32, stream)
+                             self.scale, self.num_splits, flags, stream)
 
 
 class QkNormRope:

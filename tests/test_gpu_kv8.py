@@ -516,6 +516,35 @@ def test_extender(cuda, dtype, page, block, d, S):
     assert int(ws.err.item()) == 0
 
 
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("warp", [False, True])
+@pytest.mark.parametrize("S", [1, 2])
+def test_extender_passes_flags_on(cuda, full, warp, S):
+    # PKV_FLAG_EXTEND_FULL: a chunk's first row sees its last one's token too
+    from paged_kv_decode_bind_gb300 import Kv8Extender
+    lens, new = [70, 33], [20, 33]
+    prob = _problem(lens)
+    ws, cache = prob.device()
+    ext = Kv8Extender(ws, cache, 2, max_new=33, max_context=80, scale=prob.p.scale, num_splits=S)
+    qo = torch.tensor([0, 20, 53], dtype=torch.int32).cuda()
+    q, k, v = W.normal_bf16((53, 8, 128), 90), _rows((53, 2, 128), 91), _rows((53, 2, 128), 92)
+    out = torch.zeros((53, 8, 128), dtype=torch.float32, device="cuda")
+    ext.layer(0, qo, 33, q.cuda(), k.cuda(), v.cuda(), out, A.PKV_FLAG_OUT_F32 |
+              A.PKV_FLAG_PLAN_EARLY | full * A.PKV_FLAG_EXTEND_FULL |
+              warp * A.PKV_FLAG_EXTEND_WARP_MMA)
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    kr, vr = (x[0].double().cpu().numpy() for x in (ext.k_rows, ext.v_rows))
+    for b, n in enumerate(lens):
+        at = int(ext.first_row[b])
+        kk, vv = kr[at:at + n], vr[at:at + n]
+        for t in range(new[b]):
+            m = n if full else n - new[b] + t + 1
+            o = K8.attention(K8_values(q[int(qo[b]) + t]), kk[:m], vv[:m], prob.p.scale)[0]
+            assert np.abs(got[int(qo[b]) + t] - o).max() <= 1e-3 * np.abs(vv[:m]).max()
+    assert int(ws.err.item()) == 0
+
+
 def test_extender_refuses_longer_contexts(cuda):
     # a context past max_context: its request is skipped, its neighbour's rows
     # are its own

@@ -274,6 +274,16 @@ def test_runner_and_extender_arguments():
             Kv8Extender(ws, c, args.pop("batch"), **args)
 
 
+@pytest.mark.parametrize("flag", [A.PKV_FLAG_WRITE_LSE,
+                                  A.PKV_FLAG_OUT_F32 | A.PKV_FLAG_FORCE_SIMT, 1 << 20])
+def test_extender_refuses_flags_it_does_not_pass_on(flag):
+    from paged_kv_decode_bind_gb300 import Kv8Extender
+    ws = _cpu_ws()
+    e = Kv8Extender(ws, Kv8Cache(ws), 2, max_new=3, max_context=20, scale=0.1)
+    with pytest.raises(ValueError):
+        e.layer(0, None, 2, None, None, None, None, flag)
+
+
 def test_rope_owner():
     t = rope_table(10, 32, device="cpu")
     w = torch.ones(64, dtype=torch.bfloat16)
