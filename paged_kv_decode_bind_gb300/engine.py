@@ -39,7 +39,8 @@ class DecodeRunner:
         """cache: a Kv8Cache of this workspace; the layers then append to and
         attend over it instead of the bf16 pools (flags: PKV_FLAG_OUT_F32 and
         PKV_FLAG_WRITE_LSE).  norm_rope: a QkNormRope, or one per layer, applied
-        to the layer's q and k at ws.position_ids before they are used."""
+        to the layer's q and k at ws.position_ids before they are used; a step's
+        device errors all go to ws.err, the norm's too (whatever its own word is)."""
         if cache is not None and (not fused or plan):
             raise ValueError("a step on the 8-bit cache has no unfused or planned form")
         self.cache = cache
@@ -65,6 +66,11 @@ class DecodeRunner:
                     (r.struct.n_q_heads, r.struct.n_kv_heads, r.struct.head_dim) !=
                     (sh["n_q_heads"], sh["n_kv_heads"], sh["head_dim"]) for r in self.norm_rope):
                 raise ValueError("norm_rope: one QkNormRope of the workspace's heads per layer")
+            self.rope_args = []
+            for r in self.norm_rope:
+                args = _abi.PkvQkNormRopeArgs.from_buffer_copy(r.struct)
+                args.err, args.widths = ws.err.data_ptr(), r.widths
+                self.rope_args.append(args)
             # one layer's rows at a time: the next layer's kernel waits for this one's
             self.q_use = torch.zeros_like(self.q_in[0])
             self.k_use = torch.zeros_like(self.k_in[0])
@@ -120,7 +126,7 @@ class DecodeRunner:
         s = self._s()
         q, k = self.q_in[l], self.k_in[l]
         if self.norm_rope is not None:
-            _abi.pkv_qk_norm_rope(self.norm_rope[l], self.batch, q, k, self.ws.position_ids,
+            _abi.pkv_qk_norm_rope(self.rope_args[l], self.batch, q, k, self.ws.position_ids,
                                   self.q_use, self.k_use, s)
             q, k = self.q_use, self.k_use
         if self.cache is not None:

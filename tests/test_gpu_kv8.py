@@ -478,6 +478,23 @@ def test_runner_steps(cuda, dtype, page, block, graph):
     assert int(ws.err.item()) == 0 and int(ropes[0].err.item()) == 0
 
 
+@pytest.mark.parametrize("eight_bit", [True, False])
+def test_runner_reports_positions_past_the_table(cuda, eight_bit):
+    from paged_kv_decode_bind_gb300 import DecodeRunner, QkNormRope, Workspace, rope_table
+    lens, steps = [20, 7], 3
+    prob = _problem(lens, layers=2, steps=steps)
+    if eight_bit:
+        ws, cache = prob.device()
+    else:
+        ws, cache = Workspace.from_problem(prob.p), None
+    rope = QkNormRope(n_q_heads=8, n_kv_heads=2, head_dim=128, cos_sin=rope_table(21, 128))
+    run = DecodeRunner(ws, 2, scale=prob.p.scale, cache=cache, norm_rope=rope)
+    run.step()
+    assert int(ws.err.item()) == 0  # position 20, the last of the table
+    run.step()
+    assert int(ws.err.item()) == A.PKV_DEVERR_POSITION
+
+
 @pytest.mark.parametrize("dtype,page,block,d", [("e4m3", 16, 16, 128), ("int8", 1, 1, 128),
                                                 ("int8", 12, 4, 64)])
 @pytest.mark.parametrize("S", [1, 3])

@@ -284,6 +284,20 @@ def test_extender_refuses_flags_it_does_not_pass_on(flag):
         e.layer(0, None, 2, None, None, None, None, flag)
 
 
+def test_runner_collects_position_errors():
+    # whatever word the norm's arguments have, a step's errors are in ws.err
+    from paged_kv_decode_bind_gb300 import DecodeRunner
+    ws = _cpu_ws()
+    own = torch.zeros(1, dtype=torch.int32)
+    ropes = [QkNormRope(n_q_heads=4, n_kv_heads=2, head_dim=64, err=err,
+                        cos_sin=rope_table(9, 64, device="cpu")) for err in (None, own)]
+    run = DecodeRunner(ws, 2, norm_rope=ropes)
+    for args, r in zip(run.rope_args, ropes):
+        assert args.err == ws.err.data_ptr() != r.struct.err
+        assert args.cos_sin == r.struct.cos_sin and args.max_positions == 9
+        assert args.widths == (64, 256, 128)
+
+
 def test_rope_owner():
     t = rope_table(10, 32, device="cpu")
     w = torch.ones(64, dtype=torch.bfloat16)
