@@ -197,6 +197,17 @@ def _ws(ws):
     return getattr(ws, "struct", ws)  # passed by reference (see the argtypes)
 
 
+def _kv8(ws, cache):
+    """The struct of a cache.  A Kv8Cache knows the pool shapes that it was built for:
+    under a workspace of others its calls would write past its buffers."""
+    shape, w = getattr(cache, "shape", None), _ws(ws)
+    if shape is not None and w is not None and \
+            shape != (w.n_layers, w.pool_slots, w.n_kv_heads, w.head_dim, w.page_size):
+        raise ValueError("the cache was built for a workspace of other shapes: (layers, slots, "
+                         f"KV heads, head_dim, page size) {shape}")
+    return _ws(cache)
+
+
 def _check(fn, status):
     if status != PKV_OK:
         raise PkvError(fn, status)
@@ -309,15 +320,16 @@ def pkv_kv8_append(ws, cache, batch, layer_begin, layer_count, k_new, v_new, str
                    check=True):
     """New rows [layer_count, batch, Hkv, D] quantised into an 8-bit cache (a
     Kv8Cache or a PkvKv8) at ws.out_loc."""
-    s = load().pkv_kv8_append(_ws(ws), _ws(cache), int(batch), int(layer_begin), int(layer_count),
-                              _ptr(k_new), _ptr(v_new), _stream(stream))
+    s = load().pkv_kv8_append(_ws(ws), _kv8(ws, cache), int(batch), int(layer_begin),
+                              int(layer_count), _ptr(k_new), _ptr(v_new), _stream(stream))
     return _check("pkv_kv8_append", s) if check else s
 
 
 def pkv_kv8_extend_append(ws, cache, batch, layer, qo_indptr, max_qo_len, k_new, v_new,
                           stream=None, check=True):
-    s = load().pkv_kv8_extend_append(_ws(ws), _ws(cache), int(batch), int(layer), _ptr(qo_indptr),
-                                     int(max_qo_len), _ptr(k_new), _ptr(v_new), _stream(stream))
+    s = load().pkv_kv8_extend_append(_ws(ws), _kv8(ws, cache), int(batch), int(layer),
+                                     _ptr(qo_indptr), int(max_qo_len), _ptr(k_new), _ptr(v_new),
+                                     _stream(stream))
     return _check("pkv_kv8_extend_append", s) if check else s
 
 
@@ -325,7 +337,7 @@ def pkv_kv8_read(ws, cache, batch, layer, starts, dst_indptr, n_rows, k_out, v_o
                  stream=None, check=True):
     """Cached rows of every request from token starts[b] on (None: 0) as rows
     dst_indptr[b], ... of k_out and v_out [n_rows, Hkv, D]."""
-    s = load().pkv_kv8_read(_ws(ws), _ws(cache), int(batch), int(layer), _ptr(starts),
+    s = load().pkv_kv8_read(_ws(ws), _kv8(ws, cache), int(batch), int(layer), _ptr(starts),
                             _ptr(dst_indptr), int(n_rows), _ptr(k_out), _ptr(v_out), int(flags),
                             _stream(stream))
     return _check("pkv_kv8_read", s) if check else s
@@ -335,7 +347,7 @@ def pkv_kv8_decode_layer(ws, cache, batch, layer, q, k_new, v_new, scale, num_sp
                          stream=None, check=True):
     """Append (unless k_new is None), attention and merge of one layer on the
     8-bit cache."""
-    s = load().pkv_kv8_decode_layer(_ws(ws), _ws(cache), int(batch), int(layer), _ptr(q),
+    s = load().pkv_kv8_decode_layer(_ws(ws), _kv8(ws, cache), int(batch), int(layer), _ptr(q),
                                     _ptr(k_new), _ptr(v_new), float(scale), int(num_splits),
                                     int(flags), _stream(stream))
     return _check("pkv_kv8_decode_layer", s) if check else s

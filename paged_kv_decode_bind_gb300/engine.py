@@ -12,6 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _abi
+from .kv8 import check_cache
 from .workspace import Workspace
 
 
@@ -43,6 +44,8 @@ class DecodeRunner:
         device errors all go to ws.err, the norm's too (whatever its own word is)."""
         if cache is not None and (not fused or plan):
             raise ValueError("a step on the 8-bit cache has no unfused or planned form")
+        if cache is not None:
+            check_cache(ws, cache)
         self.cache = cache
         self.ws = ws
         self.batch = batch

@@ -21,7 +21,8 @@ class Kv8Cache:
     Existing uint8 and fp32 tensors of those shapes may be given (for example
     a cache that was saved); new ones start as zeros under the
     smallest scale, so that rows never written count as zeros.  A workspace built
-    with ``pools=False`` has no bf16 pools to pay for."""
+    with ``pools=False`` has no bf16 pools to pay for.  A call with a workspace of
+    other shapes raises ValueError."""
 
     def __init__(self, ws, *, dtype="e4m3", scale_block=None, k_pool=None, v_pool=None,
                  k_scale=None, v_scale=None):
@@ -47,12 +48,20 @@ class Kv8Cache:
             return x
 
         self.dtype, self.scale_block, self.device = dtype, scale_block, ws.device
+        self.shape = (sh["n_layers"], sh["pool_slots"], H, D, P)  # calls check it against ws
         self.k_pool, self.v_pool = (own(x, codes, torch.uint8) for x in (k_pool, v_pool))
         self.k_scale, self.v_scale = (own(x, scales, torch.float32) for x in (k_scale, v_scale))
         self.struct = _abi.PkvKv8(
             dtype=DTYPES[dtype], scale_block=scale_block, k_pool=self.k_pool.data_ptr(),
             v_pool=self.v_pool.data_ptr(), k_scale=self.k_scale.data_ptr(),
             v_scale=self.v_scale.data_ptr())
+
+
+def check_cache(ws, cache):
+    """Raise ValueError unless the cache is one of this workspace's shapes and device."""
+    _abi._kv8(ws, cache)
+    if isinstance(cache, Kv8Cache) and cache.k_pool.device != ws.err.device:
+        raise ValueError(f"the cache is on {cache.k_pool.device}, the workspace on {ws.err.device}")
 
 
 class Kv8Extender:
@@ -76,6 +85,7 @@ class Kv8Extender:
             raise ValueError("batch must be in 1 .. the workspace's max_batch")
         if max_new < 1 or max_context < 1 or num_splits < 1:
             raise ValueError("max_new, max_context and num_splits start at 1")
+        check_cache(ws, cache)
         # no context is longer than its table row
         max_context = min(max_context, sh["max_pages_per_req"] * sh["page_size"])
         dev = ws.device

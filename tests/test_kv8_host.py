@@ -298,6 +298,43 @@ def test_runner_collects_position_errors():
         assert args.widths == (64, 256, 128)
 
 
+@pytest.mark.parametrize("kw", [dict(n_layers=1), dict(pool_slots=32), dict(n_kv_heads=1),
+                                dict(head_dim=128), dict(page_size=8, max_pages_per_req=4)])
+def test_a_cache_of_other_shapes_is_refused(kw):
+    # its buffers are smaller, or laid out in another way, than the workspace says
+    from paged_kv_decode_bind_gb300 import DecodeRunner, Kv8Extender
+    shape = dict(n_layers=2, pool_slots=64, n_q_heads=4, n_kv_heads=2, head_dim=64, page_size=16,
+                 max_batch=2, max_reqs=2, max_pages_per_req=2, device="cpu", pools=False)
+    ws, other = Workspace(**shape), Workspace(**{**shape, **kw})
+    cache = Kv8Cache(other, scale_block=4)
+    calls = [lambda w: P.pkv_kv8_append(w, cache, 0, 0, 1, F, F, 0),
+             lambda w: P.pkv_kv8_extend_append(w, cache, 0, 0, F, 4, F, F, 0),
+             lambda w: P.pkv_kv8_read(w, cache, 0, 0, None, F, 4, F, F, 0, 0),
+             lambda w: P.pkv_kv8_decode_layer(w, cache, 0, 0, F, None, None, 0.1, 1, 0, 0),
+             lambda w: DecodeRunner(w, 2, cache=cache),
+             lambda w: Kv8Extender(w, cache, 2, max_new=1, max_context=9, scale=0.1)]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call(ws)
+    for call in calls[:4]:  # the bare struct too
+        with pytest.raises(ValueError):
+            call(ws.struct)
+    # its own, and a copy of its struct
+    for w in (other, A.PkvWorkspace.from_buffer_copy(other.struct)):
+        assert P.pkv_kv8_append(w, cache, 0, 0, 1, None, None, 0) == P.PKV_OK
+    for call in calls[4:]:
+        call(other)
+
+
+def test_a_cache_on_another_device_is_refused():
+    from paged_kv_decode_bind_gb300 import DecodeRunner
+    ws = _cpu_ws()
+    c = Kv8Cache(ws)
+    c.k_pool = c.k_pool.to("meta")
+    with pytest.raises(ValueError):
+        DecodeRunner(ws, 2, cache=c)
+
+
 def test_rope_owner():
     t = rope_table(10, 32, device="cpu")
     w = torch.ones(64, dtype=torch.bfloat16)
