@@ -9,6 +9,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
 
@@ -172,7 +174,6 @@ def _current_stream():
     raw handle is asked for where torch has a call for that."""
     global _current
     if _current is None:
-        import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         dev = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         if not torch.cuda.is_available():
@@ -353,29 +354,51 @@ def pkv_kv8_decode_layer(ws, cache, batch, layer, q, k_new, v_new, scale, num_sp
     return _check("pkv_kv8_decode_layer", s) if check else s
 
 
-def _heads(x, width, head_dim):
+_BF16, _INT32 = torch.bfloat16, torch.int32
+
+
+def _heads(x, width, head_dim, rows=0):
     """Pointer and elements between tokens of x: a pointer or None is dense; a
-    tensor is [tokens, width] or [tokens, heads, head_dim] with dense heads."""
+    tensor is bf16 [tokens, width] or [tokens, heads, head_dim] with dense heads and
+    at least `rows` tokens."""
     if x is None or isinstance(x, int):
         return x, width
-    st = x.stride()
-    if len(st) not in (2, 3) or st[-1] != 1 or \
-            (len(st) == 3 and st[1] != head_dim and x.shape[1] > 1):
-        raise ValueError("heads must be dense: [tokens, width] or [tokens, heads, head_dim]")
+    st, n, ok = x.stride(), 0, False
+    if len(st) == 2:
+        n, w = x.shape
+        ok = w == width and st[1] == 1
+    elif len(st) == 3:
+        n, h, d = x.shape
+        ok = d == head_dim and h * d == width and st[2] == 1 and (st[1] == d or h <= 1)
+    if not ok or n < rows or x.dtype is not _BF16:
+        raise ValueError(f"expected bf16 [tokens >= {rows}, {width}] or [tokens, heads, {head_dim}] "
+                         f"with dense heads, got {x.dtype} {tuple(x.shape)} with strides {st}")
     # the stride of a single token may be anything
-    return x.data_ptr(), width if st[0] < width and x.shape[0] <= 1 else st[0]
+    return x.data_ptr(), width if st[0] < width and n <= 1 else st[0]
+
+
+def _positions(x, rows):
+    """Pointer of the int32 positions of at least `rows` tokens."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype is not _INT32 or x.numel() < rows or not x.is_contiguous():
+        raise ValueError(f"positions are dense int32 [tokens >= {rows}], got {x.dtype} "
+                         f"{tuple(x.shape)}")
+    return x.data_ptr()
 
 
 def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None, check=True):
     """RMS norm and rotation of every head of q and k into q_out and k_out
     (args: a QkNormRope or a PkvQkNormRopeArgs); q and k may be slices of one
-    projection's rows."""
+    projection's rows.  Tensors of another type, another width or fewer than
+    n_tokens rows raise ValueError."""
     st = getattr(args, "struct", args)
     D, qw, kw = getattr(args, "widths", None) or \
         (st.head_dim, st.n_q_heads * st.head_dim, st.n_kv_heads * st.head_dim)
-    s = load().pkv_qk_norm_rope(st, n_tokens, *_heads(q, qw, D), *_heads(k, kw, D),
-                                _ptr(positions), *_heads(q_out, qw, D), *_heads(k_out, kw, D),
-                                _stream(stream))
+    n = n_tokens
+    s = load().pkv_qk_norm_rope(st, n, *_heads(q, qw, D, n), *_heads(k, kw, D, n),
+                                _positions(positions, n), *_heads(q_out, qw, D, n),
+                                *_heads(k_out, kw, D, n), _stream(stream))
     return _check("pkv_qk_norm_rope", s) if check else s
 
 

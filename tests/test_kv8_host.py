@@ -208,6 +208,43 @@ def test_rope_strides_of_one_head_or_token():
     assert A._heads(torch.as_strided(x, (2, 256), (8, 1)), 256, 64)[1] == 8  # the call refuses it
 
 
+def test_rope_tensors_that_do_not_fit_are_refused():
+    # another type, width, head size or fewer tokens than the call has would be read,
+    # or written, as something else
+    r = QkNormRope(n_q_heads=4, n_kv_heads=2, head_dim=128,
+                   cos_sin=rope_table(9, 128, device="cpu"))
+    row = torch.zeros((3, 1024), dtype=torch.bfloat16)
+    q, k, pos = row[:, :512], row[:, 512:768], torch.zeros(3, dtype=torch.int32)
+    good = dict(q=q, k=k, positions=pos, q_out=q, k_out=k)
+
+    def call(n, **kw):
+        a = {**good, **kw}
+        return A.pkv_qk_norm_rope(r, n, a["q"], a["k"], a["positions"], a["q_out"], a["k_out"], 0)
+
+    assert call(0) == P.PKV_OK  # nothing is launched for no tokens
+    heads = row.view(3, 8, 128)
+    assert call(0, q=heads[:, :4], k_out=heads[:, 4:6]) == P.PKV_OK
+    for name, n_heads in (("q", 4), ("k", 2), ("q_out", 4), ("k_out", 2)):
+        w = n_heads * 128
+        for bad in (row[:, :w].float(), row[:, :w].half(), row[:, :w - 128], row[:, :w + 128],
+                    row.view(3, 16, 64)[:, :n_heads], row.view(3, 16, 64)[:, :2 * n_heads],
+                    heads[:, :n_heads + 1], row[0, :w], row.view(3, 1, 8, 128)[:, :, :n_heads],
+                    row[:, :2 * w:2]):
+            with pytest.raises(ValueError):
+                call(0, **{name: bad})
+        with pytest.raises(ValueError):
+            call(4, **{m: torch.zeros((3 if m == name else 4, x.shape[1]),
+                                        dtype=torch.bfloat16)
+                       for m, x in good.items() if m != "positions"},
+                 positions=torch.zeros(4, dtype=torch.int32))
+    for bad in (pos.long(), pos.float(), torch.zeros(6, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError):
+            call(0, positions=bad)
+    with pytest.raises(ValueError):
+        A._positions(pos, 4)
+    assert A._positions(pos, 3) == pos.data_ptr() and A._positions(None, 3) is None
+
+
 def test_empty_calls_need_no_buffers():
     kw = dict(stream=0, check=False)
     assert P.pkv_kv8_append(_ws(), _c(), 0, 0, 1, None, None, **kw) == P.PKV_OK
