@@ -69,6 +69,8 @@ class DecodeRunner:
                     (r.struct.n_q_heads, r.struct.n_kv_heads, r.struct.head_dim) !=
                     (sh["n_q_heads"], sh["n_kv_heads"], sh["head_dim"]) for r in self.norm_rope):
                 raise ValueError("norm_rope: one QkNormRope of the workspace's heads per layer")
+            if any(r.err.device != ws.err.device for r in self.norm_rope):
+                raise ValueError("norm_rope: its tensors are not on the workspace's device")
             self.rope_args = []
             for r in self.norm_rope:
                 args = _abi.PkvQkNormRopeArgs.from_buffer_copy(r.struct)

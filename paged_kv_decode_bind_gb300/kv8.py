@@ -154,8 +154,14 @@ class QkNormRope:
                         cos_sin.dim() != 2 or cos_sin.shape[1] != rot_dim or
                         not cos_sin.is_contiguous()):
             raise ValueError("cos_sin is dense fp32 [positions, rot_dim]")
-        device = next((x.device for x in (cos_sin, q_weight, k_weight) if x is not None), "cuda")
-        self.err = torch.zeros(1, dtype=torch.int32, device=device) if err is None else err
+        homes = {x.device for x in (cos_sin, q_weight, k_weight, err) if x is not None}
+        if len(homes) > 1:
+            raise ValueError(f"the tensors are on several devices: {sorted(map(str, homes))}")
+        if err is None:
+            err = torch.zeros(1, dtype=torch.int32, device=homes.pop() if homes else "cuda")
+        elif err.dtype != torch.int32 or err.numel() < 1:
+            raise ValueError("err is an int32 tensor")
+        self.err = err
         self.cos_sin, self.q_weight, self.k_weight = cos_sin, q_weight, k_weight
         self.widths = (head_dim, n_q_heads * head_dim, n_kv_heads * head_dim)  # of a token's rows
         self.struct = _abi.PkvQkNormRopeArgs(

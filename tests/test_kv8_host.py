@@ -383,6 +383,24 @@ def test_rope_owner():
             QkNormRope(n_q_heads=2, n_kv_heads=1, head_dim=64, rot_dim=32, **kw)
 
 
+def test_rope_tensors_on_several_devices_are_refused():
+    # the kernel would take a host table's address for one of its own device
+    from paged_kv_decode_bind_gb300 import DecodeRunner
+    t = rope_table(9, 64, device="cpu")
+    w = torch.ones(64, dtype=torch.bfloat16)
+    kw = dict(n_q_heads=4, n_kv_heads=2, head_dim=64)
+    for bad in (dict(cos_sin=t.to("meta"), q_weight=w), dict(cos_sin=t, k_weight=w.to("meta")),
+                dict(cos_sin=t, err=torch.zeros(1, dtype=torch.int32, device="meta")),
+                dict(cos_sin=t, err=torch.zeros(1))):
+        with pytest.raises(ValueError):
+            QkNormRope(**kw, **bad)
+    far = QkNormRope(**kw, cos_sin=t)
+    far.err = far.err.to("meta")  # as if all of it were
+    with pytest.raises(ValueError):
+        DecodeRunner(_cpu_ws(), 2, norm_rope=far)
+    assert QkNormRope(**kw, cos_sin=t, q_weight=w).err.device == t.device
+
+
 # ------------------------------------------------------------- oracle pins ----
 def test_oracle_codes():
     T = K8.TABLE["e4m3"]
