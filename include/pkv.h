@@ -497,8 +497,10 @@ size_t pkv_kv8_bytes(const pkv_workspace *ws, const pkv_kv8 *c, const char *whic
  *   code  = round to nearest even (x / scale), saturating at +-qmax; NaN is
  *           kept by e4m3 and becomes 0 in int8
  * and where the scale grew, the block's older codes are rounded once more,
- * code = rn(code * old scale / new scale).  The division is exact: new scales
- * are powers of two.  Two entries of a batch must not share a block.
+ * code = rn(code * old scale / new scale).  The scales written are powers of two,
+ * so nothing but rn rounds; a block that keeps a scale of another kind (a cache may
+ * come with them) gets the code nearest to the exact quotient all the same.  Two
+ * entries of a batch must not share a block.
  * Device errors: PKV_DEVERR_SLOT (that row is skipped).
  * Host errors: PKV_ERR_INVALID (null or misaligned pointer, bad dtype or
  * scale_block), PKV_ERR_UNSUPPORTED (head_dim not 64 / 128), PKV_ERR_CAPACITY.

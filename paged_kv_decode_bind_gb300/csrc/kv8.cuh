@@ -3,7 +3,9 @@
 //
 // A scale is a power of two, so dividing a bf16 value by it, and reading
 // code * scale back as bf16, are exact: the only rounding is the one to the
-// code.  For e4m3 a power of two costs nothing (its own exponent takes up the
+// code.  (A cache may come with other scales, as a calibration leaves them; blocks
+// that keep such a scale when rows are appended divide by it, rounded to odd, so
+// that the code is the one nearest to the exact quotient.)  For e4m3 a power of two costs nothing (its own exponent takes up the
 // difference); for int8 it costs less than one bit against amax / 127, and
 // makes a block that grows lose at most its low bits once.
 #pragma once
@@ -38,6 +40,32 @@ __device__ __forceinline__ int need_exp(float amax) {
   const int bits = __float_as_int(amax);
   const int e = (bits >> 23) - 127 - kShift + ((bits & 0x7fffff) > kTop ? 1 : 0);
   return amax > 0.f ? max(kKv8MinExp, min(kKv8MaxExp, e)) : kKv8MinExp;
+}
+
+__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_int(s) & 0x7fffff) == 0; }
+
+// A value rounded towards zero, and what was cut off: rounded to odd.  A later
+// rounding to at most 22 bits then gives what rounding the exact value gives.
+// (NaN in `rest`, behind an infinity, leaves the value.)
+__device__ __forceinline__ float to_odd(float value, float rest) {
+  return rest < 0.f || rest > 0.f ? __int_as_float(__float_as_int(value) | 1) : value;
+}
+
+// x / s for s in [2^-100, 2^100] that is no power of two, rounded to odd.  A small s
+// and its x are first brought 2^64 up, so that the remainder cannot underflow where
+// the quotient is not far below every code.
+__device__ __forceinline__ float div_odd(float x, float s) {
+  const float up = s < 1.f ? 18446744073709551616.f : 1.f;
+  x *= up;
+  s *= up;
+  const float q = __fdiv_rz(x, s);
+  return to_odd(q, fmaf(-q, s, x));
+}
+
+// a * b rounded to odd.
+__device__ __forceinline__ float mul_odd(float a, float b) {
+  const float p = __fmul_rz(a, b);
+  return to_odd(p, fmaf(a, b, -p));
 }
 
 // |x| for the maximum of a block: elements that are not finite do not count.

@@ -3,9 +3,9 @@
 //
 // All three move each byte once and are bound by memory for long inputs and
 // by the chain of dependent loads (slot, scale, rows) for short ones.  Codes
-// and scales follow pkv.h; every division is by a power of two, so the values
+// and scales follow pkv.h; every scale written is a power of two, so the values
 // compared and rounded are exact and the results do not depend on the order
-// of any sum.
+// of any sum.  A block that keeps a scale that is none divides by it (kv8.cuh).
 //
 // Measured (GB300; a pass in a graph): 64 decode rows with the blocks they touch
 // read back 5.8 us; 4 x 256 rows with their 6500-row contexts read back 14.8 us;
@@ -46,8 +46,44 @@ __device__ __forceinline__ uint2 recode8(const uint2 &w, float ratio) {
                     encode4<DT>(b[0] * ratio, b[1] * ratio, b[2] * ratio, b[3] * ratio));
 }
 
+// The same for 8 elements of rows r0, r0 + by, ... < r1 where the scale, or the
+// ratio, is no power of two.  Functions of their own: the usual rows keep their
+// registers (with both forms in the loops a block of 16 that grew took 9.1 us
+// instead of 7.7, a chunk 4 % longer).
+template <int DT>
+__device__ __noinline__ void encode_rows_odd(uint2 *dst, const uint4 *src, long long step, int r0,
+                                             int r1, int by, float s) {
+#pragma unroll 1
+  for (int r = r0; r < r1; r += by) {
+    float f[8];
+    unpack8(src[r * step], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = div_odd(f[i], s);
+    dst[r * step] =
+        make_uint2(encode4<DT>(f[0], f[1], f[2], f[3]), encode4<DT>(f[4], f[5], f[6], f[7]));
+  }
+}
+template <int DT>
+__device__ __noinline__ void recode_rows_odd(uint2 *dst, long long step, int r0, int r1, int by,
+                                             float ratio) {
+#pragma unroll 1
+  for (int r = r0; r < r1; r += by) {
+    float a[4], b[4];
+    decode4<DT>(dst[r * step].x, a);
+    decode4<DT>(dst[r * step].y, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = mul_odd(a[i], ratio);
+      b[i] = mul_odd(b[i], ratio);
+    }
+    dst[r * step] =
+        make_uint2(encode4<DT>(a[0], a[1], a[2], a[3]), encode4<DT>(b[0], b[1], b[2], b[3]));
+  }
+}
+
 // Scale of a block for new rows with finite maximum amax; `held`: the block
-// already has rows under `old`.  *inv = 1 / scale.
+// already has rows under `old`.  *inv = 1 / scale, or 0 where the scale kept is
+// no power of two (the appends write none, a cache may come with one).
 template <int DT>
 __device__ __forceinline__ float block_scale(float amax, bool held, float old, float *inv,
                                              bool *grown) {
@@ -55,7 +91,7 @@ __device__ __forceinline__ float block_scale(float amax, bool held, float old, f
   const float need = pow2i(e);
   *grown = held && !(old >= need);
   if (held && !*grown) {
-    *inv = 1.f / old;  // exact for the powers of two that the appends write
+    *inv = is_pow2(old) ? 1.f / old : 0.f;
     return old;
   }
   *inv = pow2i(-e);
@@ -89,11 +125,12 @@ __global__ void __launch_bounds__(kKAThreads)
     const int item = i0 + threadIdx.x / LPR;
     const bool live = item < 2 * H;
     const int side = item >= H, g = item - side * H;
+    const uint4 *src = (side ? v_new : k_new) + (((long long)rel * batch + b) * H + g) * LPR + j;
     uint4 x = make_uint4(0, 0, 0, 0);
     float *sp = nullptr;
     float old = 0.f;
     if (live) {
-      x = (side ? v_new : k_new)[(((long long)rel * batch + b) * H + g) * LPR + j];
+      x = *src;
       sp = (side ? c.v_scale : c.k_scale) + scale_index(ws, c.scale_block, layer, loc, g);
       if (inside > 0) old = *sp;
     }
@@ -112,9 +149,13 @@ __global__ void __launch_bounds__(kKAThreads)
     const long long step = (long long)H * LPR;  // 8-byte words between slots
     if (grown) {
       const float ratio = old * inv;
-      for (int r = 1; r <= inside; ++r) dst[-r * step] = recode8<DT>(dst[-r * step], ratio);
+      if (is_pow2(ratio))
+        for (int r = 1; r <= inside; ++r) dst[-r * step] = recode8<DT>(dst[-r * step], ratio);
+      else
+        recode_rows_odd<DT>(dst, step, -inside, 0, 1, ratio);
     }
-    *dst = encode8<DT>(x, inv);
+    if (inv > 0.f) *dst = encode8<DT>(x, inv);
+    else encode_rows_odd<DT>(dst, src, 0, 0, 1, 1, s);
     if (j == 0 && (inside == 0 || grown)) *sp = s;
   }
 }
@@ -124,9 +165,11 @@ constexpr int kKXRows = 8;  // rows a lane keeps between the maximum and the rou
 
 // One warp per (request, block that gets rows, head, K or V): 32 / (D / 8)
 // rows side by side.  Blocks of up to kKXRows passes stay in registers between
-// the maximum and the rounding; larger ones are read a second time.
+// the maximum and the rounding; larger ones are read a second time.  Eight CTAs
+// an SM, 64 registers: with 72, which it would take, 32768 rows of 16-token
+// blocks took 42.8 us instead of 40.5.
 template <int D, int DT>
-__global__ void __launch_bounds__(kKXWarps * 32)
+__global__ void __launch_bounds__(kKXWarps * 32, 8)
     kv8_extend_append_kernel(const __grid_constant__ pkv_workspace ws,
                              const __grid_constant__ pkv_kv8 c, int batch, int layer,
                              const int *__restrict__ qo_indptr, int max_qo_len, int per_req,
@@ -198,7 +241,14 @@ __global__ void __launch_bounds__(kKXWarps * 32)
   const float s = block_scale<DT>(amax, lo > 0, old, &inv, &grown);
   if (grown) {
     const float ratio = old * inv;
-    for (int r = sub; r < lo; r += RPP) dst[r * step] = recode8<DT>(dst[r * step], ratio);
+    if (is_pow2(ratio))
+      for (int r = sub; r < lo; r += RPP) dst[r * step] = recode8<DT>(dst[r * step], ratio);
+    else
+      recode_rows_odd<DT>(dst, step, sub, lo, RPP, ratio);
+  }
+  if (inv == 0.f) {  // the scale stays as it is
+    encode_rows_odd<DT>(dst, src, step, lo + sub, hi, RPP, s);
+    return;
   }
   const bool kept = hi - lo <= kKXRows * RPP;
   for (int r0 = lo; r0 < hi; r0 += kKXRows * RPP) {

@@ -1068,3 +1068,62 @@ def test_attention_values_at_the_scale_limits(cuda, zero, S):
                     ws.lse[:2].double().cpu().numpy(), (o / zero, l, bo / zero, bl),
                     f"{zero} S={S}", F32)
     assert int(ws.err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("chunk", [False, True])
+@pytest.mark.parametrize("page,block", [(16, 16), (48, 24)])
+def test_append_to_blocks_of_other_scales(cuda, dtype, chunk, page, block):
+    # a calibrated cache is appended to: kept scales that are no powers of two, and rows
+    # whose quotients are ties between two codes, or so near to one that the quotient's
+    # own rounding to fp32 makes it one; then rows that make such blocks grow
+    ties = {"e4m3": [17.0, 8.5, 19.0, 25.0, 304.0, 2.125], "int8": [0.5, 2.5, 7.5, 12.5, 99.5, 126.5]}[dtype]
+    r = np.random.default_rng(12)
+    B, H, new = 24, 2, 3 if chunk else 1
+    before = [int(x) for x in r.integers(1, block - new + 1, B)]
+    lens = [n + new for n in before]
+    prob = _problem(lens, dtype, page, block, heads=(H, H))
+    k, v = torch.zeros((B * new, H, 128)), torch.zeros((B * new, H, 128))
+    for side, x in ((prob.k, k), (prob.v, v)):
+        for b in range(B):
+            s = prob.slots(b, 0, block)
+            pg = s[0] // page
+            for h in range(H):
+                t = ties[r.integers(len(ties))]
+                if b % 3 == 0:  # exact ties: x = t * 240, t * 224
+                    scale, x0 = [(240.0, 240 * t), (224.0, 224 * t)][b // 3 % 2]
+                    if (torch.tensor(x0).bfloat16().double() != x0).any():
+                        x0 = scale * ties[1]
+                else:
+                    x0 = float(torch.tensor(r.uniform(1, 2) * 2.0 ** r.integers(-40, 40)).bfloat16())
+                    scale = np.float32(x0 / t)
+                rows = x0 * 2.0 ** -r.integers(0, 8, (new, 128)).astype(np.float64)
+                if b % 3 == 2:  # grows to `top`: older codes of 101 or 208 land at a tie
+                    top = 2.0 ** np.floor(np.log2(x0))
+                    c, t = (101, 12.5) if dtype == "int8" else (0x75, 17.0)
+                    scale = np.float32(t * top / K8.TABLE[dtype][c])
+                    side.codes[0, s, h, ::2] = c
+                    rows[0, 0] = x0
+                    rows *= 0.75 * K8.QMAX[dtype] * top / x0
+                side.scales[0, pg, h, s[0] % page // block] = scale
+                x[b * new:(b + 1) * new, h] = torch.from_numpy(
+                    rows * r.choice([-1, 1], (new, 128))).float()
+    k, v = k.bfloat16(), v.bfloat16()
+    ws, cache = prob.device()
+    if chunk:
+        qo = torch.arange(0, B * new + 1, new, dtype=torch.int32).cuda()
+        A.pkv_kv8_extend_append(ws, cache, B, 0, qo, new, k.cuda(), v.cuda())
+    else:
+        A.pkv_kv8_append(ws, cache, B, 0, 1, k.cuda(), v.cuda())
+    kept = grown = 0
+    for b in range(B):
+        s = prob.slots(b, before[b], lens[b])
+        for side, x in ((prob.k, k), (prob.v, v)):
+            at = (0, s[0] // page, slice(None), s[0] % page // block)
+            was = side.scales[at].copy()
+            side.append(0, s, K8_values(x[b * new:(b + 1) * new]))
+            kept += int((side.scales[at] == was).sum())
+            grown += int((side.scales[at] > was).sum())
+    assert kept >= B and grown >= B // 2
+    _same(cache, prob)
+    assert int(ws.err.item()) == 0
