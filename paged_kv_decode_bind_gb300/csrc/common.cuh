@@ -215,6 +215,18 @@ __device__ __forceinline__ int checked_len(const pkv_workspace &ws, int b, int *
   return L;
 }
 
+// SMs of the current device, asked once per device.
+inline cudaError_t device_sms(int *sms) {
+  static int cache[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int &n = cache[dev & 63];
+  if (n == 0) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  *sms = n;
+  return e;
+}
+
 // Launch with programmatic dependent launch allowed (the kernels wait for
 // the previous kernel on the stream at entry).
 template <typename... KArgs, typename... Args>

@@ -3,11 +3,12 @@
 //
 // A scale is a power of two, so dividing a bf16 value by it, and reading
 // code * scale back as bf16, are exact: the only rounding is the one to the
-// code.  (A cache may come with other scales, as a calibration leaves them; blocks
-// that keep such a scale when rows are appended divide by it, rounded to odd, so
-// that the code is the one nearest to the exact quotient.)  For e4m3 a power of two costs nothing (its own exponent takes up the
+// code.  For e4m3 a power of two costs nothing (its own exponent takes up the
 // difference); for int8 it costs less than one bit against amax / 127, and
-// makes a block that grows lose at most its low bits once.
+// makes a block that grows lose at most its low bits once.  A cache may come with
+// other scales, as a calibration leaves them: rows appended to a block that keeps
+// such a scale divide by it, rounded to odd, so that the code is the one nearest
+// to the exact quotient.
 #pragma once
 
 #include "common.cuh"

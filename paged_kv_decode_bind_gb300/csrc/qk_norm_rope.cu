@@ -155,7 +155,10 @@ cudaError_t launch_one(RopeArgs a, cudaStream_t st) {
   // Warps per token: one per group of heads while that fits about one wave
   // (decode: latency counts), else as few as still give that many warps, so
   // that a token's cosines and sines are loaded once for many heads.
-  const long long wave = 152 * 32;
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  const long long wave = 32ll * sms;
   a.per_token = (int)std::min<long long>(groups, std::max<long long>(1, wave / a.n_tokens));
   const long long blocks = ((long long)a.n_tokens * a.per_token + kRWarps - 1) / kRWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;

@@ -1127,3 +1127,22 @@ def test_append_to_blocks_of_other_scales(cuda, dtype, chunk, page, block):
     assert kept >= B and grown >= B // 2
     _same(cache, prob)
     assert int(ws.err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("hkv,d", [(33, 128), (40, 128), (65, 64)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_read_wide_rows(cuda, dtype, hkv, d, f32):
+    # rows of more than 256 words of 16 codes: a thread takes several columns
+    lens = [19, 5]
+    prob = _problem(lens, dtype, heads=(hkv, hkv), d=d)
+    ws, cache = prob.device()
+    dt = torch.float32 if f32 else torch.bfloat16
+    k = torch.full((24, hkv, d), -7.0, dtype=dt, device="cuda")
+    v = torch.full_like(k, -7.0)
+    A.pkv_kv8_read(ws, cache, 2, 0, None, ws.kv_indptr, 24, k, v, A.PKV_FLAG_OUT_F32 if f32 else 0)
+    torch.cuda.synchronize()
+    for got, side in ((k, prob.k), (v, prob.v)):
+        want = np.concatenate([side.rows(0, prob.slots(b, 0, n)) for b, n in enumerate(lens)])
+        assert np.array_equal(got.double().cpu().numpy(), want)
+    assert int(ws.err.item()) == 0
