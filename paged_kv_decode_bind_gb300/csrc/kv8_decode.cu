@@ -163,29 +163,36 @@ struct KUnit {
 
 // A block's units in order.
 //
-// Shared out (S > 1): the requests, one after the other, make a line of 16-token pieces.  The blocks form groups of
-// Hkv, one block per KV head, and each group takes a run of q pieces, so every
-// block has the same number whatever the lengths are; a run that crosses the
-// end of a request becomes two units.  The heads of a token lie side by side in
-// the pool, so the blocks of a group read whole DRAM pages between them (with
-// runs over one head after the other 4 x 65536 tokens took 138 us, not 96).
-// Each request counts kUnitCost pieces more than it has, in front: what a block
-// spends on starting and finishing a unit (2 us against 0.2 us for a piece).
+// Shared out (S > 1): the requests, one after the other, make a line of 16-token
+// pieces.  The blocks form groups of Hkv, one block per KV head, and each group
+// takes a run of q pieces, so every block has the same number whatever the lengths
+// are; a run that crosses the end of a request becomes two units.  The heads of a
+// token lie side by side in the pool, so the blocks of a group read whole DRAM pages
+// between them (with runs over one head after the other 4 x 65536 tokens took
+// 138 us, not 96).  Each request counts kUnitCost pieces more than it has, in front:
+// what a block spends on starting and finishing a unit (2 us against 0.2 us for a
+// piece).
 // q = ceil(line / groups), at least 8 (one piece per warp) and at least
-// ceil(longest request / (S - 1)), so that none lies in more than S runs.
+// ceil(longest request / (S - 1)), so that none lies in more than S runs: two runs
+// may cut a request anywhere.  Few splits then leave few shares (S = 2: one request
+// whole), so where that bound is the larger one and fixed chunks, which start with
+// the request, give a block less, those are taken (65536 tokens, 8 heads: S = 2
+// 228 us, was 446, S = 3 156, was 228, S = 8 65, was 73; 64 x 8192, 2 heads, S = 2
+// 50, was 84; the decision costs a short batch 0.1 us).
 // A block keeps the line of up to kMaxCompactBatch requests in shared memory.
 // Of more it keeps where each thread's few requests start, and walks on from
-// there (300 requests of 100-900 tokens 30 us, against 49 with fixed chunks;
+// there (300 requests of 100-900 tokens 29 us, against 49 with fixed chunks;
 // tables for 1024 requests would cost the gathering form its L1: 16 flat
-// contexts 20.6 us, against 19.0).
-// Whole pairs (S == 1), or fixed chunks (fewer blocks than heads): unit u =
-// (split, request, head), every gridDim.x-th one from blockIdx.x.
+// contexts 20.6 us, against 19.0 then).
+// Whole pairs (S == 1), or fixed chunks (as above, or fewer blocks than heads):
+// unit u = (split, request, head), every gridDim.x-th one from blockIdx.x.
 constexpr int kUnitCost = 14;
 
 struct KUnits {
-  int q, pos, end, b, chunk;  // pos, end: of the line, or unit numbers
-  int at;                     // where request b starts (batches past the tables)
-  int group, head;            // the block's, where shared out
+  int q;                   // pieces of a run; 0: whole pairs or fixed chunks
+  int pos, end, b, chunk;  // pos, end: of the line, or unit numbers
+  int at;                  // where request b starts (batches past the tables)
+  int group, head;         // the block's, where shared out
 };
 
 // Pieces of a request in the line.
@@ -250,8 +257,21 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     KUnits us;
     us.group = group;
     us.head = (int)blockIdx.x - group * H;
-    us.q = max(max((run + groups - 1) / groups, 8),
-               (most - kUnitCost + a.num_splits - 2) / (a.num_splits - 1));
+    us.q = max((run + groups - 1) / groups, 8);
+    const int least = (most - kUnitCost + a.num_splits - 2) / (a.num_splits - 1);
+    if (least > us.q) {
+      us.q = least;
+      const int units = a.num_splits * a.batch * H;
+      const int chunk = split_chunk(16 * (most - kUnitCost), a.num_splits, ws.page_size);
+      const int each = (units + (int)gridDim.x - 1) / (int)gridDim.x;
+      if ((long long)each * ((chunk + 15) / 16 + kUnitCost) < least) {
+        us.q = us.b = 0;
+        us.chunk = chunk;
+        us.pos = blockIdx.x;
+        us.end = units;
+        return us;
+      }
+    }
     const long long first = group < groups ? (long long)group * us.q : run;
     us.pos = (int)min(first, (long long)run);
     us.end = (int)min(first + us.q, (long long)run);
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       __syncwarp();
       if (lane == 0 && a.apportion) {
         KUnits us = share(run, most);
-        us.b = find(a.batch, us.pos);
+        if (us.q > 0) us.b = find(a.batch, us.pos);
         s_us = us;
       }
     }
@@ -346,9 +366,11 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     __syncthreads();
     if (tid == 0) {
       KUnits us = share(run, most);
-      const int t = find(C::THREADS, us.pos);
-      us.b = t * per;
-      us.at = s_pref[t];
+      if (us.q > 0) {
+        const int t = find(C::THREADS, us.pos);
+        us.b = t * per;
+        us.at = s_pref[t];
+      }
       s_us = us;
     }
   }
@@ -377,7 +399,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
     while (us.pos < us.end) {
       ReqIndex ri;
       int L;
-      if (a.apportion) {
+      if (us.q > 0) {
         int start, last;  // the request's pieces in the line
         if (compact) {
           while (s_pref[us.b + 1] <= us.pos) ++us.b;

@@ -1146,3 +1146,26 @@ def test_read_wide_rows(cuda, dtype, hkv, d, f32):
         want = np.concatenate([side.rows(0, prob.slots(b, 0, n)) for b, n in enumerate(lens)])
         assert np.array_equal(got.double().cpu().numpy(), want)
     assert int(ws.err.item()) == 0
+
+
+@pytest.mark.parametrize("lens", [[20000], [20000, 300, 7], [9000] * 6])
+@pytest.mark.parametrize("page", [16, 1])
+@pytest.mark.parametrize("S", [2, 3, 4, 8])
+def test_splits_share_a_request_out(cuda, lens, page, S):
+    # with a query of zeros a partial's log-sum-exp is the logarithm of its tokens: few
+    # splits cut the longest request into about S equal parts, not S - 1
+    prob = _problem(lens, page=page, block=page, heads=(4, 2), d=64)
+    ws, cache = prob.device(max_splits=S)
+    B = len(lens)
+    ws.ml_part.zero_()
+    q = torch.zeros((B, 4, 64), dtype=torch.bfloat16, device="cuda")
+    A.pkv_kv8_decode_layer(ws, cache, B, 0, q, None, None, prob.p.scale, S, A.PKV_FLAG_WRITE_LSE)
+    torch.cuda.synchronize()
+    n = ws.ml_part[:B].double().cpu().numpy()
+    n = np.where(n[..., 1] > 0, np.exp(n[..., 0]), 0)  # [B, Hq, S]
+    whole = np.exp(ws.lse[:B].double().cpu().numpy())
+    assert np.abs(whole - np.array(lens)[:, None]).max() <= 0.1
+    # (a request in one piece has no partials)
+    assert np.all((np.abs(n.sum(-1) - whole) <= 0.1) | (n.sum(-1) == 0)) and n[0].all(0).any()
+    assert n[0].max() <= lens[0] / S + 16 * 20  # rounding to pages, a start's share
+    _attend(prob, ws, cache, W.normal_bf16((B, 4, 64), 77).cuda(), S, lens, what=f"{lens} {S}")
