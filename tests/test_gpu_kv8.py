@@ -1169,3 +1169,54 @@ def test_splits_share_a_request_out(cuda, lens, page, S):
     assert np.all((np.abs(n.sum(-1) - whole) <= 0.1) | (n.sum(-1) == 0)) and n[0].all(0).any()
     assert n[0].max() <= lens[0] / S + 16 * 20  # rounding to pages, a start's share
     _attend(prob, ws, cache, W.normal_bf16((B, 4, 64), 77).cuda(), S, lens, what=f"{lens} {S}")
+
+
+@pytest.mark.parametrize("form", ["fused", "unfused", "planned"])
+@pytest.mark.parametrize("page", [16, 1])
+@pytest.mark.parametrize("S", [1, 3])
+@pytest.mark.parametrize("graph", [False, True])
+def test_runner_norm_rope_on_the_bf16_cache(cuda, form, page, S, graph):
+    # whole steps with the norm and rotation in front of the bf16 cache's layers, which
+    # (fused) may start while the kernel before them runs
+    from paged_kv_decode_bind_gb300 import DecodeRunner, QkNormRope, Workspace, rope_table
+    lens, steps, layers, d = [3, 40, 700, 0], 3, 3, 128
+    B = len(lens)
+    p = W.make_problem(batch=B, n_layers=layers, n_q_heads=8, n_kv_heads=2, head_dim=d,
+                       page_size=page, seq_lens=lens, steps=steps, seed=21)
+    ws = Workspace.from_problem(p, max_splits=S)
+    table = rope_table(800, d)
+    ropes = [QkNormRope(n_q_heads=8, n_kv_heads=2, head_dim=d, cos_sin=table,
+                        q_weight=W.normal_bf16((d,), 50 + l).cuda(),
+                        k_weight=W.normal_bf16((d,), 60 + l).cuda()) for l in range(layers)]
+    run = DecodeRunner(ws, B, num_splits=S, scale=p.scale, norm_rope=ropes, out_per_layer=True,
+                       flags=A.PKV_FLAG_OUT_F32, fused=form != "unfused", plan=form == "planned")
+    if graph:
+        run.capture()
+    pools = {n: x.clone() for n, x in (("k", p.k_pool), ("v", p.v_pool))}
+    for step in range(steps):
+        q, k, v = W.step_inputs(p, step)
+        for dst, src in ((run.q_in, q), (run.k_in, k), (run.v_in, v)):
+            dst.copy_(src)
+        run.replay() if graph else run.step()
+        torch.cuda.synchronize()
+        lens = [n + 1 for n in lens]
+        for l in range(layers):
+            # the rotated rows as the kernel rounds them (its own tests bound them)
+            qr = torch.zeros((B, 8, d), dtype=torch.bfloat16, device="cuda")
+            kr = torch.zeros((B, 2, d), dtype=torch.bfloat16, device="cuda")
+            A.pkv_qk_norm_rope(ropes[l], B, run.q_in[l], run.k_in[l], ws.position_ids, qr, kr)
+            torch.cuda.synchronize()
+            got = run.outs[l].double().cpu().numpy()
+            for b, n in enumerate(lens):
+                row = p.page_table[int(p.req_pool_indices[b])].long()
+                t = torch.arange(n)
+                s = row[t // page] * page + t % page
+                pools["k"][l, s[-1]], pools["v"][l, s[-1]] = kr[b].cpu(), v[l, b]
+                kk, vv = (K8_values(pools[x][l, s]) for x in "kv")
+                o, _, mass, size, _ = K8.attention(K8_values(qr[b].cpu()), kk, vv, p.scale)
+                # scores as in Problem.attention; weights as bf16 high and low parts, 2^-17
+                dw = 2.0 ** -17 + 2 * (d + 8) * F32 * size + 2.0 ** -20
+                assert np.all(np.abs(got[b] - o) <= 2 * dw[:, None] * mass + F32 * np.abs(o))
+    for name, pool in (("k", ws.k_pool), ("v", ws.v_pool)):
+        assert torch.equal(pool.cpu(), pools[name])
+    assert int(ws.err.item()) == 0 and ws.seq_lens[:B].tolist() == lens
