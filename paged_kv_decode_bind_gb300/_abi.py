@@ -188,7 +188,7 @@ def _current_stream():
 
 def _stream(s):
     if s is None:
-        return _current_stream()
+        return (_current or _current_stream)()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -201,11 +201,14 @@ def _ws(ws):
 def _kv8(ws, cache):
     """The struct of a cache.  A Kv8Cache knows the pool shapes that it was built for:
     under a workspace of others its calls would write past its buffers."""
-    shape, w = getattr(cache, "shape", None), _ws(ws)
-    if shape is not None and w is not None and \
-            shape != (w.n_layers, w.pool_slots, w.n_kv_heads, w.head_dim, w.page_size):
-        raise ValueError("the cache was built for a workspace of other shapes: (layers, slots, "
-                         f"KV heads, head_dim, page size) {shape}")
+    shape = getattr(cache, "pool_shape", None)
+    if shape is not None and ws is not None:
+        have = getattr(ws, "pool_shape", None)
+        if have is None:  # a bare struct
+            have = (ws.n_layers, ws.pool_slots, ws.n_kv_heads, ws.head_dim, ws.page_size)
+        if shape != have:
+            raise ValueError("(layers, slots, KV heads, head_dim, page size): the cache was built "
+                             f"for {shape}, the workspace has {have}")
     return _ws(cache)
 
 

@@ -48,7 +48,7 @@ class Kv8Cache:
             return x
 
         self.dtype, self.scale_block, self.device = dtype, scale_block, ws.device
-        self.shape = (sh["n_layers"], sh["pool_slots"], H, D, P)  # calls check it against ws
+        self.pool_shape = ws.pool_shape  # calls hold it against their workspace's
         self.k_pool, self.v_pool = (own(x, codes, torch.uint8) for x in (k_pool, v_pool))
         self.k_scale, self.v_scale = (own(x, scales, torch.float32) for x in (k_scale, v_scale))
         self.struct = _abi.PkvKv8(

@@ -30,6 +30,7 @@ class Workspace:
                           index_mode=index_mode, max_batch=max_batch, max_reqs=max_reqs,
                           max_pages_per_req=max_pages_per_req, max_splits=max_splits,
                           max_total_tokens=max_total_tokens)
+        self.pool_shape = (n_layers, pool_slots, n_kv_heads, head_dim, page_size)
         kv_shape = (n_layers, pool_slots, n_kv_heads, head_dim)
         self.k_pool = torch.empty(kv_shape, dtype=torch.bfloat16, device=dev) if pools else None
         self.v_pool = torch.empty(kv_shape, dtype=torch.bfloat16, device=dev) if pools else None
