@@ -528,8 +528,8 @@ pkv_status pkv_kv8_extend_append(const pkv_workspace *ws, const pkv_kv8 *c, int 
  *   n_rows      rows that k_out and v_out hold (0: they may be NULL).
  *   k_out, v_out device bf16 [n_rows, Hkv, D] (fp32 with PKV_FLAG_OUT_F32),
  *               16-byte aligned; rows that no token maps to are left as they
- *               were.  A value is code * scale rounded once, which is exact for
- *               power-of-two scales.
+ *               were.  A value is the fp32 product code * scale, rounded to bf16:
+ *               exact for power-of-two scales.
  *   flags       PKV_FLAG_OUT_F32; PKV_FLAG_PLAN_EARLY (lengths, starts, dst_indptr
  *               and index entries are as old as that flag asks; codes, scales and
  *               the outputs wait for the previous launch).
@@ -556,6 +556,15 @@ pkv_status pkv_kv8_read(const pkv_workspace *ws, const pkv_kv8 *c, int batch, in
  *               PKV_FLAG_TEST_SKIP_FIRST_TILE (no effect where TMA boxes do not
  *               apply).
  * The partial of a split holds its (normalised output, log-sum-exp, 1).
+ * Precision: codes, scales and q (to 2^-28 of its head's largest element) enter the
+ * products exactly; sums and the softmax's statistics are fp32.  A weight
+ * exp(s_t - m) v_scale_t is rounded to fp16 for its product with the codes, 2^-11 of
+ * itself: an eighth of a bf16 output's half step, but what an fp32 output or a partial
+ * may be off (the bf16 cache's kernels keep their weights to 2^-17).  A weight below
+ * 2^-21 of the request's largest is off by up to 2^-32 of that one; by 2^-12 where all
+ * value scales that count are 2^-100, the smallest.  Scores s_t / ln 2 are to lie
+ * within 2^26 in size; splits are weighed by fp32 log-sum-exps, 2^-23 of their size
+ * exact, as the scores themselves are at best.
  * Host errors: as pkv_decode_layer and pkv_kv8_append; PKV_ERR_INVALID for
  * another flag; PKV_ERR_UNSUPPORTED for G not in {1, 2, 4, 8, 16}.
  */

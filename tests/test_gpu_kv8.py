@@ -1216,7 +1216,42 @@ def test_runner_norm_rope_on_the_bf16_cache(cuda, form, page, S, graph):
                 o, _, mass, size, _ = K8.attention(K8_values(qr[b].cpu()), kk, vv, p.scale)
                 # scores as in Problem.attention; weights as bf16 high and low parts, 2^-17
                 dw = 2.0 ** -17 + 2 * (d + 8) * F32 * size + 2.0 ** -20
-                assert np.all(np.abs(got[b] - o) <= 2 * dw[:, None] * mass + F32 * np.abs(o))
+                tol = 2 * dw[:, None] * mass + F32 * np.abs(o)
+                assert (np.abs(got[b] - o) - tol).max() <= 0
     for name, pool in (("k", ws.k_pool), ("v", ws.v_pool)):
         assert torch.equal(pool.cpu(), pools[name])
     assert int(ws.err.item()) == 0 and ws.seq_lens[:B].tolist() == lens
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_scores_at_their_limit(cuda, sign):
+    # scores near 2^26 (in powers of two), a few tokens tied at the top of each request
+    # whose value scales lie far apart: their average.  (One split: several are weighed
+    # by log-sum-exps that fp32 holds in steps of 4 here.)
+    lens = [900, 70]
+    prob = _problem(lens, "int8", heads=(2, 1), d=64)
+    prob.k.codes[...] = 0
+    prob.k.scales[...] = 2.0 ** 21
+    prob.v.scales[...] = 2.0 ** np.random.default_rng(6).integers(-30, 31, prob.v.scales.shape)
+    for b, n in enumerate(lens):
+        s = prob.slots(b, 0, n)
+        prob.k.codes[0, s, 0, 0] = 0x81  # -127
+        prob.k.codes[0, s[[3, n // 2, n - 2]], 0, 0] = 127 if sign > 0 else 0x82  # -126
+    prob.p.scale = 0.125
+    q = torch.zeros((2, 2, 64), dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    ws, cache = prob.device()
+    A.pkv_kv8_decode_layer(ws, cache, 2, 0, q.cuda(), None, None, prob.p.scale, 1,
+                           A.PKV_FLAG_OUT_F32)
+    torch.cuda.synchronize()
+    got = ws.out_f32(2).double().cpu().numpy()
+    for b, n in enumerate(lens):
+        s = prob.slots(b, 0, n)
+        o, _, mass, _, floor = K8.attention(K8_values(q)[b], prob.k.rows(0, s), prob.v.rows(0, s),
+                                            prob.p.scale, prob.v.scale_of(0, s))
+        # equal scores are equal in fp32 too, so the weights are off by their rounding to
+        # fp16 alone; r is in steps of 4, so the largest weight is at least 2^3 and the
+        # smallest step 2^-25 at most 2^-28 of it
+        tol = 2 * 2.0 ** -11 * mass + 2.0 ** -28 * floor + 4 * F32 * np.abs(o)
+        assert (np.abs(got[b] - o) - tol).max() <= 0
+    assert int(ws.err.item()) == 0
