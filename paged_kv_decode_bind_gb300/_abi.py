@@ -364,30 +364,33 @@ def _heads(x, width, head_dim, rows=0):
     """Pointer and elements between tokens of x: a pointer or None is dense; a
     tensor is bf16 [tokens, width] or [tokens, heads, head_dim] with dense heads and
     at least `rows` tokens."""
-    if x is None or isinstance(x, int):
+    try:
+        st = x.stride()
+    except AttributeError:
         return x, width
-    st, n, ok = x.stride(), 0, False
     if len(st) == 2:
         n, w = x.shape
         ok = w == width and st[1] == 1
     elif len(st) == 3:
         n, h, d = x.shape
         ok = d == head_dim and h * d == width and st[2] == 1 and (st[1] == d or h <= 1)
-    if not ok or n < rows or x.dtype is not _BF16:
-        raise ValueError(f"expected bf16 [tokens >= {rows}, {width}] or [tokens, heads, {head_dim}] "
-                         f"with dense heads, got {x.dtype} {tuple(x.shape)} with strides {st}")
-    # the stride of a single token may be anything
-    return x.data_ptr(), width if st[0] < width and n <= 1 else st[0]
+    else:
+        n, ok = 0, False
+    if ok and n >= rows and x.dtype is _BF16:
+        # the stride of a single token may be anything
+        return x.data_ptr(), st[0] if st[0] >= width or n > 1 else width
+    raise ValueError(f"expected bf16 [tokens >= {rows}, {width}] or [tokens, heads, {head_dim}] "
+                     f"with dense heads, got {x.dtype} {tuple(x.shape)} with strides {st}")
 
 
 def _positions(x, rows):
     """Pointer of the int32 positions of at least `rows` tokens."""
     if x is None or isinstance(x, int):
         return x
-    if x.dtype is not _INT32 or x.numel() < rows or not x.is_contiguous():
-        raise ValueError(f"positions are dense int32 [tokens >= {rows}], got {x.dtype} "
-                         f"{tuple(x.shape)}")
-    return x.data_ptr()
+    if x.dtype is _INT32 and x.numel() >= rows and x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError(f"positions are dense int32 [tokens >= {rows}], got {x.dtype} "
+                     f"{tuple(x.shape)}")
 
 
 def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None, check=True):
@@ -399,10 +402,13 @@ def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None,
     D, qw, kw = getattr(args, "widths", None) or \
         (st.head_dim, st.n_q_heads * st.head_dim, st.n_kv_heads * st.head_dim)
     n = n_tokens
-    s = load().pkv_qk_norm_rope(st, n, *_heads(q, qw, D, n), *_heads(k, kw, D, n),
-                                _positions(positions, n), *_heads(q_out, qw, D, n),
-                                *_heads(k_out, kw, D, n), _stream(stream))
-    return _check("pkv_qk_norm_rope", s) if check else s
+    qp, qs = _heads(q, qw, D, n)
+    kp, ks = _heads(k, kw, D, n)
+    qo, qos = _heads(q_out, qw, D, n)
+    ko, kos = _heads(k_out, kw, D, n)
+    s = (_lib or load()).pkv_qk_norm_rope(st, n, qp, qs, kp, ks, _positions(positions, n), qo, qos,
+                                          ko, kos, _stream(stream))
+    return _check("pkv_qk_norm_rope", s) if check and s else s
 
 
 def pkv_is_steady_increment(prev_ids, prev_lens, ids, lens) -> bool:
