@@ -43,14 +43,14 @@
 // their way; the splits of a request meet in the block that finishes last (an
 // atomic ticket).
 //
-// Measured (GB300, 2070 MHz; a pass in a graph): 4 x 65536 tokens, 32/8 heads
-// 89 us, 6.0 TB/s, 91 % of the copy rate; 64 x 1024-4096, 16/2 heads 23.7 us,
-// 3.3 TB/s; 16 flat contexts of 1-8192, 19.4 us, 2.3 TB/s; 4 x 512-2048 9.1 us.
-// The bound of the long case is the warps' own latency (356 instructions a
-// piece for e4m3, four warps a scheduler, IPC 2.2; they wait for data in 8 of
-// 86 us), that of the short ones the chain lengths - page ids - tile - meeting -
-// ticket - merge.  Two stages beat three (94 against 96 us, flat 20.5 against
-// 23.7): the first tile does not wait behind two more.
+// Measured (GB300, 2070 MHz; a pass in a graph): 4 x 65536 tokens, 32/8 heads, int8
+// 91 us, 5.9 TB/s, 88 % of the copy rate (e4m3 90 us); 64 x 1024-4096, 16/2 heads
+// 23.9 us, 3.3 TB/s; 16 flat contexts of 1-8192, 19.3 us, 2.3 TB/s; 4 x 512-2048
+// 9.3 us.  The bound of the long case is the warps' own latency (353 instructions a
+// piece for e4m3, 449 for int8, four warps a scheduler, IPC 2.0 for int8; they waited
+// for data in 8 of 86 us), that of the short ones the chain lengths - page ids -
+// tile - meeting - ticket - merge.  Two stages beat three (94 against 96 us, flat 20.5
+// against 23.7 when that was measured): the first tile does not wait behind two more.
 #include <cuda.h>
 
 #include <cstring>
@@ -171,7 +171,11 @@ struct KUnit {
 // between them (with runs over one head after the other 4 x 65536 tokens took
 // 138 us, not 96).  Each request counts kUnitCost pieces more than it has, in front:
 // what a block spends on starting and finishing a unit (2 us against 0.2 us for a
-// piece).
+// piece, D = 128 and up to 8 heads).  The same 14 for all shapes: of 4, 8, 14, 20 and
+// 28 it is within 4 % of the best for each (16 flat contexts 24.3 / 21.3 / 19.4 / 19.7
+// / 20.3 us, 4 x 512-2048 11.7 / 9.3 / 9.3 / 9.3 / 9.8, 64 x 1024-4096 24.5 / 24.1 /
+// 23.8 / 23.0 / 22.5, with 16 heads a group 31.3 / 30.9 / 29.9 / 29.2 / 29.6, with
+// D = 64 20.2 / 19.8 / 19.2 / 19.1 / 18.6).
 // q = ceil(line / groups), at least 8 (one piece per warp) and at least
 // ceil(longest request / (S - 1)), so that none lies in more than S runs: two runs
 // may cut a request anywhere.  Few splits then leave few shares (S = 2: one request
