@@ -558,13 +558,11 @@ pkv_status pkv_kv8_read(const pkv_workspace *ws, const pkv_kv8 *c, int batch, in
  * The partial of a split holds its (normalised output, log-sum-exp, 1).
  * Precision: codes, scales and q (to 2^-28 of its head's largest element) enter the
  * products exactly; sums and the softmax's statistics are fp32.  A weight
- * exp(s_t - m) v_scale_t is rounded to fp16 for its product with the codes, 2^-11 of
- * itself: an eighth of a bf16 output's half step, but what an fp32 output or a partial
- * may be off (the bf16 cache's kernels keep their weights to 2^-17).  A weight below
- * 2^-21 of the request's largest is off by up to 2^-32 of that one; by 2^-12 where all
- * value scales that count are 2^-100, the smallest.  Scores s_t / ln 2 are to lie
- * within 2^26 in size; splits are weighed by fp32 log-sum-exps, 2^-23 of their size
- * exact, as the scores themselves are at best.
+ * exp(s_t - m) v_scale_t enters its product with the codes as two fp16 parts, 2^-20 of
+ * itself exact.  A weight below 2^-12 of the request's largest is off by up to 2^-32 of
+ * that one; by 2^-12 where all value scales that count are 2^-100, the smallest.
+ * Scores s_t / ln 2 are to lie within 2^26 in size; splits are weighed by fp32
+ * log-sum-exps, 2^-23 of their size exact, as the scores themselves are at best.
  * Host errors: as pkv_decode_layer and pkv_kv8_append; PKV_ERR_INVALID for
  * another flag; PKV_ERR_UNSUPPORTED for G not in {1, 2, 4, 8, 16}.
  */

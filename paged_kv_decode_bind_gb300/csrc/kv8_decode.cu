@@ -13,15 +13,22 @@
 //   x_t = (q . code_k,t) * k_scale_t * scale,  and its weight in O
 //   w_t = exp(x_t - r) * v_scale_t,
 // with a reference r that follows max(x_t + ln max(v_scale_t, 2^-80)): the
-// largest w_t is then 2^7 .. 2^15, which fp16 holds whatever the value scales
+// largest w_t is then 2^8 .. 2^16, which fp16 holds whatever the value scales
 // are, while the softmax sum  l = sum exp(x_t - r)  stays in fp32.  out = O / l.
 // The floor of 2^-80 is for l: a block of zeros has v_scale = 2^-100, and terms
-// of 2^115 each would pass fp32's range from 8192 such tokens on; no term is
-// now above 2^95, so 2^31 tokens stay below 2^126.  Rounding w to fp16 costs
-// 2^-11 of a weight, an eighth of what the bf16 output's own rounding may cost
-// (weights under 2^-21 of the largest: 2^-32 of the largest; where all value
-// scales that count lie below 2^-80, that is 2^-12, at 2^-100).
-// r moves only when a weight (at the floored scale) would pass 2^15, so most
+// of 2^116 each would pass fp32's range from 4096 such tokens on; no term is
+// now above 2^96, so 2^31 tokens stay below 2^127.
+//
+// w goes into the product as two fp16 parts, what fp16 towards zero keeps and
+// what that leaves, 2^-20 of w together (weights under 2^-12 of the largest: 2^-32
+// of the largest; where all value scales that count lie below 2^-80, that is
+// 2^-12, at 2^-100).  One part, 2^-11, put as many bf16 outputs on the other side
+// of a rounding step as 0.0008 of their size, and showed in fp32 outputs.  Up to
+// four heads a group leave half the columns of the product empty: the low parts
+// go there for 8 instructions a piece, the queries standing in Q^T twice.  Eight
+// and sixteen heads take a second product (4 x 65536 tokens, 4 heads a group 91.4 us,
+// 91.1 with one part; 64 x 1024-4096, 8 heads 24.0 and 23.8, 16 heads 31.1 and 29.7).
+// r moves only when a weight (at the floored scale) would pass fp16's range, so most
 // tokens need one vote instead of a maximum over lanes and a rescaling of O.
 //
 // Data.  Each warp takes every W-th piece of 16 tokens of the unit and fills
@@ -44,9 +51,8 @@
 // atomic ticket).
 //
 // Measured (GB300, 2070 MHz; a pass in a graph): 4 x 65536 tokens, 32/8 heads, int8
-// 91 us, 5.9 TB/s, 88 % of the copy rate (e4m3 90 us); 64 x 1024-4096, 16/2 heads
-// 23.9 us, 3.3 TB/s; 16 flat contexts of 1-8192, 19.3 us, 2.3 TB/s; 4 x 512-2048
-// 9.3 us.  The bound of the long case is the warps' own latency (353 instructions a
+// 91 us, 5.9 TB/s, 88 % of the copy rate; 64 x 1024-4096, 16/2 heads 24.0 us,
+// 3.3 TB/s; 16 flat contexts of 1-8192, 19.6 us, 2.3 TB/s; 4 x 512-2048 9.5 us.  The bound of the long case is the warps' own latency (353 instructions a
 // piece for e4m3, 449 for int8, four warps a scheduler, IPC 2.0 for int8; they waited
 // for data in 8 of 86 us), that of the short ones the chain lengths - page ids -
 // tile - meeting - ticket - merge.  Two stages beat three (94 against 96 us, flat 20.5
@@ -67,6 +73,9 @@ namespace {
 template <int D, int G>
 struct KCfg {
   static constexpr int NH = (G + 7) / 8;           // 8-wide head tiles
+  // the weights' low parts: in the columns G .. 2 G - 1 of the head tile, or in
+  // products of their own
+  static constexpr bool LOCOL = G <= 4;
   // warps (16 heads: twice the registers); one block of sixteen was no faster
   // (93.0 against 93.5 us at 4 x 65536, 25.4 against 23.6 at 64 x 1024-4096)
   static constexpr int W = NH == 1 ? 8 : 4;
@@ -103,6 +112,20 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same, towards zero.
+__device__ __forceinline__ uint32_t pack_f16x2_rz(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// x without its first 11 bits (those that fp16 towards zero keeps) where `mask` is
+// kHighBits, x itself where it is 0.
+constexpr uint32_t kHighBits = 0xffffe000u;
+__device__ __forceinline__ float low_part(float x, uint32_t mask) {
+  return x - __uint_as_float(__float_as_uint(x) & mask);
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -212,7 +235,7 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   using C = KCfg<D, G>;
   constexpr int W = C::W, NS = C::NS, NH = C::NH;
   // log2 of the largest weight where r is placed, and the weight at which it moves
-  constexpr float kPlace = 7.f, kMove = 32768.f;
+  constexpr float kPlace = 8.f, kMove = 65504.f;  // fp16's largest number
   constexpr float kScaleFloor = 8.271806125530277e-25f;  // 2^-80
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[PAGED ? W : 1][NS];
@@ -493,6 +516,8 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   const int tv0 = perm<D>(2 * c), tv1 = perm<D>(2 * c + 1);
   const int voff0 = C::KB + (D == 128 ? swz<D>(tv0, r) : swz<D>(tv0, r >> 1) + (r & 1) * 8);
   const int voff1 = C::KB + (D == 128 ? swz<D>(tv1, r) : swz<D>(tv1, r >> 1) + (r & 1) * 8);
+  // LOCOL: this lane's heads 2 c and 2 c + 1 are high or low parts
+  const uint32_t lo0 = 2 * c >= G ? kHighBits : 0, lo1 = 2 * c + 1 >= G ? kHighBits : 0;
   int st_in = 0, st_out = 0, ph_out = 0;  // ring positions: next to fill, next to read
   bool dead = false;                      // a wait of this warp ran out
 
@@ -645,7 +670,9 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
   fill(NS - 2);  // the last stage follows in the unit's first step
 
   // Q^T as the B operand: lane r is head r (+ 8), its 16 elements 64 x + 16 c ..
-  // 64 x + 16 c + 15 of each half x match the K bytes the lane reads.
+  // 64 x + 16 c + 15 of each half x match the K bytes the lane reads.  With LOCOL
+  // columns G .. 2 G - 1 are the same heads again: scores and reference come out the
+  // same, their weights go into the second product as low parts.
   uint4 qraw[NH][D / 32];
   auto load_q = [&](const KUnit &u) {
 #pragma unroll
@@ -653,10 +680,11 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
       const int h = r + 8 * n;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
-        qraw[n][i] = h < G ? reinterpret_cast<const uint4 *>(
-                                 a.q)[((long long)u.b * Hq + u.g * G + h) * (D / 8) +
-                                      8 * (i >> 1) + 2 * c + (i & 1)]
-                           : make_uint4(0, 0, 0, 0);
+        qraw[n][i] = h < (C::LOCOL ? 2 * G : G)
+                         ? reinterpret_cast<const uint4 *>(
+                               a.q)[((long long)u.b * Hq + u.g * G + h % G) * (D / 8) +
+                                    8 * (i >> 1) + 2 * c + (i & 1)]
+                         : make_uint4(0, 0, 0, 0);
     }
   };
   wait_previous();  // q comes from the previous kernel
@@ -814,13 +842,21 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
           weigh();
         }
         uint32_t wb[NH][2];  // W^T as B: tokens of rows 0-7 / 8-15
+        uint32_t wl[C::LOCOL ? 1 : NH][2];  // its low parts
 #pragma unroll
         for (int n = 0; n < NH; ++n)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             l_run[n][0] += p[n][2 * t];
             l_run[n][1] += p[n][2 * t + 1];
-            wb[n][t] = movmatrix_t(pack_f16x2(p[n][2 * t] * vs[t], p[n][2 * t + 1] * vs[t]));
+            const float w0 = p[n][2 * t] * vs[t], w1 = p[n][2 * t + 1] * vs[t];
+            if constexpr (C::LOCOL) {
+              wb[n][t] = movmatrix_t(pack_f16x2_rz(low_part(w0, lo0), low_part(w1, lo1)));
+            } else {
+              wb[n][t] = movmatrix_t(pack_f16x2_rz(w0, w1));
+              wl[n][t] = movmatrix_t(
+                  pack_f16x2_rz(low_part(w0, kHighBits), low_part(w1, kHighBits)));
+            }
           }
         // ---- O^T += V^T W^T ----
         uint32_t v[4][C::VB / 4];
@@ -852,8 +888,11 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
             codes_f16<DT>(__byte_perm(v[0][w], v[1][w], sel), a0, a1);
             codes_f16<DT>(__byte_perm(v[2][w], v[3][w], sel), a2, a3);
 #pragma unroll
-            for (int n = 0; n < NH; ++n)
+            for (int n = 0; n < NH; ++n) {
               mma_f16(acc[n][2 * w + hlf], a0, a1, a2, a3, wb[n][0], wb[n][1]);
+              if constexpr (!C::LOCOL)
+                mma_f16(acc[n][2 * w + hlf], a0, a1, a2, a3, wl[n][0], wl[n][1]);
+            }
           }
         }
         if (++st_out == NS) {
@@ -918,7 +957,12 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
           M = fmaxf(M, ml[w].x);
         }
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int sx = D == 128 ? (((d >> 5) & 1) << 1) | ((h8 >> 1) << 2) : (h8 >> 1) << 1;
+        // 4 floats of row hh, column d of a warp's O
+        auto take = [&](const uint8_t *o, int hh) {
+          const int sx = D == 128 ? (((d >> 5) & 1) << 1) | ((hh >> 1) << 2) : (hh >> 1) << 1;
+          const float4 y = *reinterpret_cast<const float4 *>(o + (hh * D + (d ^ (sx & ~3))) * 4);
+          return sx & 2 ? make_float4(y.z, y.w, y.x, y.y) : y;
+        };
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const int slot = s_slot[w];
@@ -927,13 +971,16 @@ __global__ void __launch_bounds__(KCfg<D, G>::THREADS, 2)
           // passes its NaN on
           const float f = ml[w].x == -INFINITY ? 1.f : fast_exp2(ml[w].x - M);
           L += f * ml[w].y;
-          const float4 y = *reinterpret_cast<const float4 *>(
-              smem + (w * NS + slot) * C::STAGE + (h8 * D + (d ^ (sx & ~3))) * 4);
-          const bool sw = sx & 2;
-          x.x = fmaf(f, sw ? y.z : y.x, x.x);
-          x.y = fmaf(f, sw ? y.w : y.y, x.y);
-          x.z = fmaf(f, sw ? y.x : y.z, x.z);
-          x.w = fmaf(f, sw ? y.y : y.w, x.w);
+          const uint8_t *o = smem + (w * NS + slot) * C::STAGE;
+          float4 y = take(o, h8);
+          if constexpr (C::LOCOL) {
+            const float4 z = take(o, h8 + G);
+            y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+          }
+          x.x = fmaf(f, y.x, x.x);
+          x.y = fmaf(f, y.y, x.y);
+          x.z = fmaf(f, y.z, x.z);
+          x.w = fmaf(f, y.w, x.w);
         }
         const float inv = 1.f / L;
         x = unit_bad ? make_float4(0.f, 0.f, 0.f, 0.f)

@@ -1021,6 +1021,15 @@ def _rising_scores(lens, hq, tail, zero):
     return prob, q
 
 
+def _far(scale):
+    """What lse may be off besides Problem.attention's bound where the value scales lie far
+    from 1.  The reference r is as large as far = 8 + |log2 scale| + 8 (place, scale,
+    scores): the subtraction x - r rounds by half a step of that, and so do both terms of
+    lse = r ln 2 + log(sum): ln 2 itself and the product (1.5 half steps), the logarithm
+    (2 half steps)."""
+    return 5 * F32 * (16 + abs(np.log2(max(scale, 2.0 ** -80)))) * np.log(2)
+
+
 @pytest.mark.parametrize("n,hq", [(20000, 2), (20000, 16), (150000, 2)])
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("S", [1, 2, 5])
@@ -1029,8 +1038,14 @@ def test_attention_long_runs_of_zero_values(cuda, n, hq, tail, S):
     # within a warp (150000: over 9000 tokens each), a unit and a merge
     prob, q = _rising_scores([n, 40], hq, tail, 2.0 ** -100)
     ws, cache = prob.device(max_splits=S)
-    got = _attend(prob, ws, cache, q.cuda(), S, [n, 40], A.PKV_FLAG_OUT_F32, what=f"{n} S={S}")
-    assert got.any() == tail
+    A.pkv_kv8_decode_layer(ws, cache, 2, 0, q.cuda(), None, None, prob.p.scale, S,
+                           A.PKV_FLAG_WRITE_LSE | A.PKV_FLAG_OUT_F32)
+    torch.cuda.synchronize()
+    got = ws.out_f32(2).double().cpu().numpy()
+    o, l, bo, bl = prob.attention(0, q, [n, 40])
+    check_attention(got, ws.lse[:2].double().cpu().numpy(), (o, l, bo, bl + _far(2.0 ** -100)),
+                    f"{n} S={S}", F32)
+    assert got.any() == tail and int(ws.err.item()) == 0
 
 
 @pytest.mark.parametrize("zero", [2.0 ** -100, 2.0 ** -81, 2.0 ** -80, 2.0 ** -60, 2.0 ** 100])
@@ -1047,23 +1062,18 @@ def test_attention_values_at_the_scale_limits(cuda, zero, S):
                            A.PKV_FLAG_WRITE_LSE | A.PKV_FLAG_OUT_F32)
     torch.cuda.synchronize()
     o, l, bo, bl = prob.attention(0, q, lens)
-    # the reference r is as large as far = 7 + |log2 scale| + 8 (place, scale, scores):
-    # the subtraction x - r rounds by half a step of that, and so do both terms of
-    # lse = r ln 2 + log(sum): ln 2 itself and the product (1.5 half steps), the
-    # logarithm (2 half steps)
-    far = 15 + abs(np.log2(max(zero, 2.0 ** -80)))
-    bl += 5 * F32 * far * np.log(2)
+    bl += _far(zero)
     if zero < 2.0 ** -80:
         # the reference counts these scales as 2^-80, so a warp's largest weight is at
-        # least 2^7 zero / 2^-80, and a weight below fp16's normal range is off by
-        # 2^-25: over all tokens 2^-25 / (2^87 zero) of the largest p_t v_scale_t, times
+        # least 2^8 zero / 2^-80, and a weight below fp16's normal range is cut off at
+        # 2^-24: over all tokens 2^-24 / (2^88 zero) of the largest p_t v_scale_t, times
         # sum_t |code_t| (2 %: the query is rounded, the scores rise by 5.5 / 2^8 more)
         codes = [np.abs(prob.v.rows(0, prob.slots(b, 0, n)) / zero).sum(0) for b, n in
                  enumerate(lens)]
         for b, n in enumerate(lens):
             x = np.where(np.arange(n) < 128, 0, 5.5)
             top = zero / np.exp(x - x.max()).sum()  # the largest p_t v_scale_t
-            bo[b] += 2.0 ** -25 / (2.0 ** 87 * zero) * 1.02 * top * codes[b]
+            bo[b] += 2.0 ** -24 / (2.0 ** 88 * zero) * 1.02 * top * codes[b]
     check_attention(ws.out_f32(2).double().cpu().numpy() / zero,
                     ws.lse[:2].double().cpu().numpy(), (o / zero, l, bo / zero, bl),
                     f"{zero} S={S}", F32)
@@ -1249,9 +1259,38 @@ def test_attention_scores_at_their_limit(cuda, sign):
         s = prob.slots(b, 0, n)
         o, _, mass, _, floor = K8.attention(K8_values(q)[b], prob.k.rows(0, s), prob.v.rows(0, s),
                                             prob.p.scale, prob.v.scale_of(0, s))
-        # equal scores are equal in fp32 too, so the weights are off by their rounding to
-        # fp16 alone; r is in steps of 4, so the largest weight is at least 2^3 and the
-        # smallest step 2^-25 at most 2^-28 of it
-        tol = 2 * 2.0 ** -11 * mass + 2.0 ** -28 * floor + 4 * F32 * np.abs(o)
+        # equal scores are equal in fp32 too, so the weights are off by their two fp16
+        # parts alone; r is in steps of 4, so the largest weight is at least 2^4 and the
+        # smallest step 2^-24 at most 2^-28 of it
+        tol = 2 * 2.0 ** -20 * mass + 2.0 ** -28 * floor + 4 * F32 * np.abs(o)
         assert (np.abs(got[b] - o) - tol).max() <= 0
+    assert int(ws.err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("heads", [(2, 2), (4, 2), (8, 2), (16, 2), (32, 2)])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (128, 1), (64, 8)])
+def test_attention_weights_keep_their_low_parts(cuda, dtype, heads, d, page):
+    # fp32 outputs: a weight is a high and a low fp16 part, each cut off after 11 bits
+    # (2^-20 of it in all), of a smallest step 2^-24 where the largest is at least 2^8
+    lens = [700, 33, 5]
+    prob = _problem(lens, dtype, page, page, heads=heads, d=d, outlier=0.01)
+    prob.v.scales[...] *= 2.0 ** np.random.default_rng(3).integers(-3, 4, prob.v.scales.shape)
+    ws, cache = prob.device(max_splits=3)
+    q = W.normal_bf16((3, heads[0], d), 88)
+    for S in (1, 3):
+        A.pkv_kv8_decode_layer(ws, cache, 3, 0, q.cuda(), None, None, prob.p.scale, S,
+                               A.PKV_FLAG_OUT_F32)
+        torch.cuda.synchronize()
+        got = ws.out_f32(3).double().cpu().numpy()
+        for b, n in enumerate(lens):
+            s = prob.slots(b, 0, n)
+            o, _, mass, size, floor = K8.attention(
+                K8_values(q)[b], prob.k.rows(0, s), prob.v.rows(0, s), prob.p.scale,
+                prob.v.scale_of(0, s))
+            # scores and exponentials as in Problem.attention; the sums of n products in
+            # fp32 (n / 16 of them in a row, then the warps')
+            dw = 2.0 ** -20 + 2 * (d + 8) * F32 * size + 2.0 ** -20 + (n / 16 + 16) * F32
+            tol = 2 * dw[:, None] * mass + 2.0 ** -32 * floor + F32 * np.abs(o)
+            assert (np.abs(got[b] - o) - tol).max() <= 0
     assert int(ws.err.item()) == 0
