@@ -25,7 +25,7 @@
 // 2^-12, at 2^-100).  One part, 2^-11, put as many bf16 outputs on the other side
 // of a rounding step as 0.0008 of their size, and showed in fp32 outputs.  Up to
 // four heads a group leave half the columns of the product empty: the low parts
-// go there for 8 instructions a piece, the queries standing in Q^T twice.  Eight
+// go there for 11 instructions a piece, the queries standing in Q^T twice.  Eight
 // and sixteen heads take a second product (4 x 65536 tokens, 4 heads a group 91.4 us,
 // 91.1 with one part; 64 x 1024-4096, 8 heads 24.0 and 23.8, 16 heads 31.1 and 29.7).
 // r moves only when a weight (at the floored scale) would pass fp16's range, so most
@@ -37,8 +37,8 @@
 // the 16-byte chunks swizzled (TMA's 128- or 64-byte pattern).  Pages of whole
 // pieces come as one TMA box for K and one for V, completing on the stage's
 // mbarrier; other page sizes and flat indices as 16-byte cp.async copies of
-// the rows (whole rows per 8 or 4 lanes), the index entries NS pieces ahead.  Fragments are read with plain
-// 16-byte loads: which token a row of S^T is, and which head_dim an index of
+// the rows (whole rows per 8 or 4 lanes), the index entries NS pieces ahead.
+// Fragments are read with plain 16-byte loads: which token a row of S^T is, and which head_dim an index of
 // the contraction is, is free as long as V and Q agree.  K: lane (r = lane / 4,
 // c = lane % 4) takes 16 bytes of token perm(r); V: 16 (8 at D = 64) bytes of
 // the tokens perm(2 c), perm(2 c + 1) (+ 8), whose bytes one byte permute per
@@ -52,11 +52,13 @@
 //
 // Measured (GB300, 2070 MHz; a pass in a graph): 4 x 65536 tokens, 32/8 heads, int8
 // 91 us, 5.9 TB/s, 88 % of the copy rate; 64 x 1024-4096, 16/2 heads 24.0 us,
-// 3.3 TB/s; 16 flat contexts of 1-8192, 19.6 us, 2.3 TB/s; 4 x 512-2048 9.5 us.  The bound of the long case is the warps' own latency (353 instructions a
-// piece for e4m3, 449 for int8, four warps a scheduler, IPC 2.0 for int8; they waited
-// for data in 8 of 86 us), that of the short ones the chain lengths - page ids -
-// tile - meeting - ticket - merge.  Two stages beat three (94 against 96 us, flat 20.5
-// against 23.7 when that was measured): the first tile does not wait behind two more.
+// 3.3 TB/s; 16 flat contexts of 1-8192, 19.6 us, 2.3 TB/s; 4 x 512-2048 9.5 us.
+// The bound of the long case is the warps' own latency (364 instructions a piece for
+// e4m3, 460 for int8 at four heads a group, four warps a scheduler, IPC 2.0 for int8;
+// they waited for data in 8 of 86 us), that of the short ones the chain lengths -
+// page ids - tile - meeting - ticket - merge.  Two stages beat three (94 against
+// 96 us, flat 20.5 against 23.7 when that was measured): the first tile does not
+// wait behind two more.
 #include <cuda.h>
 
 #include <cstring>
@@ -194,18 +196,18 @@ struct KUnit {
 // between them (with runs over one head after the other 4 x 65536 tokens took
 // 138 us, not 96).  Each request counts kUnitCost pieces more than it has, in front:
 // what a block spends on starting and finishing a unit (2 us against 0.2 us for a
-// piece, D = 128 and up to 8 heads).  The same 14 for all shapes: of 4, 8, 14, 20 and
-// 28 it is within 4 % of the best for each (16 flat contexts 24.3 / 21.3 / 19.4 / 19.7
-// / 20.3 us, 4 x 512-2048 11.7 / 9.3 / 9.3 / 9.3 / 9.8, 64 x 1024-4096 24.5 / 24.1 /
-// 23.8 / 23.0 / 22.5, with 16 heads a group 31.3 / 30.9 / 29.9 / 29.2 / 29.6, with
-// D = 64 20.2 / 19.8 / 19.2 / 19.1 / 18.6).
+// piece, D = 128 and up to 8 heads).  One number for all shapes: of 4, 8, 14, 20 and
+// 28, 14 was within 6 % of the best for each and 20 within 3 (16 flat contexts 24.3 /
+// 21.3 / 19.4 / 19.7 / 20.3 us, 4 x 512-2048 11.7 / 9.3 / 9.3 / 9.3 / 9.8, 64 x
+// 1024-4096 24.5 / 24.1 / 23.8 / 23.0 / 22.5, with 16 heads a group 31.3 / 30.9 / 29.9
+// / 29.2 / 29.6, with D = 64 20.2 / 19.8 / 19.2 / 19.1 / 18.6).
 // q = ceil(line / groups), at least 8 (one piece per warp) and at least
 // ceil(longest request / (S - 1)), so that none lies in more than S runs: two runs
 // may cut a request anywhere.  Few splits then leave few shares (S = 2: one request
 // whole), so where that bound is the larger one and fixed chunks, which start with
 // the request, give a block less, those are taken (65536 tokens, 8 heads: S = 2
-// 228 us, was 446, S = 3 156, was 228, S = 8 65, was 73; 64 x 8192, 2 heads, S = 2
-// 50, was 84; the decision costs a short batch 0.1 us).
+// 233 us, was 446, S = 3 161, was 228, S = 8 66, was 73; 64 x 8192, 2 heads, S = 2
+// 52, was 84; the decision costs a short batch 0.1 us).
 // A block keeps the line of up to kMaxCompactBatch requests in shared memory.
 // Of more it keeps where each thread's few requests start, and walks on from
 // there (300 requests of 100-900 tokens 29 us, against 49 with fixed chunks;
