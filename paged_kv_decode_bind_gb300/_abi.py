@@ -204,8 +204,9 @@ def _kv8(ws, cache):
     shape = getattr(cache, "pool_shape", None)
     if shape is not None and ws is not None:
         have = getattr(ws, "pool_shape", None)
-        if have is None:  # a bare struct
-            have = (ws.n_layers, ws.pool_slots, ws.n_kv_heads, ws.head_dim, ws.page_size)
+        if have is None:  # a bare struct, or a reference or pointer to one
+            w = getattr(ws, "_obj", None) or getattr(ws, "contents", None) or _ws(ws)
+            have = (w.n_layers, w.pool_slots, w.n_kv_heads, w.head_dim, w.page_size)
         if shape != have:
             raise ValueError("(layers, slots, KV heads, head_dim, page size): the cache was built "
                              f"for {shape}, the workspace has {have}")

@@ -40,8 +40,9 @@ class DecodeRunner:
         """cache: a Kv8Cache of this workspace; the layers then append to and
         attend over it instead of the bf16 pools (flags: PKV_FLAG_OUT_F32 and
         PKV_FLAG_WRITE_LSE).  norm_rope: a QkNormRope, or one per layer, applied
-        to the layer's q and k at ws.position_ids before they are used; a step's
-        device errors all go to ws.err, the norm's too (whatever its own word is)."""
+        to the layer's q and k at ws.position_ids before they are used (its arguments
+        are copied here); a step's device errors all go to ws.err, the norm's too,
+        whatever its own word is."""
         if cache is not None and (not fused or plan):
             raise ValueError("a step on the 8-bit cache has no unfused or planned form")
         if cache is not None:

@@ -356,8 +356,12 @@ def test_a_cache_of_other_shapes_is_refused(kw):
     for call in calls[:4]:  # the bare struct too
         with pytest.raises(ValueError):
             call(ws.struct)
-    # its own, and a copy of its struct
-    for w in (other, A.PkvWorkspace.from_buffer_copy(other.struct)):
+    for w in (ctypes.byref(ws.struct), ctypes.pointer(ws.struct)):
+        with pytest.raises(ValueError):
+            calls[0](w)
+    # its own, a copy of its struct, a reference to it
+    for w in (other, A.PkvWorkspace.from_buffer_copy(other.struct), ctypes.byref(other.struct),
+              ctypes.pointer(other.struct)):
         assert P.pkv_kv8_append(w, cache, 0, 0, 1, None, None, 0) == P.PKV_OK
     for call in calls[4:]:
         call(other)
