@@ -1294,3 +1294,36 @@ def test_attention_weights_keep_their_low_parts(cuda, dtype, heads, d, page):
             tol = 2 * dw[:, None] * mass + 2.0 ** -32 * floor + F32 * np.abs(o)
             assert (np.abs(got[b] - o) - tol).max() <= 0
     assert int(ws.err.item()) == 0
+
+
+@pytest.mark.parametrize("page,block", [(16, 16), (1, 1)])
+def test_extender_captured_on_another_stream(cuda, page, block):
+    # one chunk captured on a stream of its own and replayed with other rows: as call by call
+    from paged_kv_decode_bind_gb300 import Kv8Extender
+    lens, qo = [70, 45], torch.tensor([0, 20, 53], dtype=torch.int32).cuda()
+    rows = [[x.cuda() for x in (W.normal_bf16((53, 8, 128), 90 + i), _rows((53, 2, 128), 93 + i),
+                                _rows((53, 2, 128), 96 + i))] for i in range(2)]
+    got = []
+    for graph in (False, True):
+        prob = _problem(lens, page=page, block=block)
+        ws, cache = prob.device()
+        ext = Kv8Extender(ws, cache, 2, max_new=33, max_context=80, scale=prob.p.scale)
+        q, k, v = (x.clone() for x in rows[0])
+        out = torch.zeros((53, 8, 128), dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        outs = []
+        if graph:
+            side = torch.cuda.Stream()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                ext.layer(0, qo, 33, q, k, v, out)
+        for i in range(2):
+            for dst, src in zip((q, k, v), rows[i]):
+                dst.copy_(src)
+            g.replay() if graph else ext.layer(0, qo, 33, q, k, v, out)
+            torch.cuda.synchronize()
+            outs.append(out.clone())
+        got.append(outs + [cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale])
+        assert int(ws.err.item()) == 0 and outs[0].any() and not torch.equal(*outs)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
