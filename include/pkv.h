@@ -118,7 +118,8 @@ enum {
   PKV_DEVERR_TOTAL = 4,    /* flat mode: kv_indptr[b] + seq_len > max_total_tokens */
   PKV_DEVERR_SLOT = 8,     /* a flat slot or out_loc outside [0, pool_slots)    */
   PKV_DEVERR_TIMEOUT = 16, /* a bounded wait on an async copy ran out (~1 s)    */
-  PKV_DEVERR_POSITION = 32 /* pkv_qk_norm_rope: position < -1 or >= max_positions */
+  PKV_DEVERR_POSITION = 32 /* pkv_qk_norm_rope, pkv_qk_norm_rope_axes: position < -1 or
+                              >= max_positions                                 */
 };
 
 /*
@@ -570,6 +571,108 @@ pkv_status pkv_kv8_decode_layer(const pkv_workspace *ws, const pkv_kv8 *c, int b
                                 const void *q, const void *k_new, const void *v_new, float scale,
                                 int num_splits, int flags, pkv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Tally of attention weight, and the eviction it decides.  Beside the bf16 pools
+ * each cached token has, for each layer and KV head, the sum of the weights that
+ * queries gave it and the place it took in its request.  A request past a limit is
+ * cut to a budget of tokens, chosen for each layer and head by that sum; the kept
+ * rows move together, so page table, lengths and attention stay as they are.
+ * ------------------------------------------------------------------------ */
+
+/* A tally beside a workspace.  Page p of a layer holds [Hkv][page_size] entries. */
+typedef struct pkv_tally {
+  float *weight;       /* [NL, pool_slots / P, Hkv, P] accumulated weight                 */
+  int32_t *origin;     /* same shape: tokens that the request held before this one,
+                          evicted ones counted                                          */
+  int32_t *evicted;    /* [max_reqs] tokens evicted so far from the request of that table
+                          row; the caller zeroes it when a new request takes the row     */
+  float *score;        /* [max_batch, Hkv, score_tokens, G] fp32, 16-byte aligned: a decode
+                          layer's scores (scratch of that call)                         */
+  int32_t score_tokens; /* at least the tokens a request may hold (max_pages_per_req *
+                          page_size, or max_seq_len where that is set and less)         */
+  int32_t reserved;    /* 0                                                              */
+} pkv_tally;
+
+/* Bytes of the named pkv_tally buffer ("weight", "origin", "evicted", "score") for the
+ * shapes in `ws` and t->score_tokens; 0 for an unknown name.  Host only. */
+size_t pkv_tally_bytes(const pkv_workspace *ws, const pkv_tally *t, const char *which);
+
+/*
+ * pkv_decode_layer that also tallies: with the scores s_ht and log-sum-exps lse_h of
+ * its attention, for every cached token t and KV head g
+ *   w = sum over the group's heads h of exp(s_ht - lse_h),  weight[t, g] += w;
+ * an appended token starts anew: weight = w, origin = seq_lens[b] - 1 + evicted[row].
+ * With k_new and v_new NULL nothing is appended and every token adds.
+ * Arguments, outputs and errors are pkv_decode_layer's; ws->lse is always written
+ * (PKV_FLAG_WRITE_LSE may be given).  Two launches; PKV_FLAG_PLAN_EARLY's guarantee is
+ * the same.  A weight that is NaN adds nothing, and the tokens of a split that is
+ * written as empty (a bad page, a wait that ran out, scores that are not finite) gain
+ * nothing from it.  Entries of a batch must not share the pages they append to or tally.
+ * Host errors: as pkv_decode_layer; PKV_ERR_INVALID for PKV_FLAG_FORCE_SIMT, a null
+ * buffer of the tally or a null ws->lse; PKV_ERR_CAPACITY when score_tokens is less than
+ * a request may hold; PKV_ERR_UNSUPPORTED for shapes without the tensor-core kernel.
+ * Device errors: as pkv_decode_layer; PKV_DEVERR_PAGE also for a request row (flat
+ * mode, where the attention reads none) outside the page table: not tallied.
+ */
+pkv_status pkv_tally_decode_layer(const pkv_workspace *ws, const pkv_tally *t, int batch,
+                                  int layer, const void *q, const void *k_new,
+                                  const void *v_new, float scale, int num_splits, int flags,
+                                  pkv_stream_t stream);
+
+/*
+ * The weight that a chunk's last queries give their context.  Call it after the chunk's
+ * pkv_extend_append and pkv_extend_attn with PKV_FLAG_WRITE_LSE.  Observed are the last
+ * min(window, n_b) of request b's n_b new tokens, each attending causally as there:
+ *   w = sum over observed i with position p_i >= t, and the group's heads h, of
+ *       exp(scale * q_ih . k_t - lse_ih).
+ * A cached token (t < seq_lens[b] - n_b) gains w; a new one starts with it, weight = w,
+ * origin = t + evicted[row].  Every weight enters with the scores of exact bf16 products
+ * summed in fp32 and ex2's 2^-22; the sum over queries is fp32, in an order that does
+ * not depend on the launch.  A weight that is NaN, or of a query whose lse is -inf, NaN
+ * or +inf, adds nothing.
+ *   n_rows      rows that q and lse hold (qo_indptr[batch] or more).
+ *   window      >= 1; max_qo_len or more observes every new token.
+ *   q           bf16 [n_rows, Hq, D], 16-byte aligned.
+ *   lse         fp32 [n_rows, Hq], natural log, as ws->lse of the attention.
+ * Device errors: PKV_DEVERR_LEN (a length or new-token count out of range, or rows
+ * outside [0, n_rows)) and PKV_DEVERR_TOTAL, _PAGE for the request's row: the request is
+ * skipped; PKV_DEVERR_PAGE, _SLOT: the entries of the 128-token tile that meets a bad
+ * index keep what they held; PKV_DEVERR_TIMEOUT (a wait that ran out: the same).
+ * Host errors: as pkv_extend_attn; PKV_ERR_INVALID (n_rows < 0, window < 1, a null
+ * buffer); PKV_ERR_UNSUPPORTED (head_dim not 64 / 128, or G not 1, 2, 4, 8, 16).
+ */
+pkv_status pkv_tally_extend(const pkv_workspace *ws, const pkv_tally *t, int batch, int layer,
+                            const int32_t *qo_indptr, int max_qo_len, int n_rows, int window,
+                            const void *q, const float *lse, float scale, pkv_stream_t stream);
+
+/*
+ * Eviction.  Every request with seq_lens[b] > limit is cut to `budget` tokens, in every
+ * layer and for each KV head by itself.  With L = seq_lens[b], row = req_pool_indices[b]
+ * and total = L + evicted[row], the tokens rank by
+ *   1. protected ones first: origin < sinks, or origin >= total - recent
+ *   2. the larger weight (NaN below every number)
+ *   3. the lower index,
+ * and the first `budget` stay.  The j-th kept token of index >= budget moves into the
+ * j-th index < budget that is not kept: its K and V rows, weight and origin.  Then
+ * seq_lens[b] = budget and evicted[row] += L - budget.  Rows of index >= budget are left
+ * as they were; the pages behind the budget are free.  position_ids, kv_indptr and
+ * kv_indices are as the last bind left them (a step binds before its layers), and a
+ * request's next token belongs at position seq_lens + evicted[row]
+ * (pkv_qk_norm_rope_axes).  Slots come from the page table in both index modes.
+ *   max_len     host upper bound on every seq_lens[b]; at most PKV_TALLY_MAX_LEN.
+ *   limit       >= budget.
+ *   budget      >= 1, at least sinks + recent (both >= 0).
+ * Requests of a batch must not share pages, nor a table row.  split_counters must be
+ * set (zeroed once; left zeroed).
+ * Device errors: PKV_DEVERR_LEN (seq_lens[b] out of range or above max_len),
+ * PKV_DEVERR_PAGE (a bad request row or page id): the request is left as it is.
+ * Host errors: PKV_ERR_INVALID (null or misaligned pointer, bad size),
+ * PKV_ERR_CAPACITY (batch), PKV_ERR_UNSUPPORTED (head_dim not 64 / 128, max_len).
+ */
+#define PKV_TALLY_MAX_LEN 393216
+pkv_status pkv_tally_evict(const pkv_workspace *ws, const pkv_tally *t, int batch, int max_len,
+                           int limit, int budget, int sinks, int recent, pkv_stream_t stream);
+
 /*
  * RMS norm of every query and key head with the position rotation, in one
  * pass: the step between a layer's projection and its append and attention.
@@ -611,6 +714,38 @@ pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, con
                             int64_t q_stride, const void *k, int64_t k_stride,
                             const int32_t *positions, void *q_out, int64_t q_out_stride,
                             void *k_out, int64_t k_out_stride, pkv_stream_t stream);
+
+/* Positions of several axes for pkv_qk_norm_rope_axes. */
+typedef struct pkv_rope_axes {
+  int32_t n_axes;          /* 1 .. 4                                                       */
+  int32_t n_rows;          /* entries of `evicted` and `delta` (0 without them)            */
+  const int32_t *rows;     /* device [n_tokens]: each token's entry there (ws->
+                              req_pool_indices in a decode step); NULL: no shift           */
+  const int32_t *evicted;  /* device [n_rows] added to all of a token's positions, or NULL */
+  const int32_t *delta;    /* device [n_rows] the same (what a prompt's images took from
+                              its positions), or NULL                                      */
+  uint8_t axis[128];       /* axis of pair i < rot_dim / 2                                 */
+} pkv_rope_axes;
+
+/*
+ * pkv_qk_norm_rope with a row of cos_sin for each axis: pair i of token t turns by row
+ *   positions[axis[i] * axis_stride + t] + evicted[rows[t]] + delta[rows[t]]
+ * (columns i and rot_dim / 2 + i, so a pair's frequency is the table's).
+ *   positions    device int32; axis a of token t at a * axis_stride + t.
+ *   axis_stride  elements; 0: all axes read the same positions (a decode step's, text).
+ * A token whose positions of the axes in use are all -1 before the shift is written as
+ * zeros, without an error.
+ * Device errors: PKV_DEVERR_POSITION (a shifted position of an axis in use outside the
+ * table, or rows[t] outside [0, n_rows): the token's heads are written as zeros).
+ * Host errors: as pkv_qk_norm_rope; PKV_ERR_INVALID (n_axes, an axis out of range,
+ * axis_stride not 0 and less than n_tokens, rows without n_rows or without both arrays,
+ * or an array without rows).
+ */
+pkv_status pkv_qk_norm_rope_axes(const pkv_qk_norm_rope_args *args, const pkv_rope_axes *axes,
+                                 int n_tokens, const void *q, int64_t q_stride, const void *k,
+                                 int64_t k_stride, const int32_t *positions, int64_t axis_stride,
+                                 void *q_out, int64_t q_out_stride, void *k_out,
+                                 int64_t k_out_stride, pkv_stream_t stream);
 
 /*
  * Host steady-state test (cache.py page, bullets 1-4): non-zero when the

@@ -8,11 +8,13 @@ from . import _abi
 from ._abi import *  # noqa: F401,F403  (constants and pkv_* entry points)
 from .cascade import CascadeDecoder, choose_prefix_splits
 from .engine import BindTracker, DecodeRunner
-from .kv8 import Kv8Cache, Kv8Extender, QkNormRope, rope_table
+from .kv8 import Kv8Cache, Kv8Extender, QkNormRope, QkNormRopeAxes, rope_table
+from .tally import Eviction, Tally, TallyExtender
 from .workspace import Workspace
 
 _abi.load()
 
 __all__ = ["Workspace", "DecodeRunner", "BindTracker", "CascadeDecoder", "choose_prefix_splits",
-           "Kv8Cache", "Kv8Extender", "QkNormRope", "rope_table"] + [
+           "Kv8Cache", "Kv8Extender", "QkNormRope", "QkNormRopeAxes", "rope_table", "Tally",
+           "TallyExtender", "Eviction"] + [
     n for n in dir(_abi) if n.startswith(("pkv_", "PKV_"))]

@@ -27,6 +27,7 @@ PKV_DEVERR_PAGE, PKV_DEVERR_LEN, PKV_DEVERR_TOTAL, PKV_DEVERR_SLOT, PKV_DEVERR_T
     1, 2, 4, 8, 16
 PKV_DEVERR_POSITION = 32
 PKV_KV8_E4M3, PKV_KV8_INT8 = 0, 1
+PKV_TALLY_MAX_LEN = 393216
 
 # Every symbol include/pkv.h declares (checked by the ABI test).
 EXPORTS = ("pkv_workspace_bytes", "pkv_bind_step", "pkv_choose_splits", "pkv_choose_pieces",
@@ -36,7 +37,8 @@ EXPORTS = ("pkv_workspace_bytes", "pkv_bind_step", "pkv_choose_splits", "pkv_cho
            "pkv_decode_attn_static_scratch",
            "pkv_extend_attn", "pkv_extend_append", "pkv_merge_lse",
            "pkv_kv8_bytes", "pkv_kv8_append", "pkv_kv8_extend_append", "pkv_kv8_read",
-           "pkv_kv8_decode_layer", "pkv_qk_norm_rope",
+           "pkv_kv8_decode_layer", "pkv_qk_norm_rope", "pkv_qk_norm_rope_axes",
+           "pkv_tally_bytes", "pkv_tally_decode_layer", "pkv_tally_extend", "pkv_tally_evict",
            "pkv_is_steady_increment",
            "pkv_status_string", "pkv_version")
 PKV_STATIC_SCRATCH_BYTES = 8 << 20
@@ -84,6 +86,24 @@ class PkvQkNormRopeArgs(ctypes.Structure):
         ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
         ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
         ("cos_sin", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class PkvTally(ctypes.Structure):
+    """Mirror of ``pkv_tally``."""
+
+    _fields_ = [
+        ("weight", ctypes.c_void_p), ("origin", ctypes.c_void_p), ("evicted", ctypes.c_void_p),
+        ("score", ctypes.c_void_p), ("score_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class PkvRopeAxes(ctypes.Structure):
+    """Mirror of ``pkv_rope_axes``."""
+
+    _fields_ = [
+        ("n_axes", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("rows", ctypes.c_void_p),
+        ("evicted", ctypes.c_void_p), ("delta", ctypes.c_void_p), ("axis", ctypes.c_uint8 * 128),
     ]
 
 
@@ -146,6 +166,19 @@ def load(path: str = LIB_PATH):
     lib.pkv_qk_norm_rope.argtypes = [ctypes.POINTER(PkvQkNormRopeArgs), i32, vp, i64, vp, i64, vp,
                                      vp, i64, vp, i64, vp]
     lib.pkv_qk_norm_rope.restype = i32
+    lib.pkv_qk_norm_rope_axes.argtypes = [
+        ctypes.POINTER(PkvQkNormRopeArgs), ctypes.POINTER(PkvRopeAxes), i32, vp, i64, vp, i64, vp,
+        i64, vp, i64, vp, i64, vp]
+    lib.pkv_qk_norm_rope_axes.restype = i32
+    T = ctypes.POINTER(PkvTally)
+    lib.pkv_tally_bytes.argtypes = [W, T, ctypes.c_char_p]
+    lib.pkv_tally_bytes.restype = ctypes.c_size_t
+    lib.pkv_tally_decode_layer.argtypes = [W, T, i32, i32, vp, vp, vp, f32, i32, i32, vp]
+    lib.pkv_tally_decode_layer.restype = i32
+    lib.pkv_tally_extend.argtypes = [W, T, i32, i32, vp, i32, i32, i32, vp, vp, f32, vp]
+    lib.pkv_tally_extend.restype = i32
+    lib.pkv_tally_evict.argtypes = [W, T, i32, i32, i32, i32, i32, i32, vp]
+    lib.pkv_tally_evict.restype = i32
     p64, p32 = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int32)
     lib.pkv_is_steady_increment.argtypes = [p64, p32, i32, p64, p32, i32]
     lib.pkv_is_steady_increment.restype = i32
@@ -211,6 +244,21 @@ def _kv8(ws, cache):
             raise ValueError("(layers, slots, KV heads, head_dim, page size): the cache was built "
                              f"for {shape}, the workspace has {have}")
     return _ws(cache)
+
+
+def _tally(ws, tally, batch=0):
+    """The struct of a tally.  A Tally knows the shapes that it was built for: under a
+    workspace of others its calls would write past its buffers."""
+    shape = getattr(tally, "shape", None)
+    if shape is not None and ws is not None:
+        w = getattr(ws, "_obj", None) or getattr(ws, "contents", None) or _ws(ws)
+        have = (w.n_layers, w.pool_slots, w.n_q_heads, w.n_kv_heads, w.page_size, w.max_reqs)
+        if shape != have:
+            raise ValueError("(layers, slots, query heads, KV heads, page size, table rows): the "
+                             f"tally was built for {shape}, the workspace has {have}")
+        if batch > tally.max_batch:
+            raise ValueError(f"the tally holds the scores of {tally.max_batch} requests")
+    return _ws(tally)
 
 
 def _check(fn, status):
@@ -410,6 +458,72 @@ def pkv_qk_norm_rope(args, n_tokens, q, k, positions, q_out, k_out, stream=None,
     s = (_lib or load()).pkv_qk_norm_rope(st, n, qp, qs, kp, ks, _positions(positions, n), qo, qos,
                                           ko, kos, _stream(stream))
     return _check("pkv_qk_norm_rope", s) if check and s else s
+
+
+def _axis_positions(x, rows, n_axes):
+    """Pointer and elements between axes of int32 positions: [tokens] (every axis the
+    same) or [n_axes, tokens], tokens dense."""
+    if x is None or isinstance(x, int):
+        return x, 0
+    if x.dtype is _INT32 and x.dim() in (1, 2) and x.shape[-1] >= rows and \
+            (x.stride(-1) == 1 or x.shape[-1] <= 1):
+        if x.dim() == 1:
+            return x.data_ptr(), 0
+        if x.shape[0] == n_axes and (n_axes == 1 or x.stride(0) >= rows):
+            return x.data_ptr(), 0 if n_axes == 1 else x.stride(0)
+    raise ValueError(f"positions are int32 [tokens >= {rows}] or [{n_axes}, tokens], dense along "
+                     f"the tokens, got {x.dtype} {tuple(x.shape)} with strides {x.stride()}")
+
+
+def pkv_qk_norm_rope_axes(rope, n_tokens, q, k, positions, q_out, k_out, stream=None, check=True):
+    """pkv_qk_norm_rope with positions of several axes (rope: a QkNormRopeAxes).
+    positions: int32 [n_axes, tokens], or [tokens] for the same on every axis; the
+    tensors' checks are pkv_qk_norm_rope's."""
+    st, axes, n = rope.args, rope.axes, n_tokens
+    D, qw, kw = rope.widths
+    if n > rope.max_tokens:
+        raise ValueError(f"rows holds {rope.max_tokens} tokens, {n} asked for")
+    qp, qs = _heads(q, qw, D, n)
+    kp, ks = _heads(k, kw, D, n)
+    qo, qos = _heads(q_out, qw, D, n)
+    ko, kos = _heads(k_out, kw, D, n)
+    pp, ps = _axis_positions(positions, n, axes.n_axes)
+    s = (_lib or load()).pkv_qk_norm_rope_axes(st, axes, n, qp, qs, kp, ks, pp, ps, qo, qos, ko,
+                                               kos, _stream(stream))
+    return _check("pkv_qk_norm_rope_axes", s) if check and s else s
+
+
+def pkv_tally_bytes(ws, tally, which: str) -> int:
+    return int(load().pkv_tally_bytes(_ws(ws), _ws(tally), which.encode()))
+
+
+def pkv_tally_decode_layer(ws, tally, batch, layer, q, k_new, v_new, scale, num_splits=1, flags=0,
+                           stream=None, check=True):
+    """pkv_decode_layer that adds every token's attention weight to a tally (a Tally or
+    a PkvTally) and leaves the log-sum-exps in ws.lse."""
+    s = load().pkv_tally_decode_layer(_ws(ws), _tally(ws, tally, batch), int(batch), int(layer),
+                                      _ptr(q), _ptr(k_new), _ptr(v_new), float(scale),
+                                      int(num_splits), int(flags), _stream(stream))
+    return _check("pkv_tally_decode_layer", s) if check else s
+
+
+def pkv_tally_extend(ws, tally, batch, layer, qo_indptr, max_qo_len, n_rows, window, q, lse, scale,
+                     stream=None, check=True):
+    """The weights that the last `window` new tokens of every request give its context,
+    into the tally; q [n_rows, Hq, D] and lse [n_rows, Hq] as of the chunk's attention."""
+    s = load().pkv_tally_extend(_ws(ws), _tally(ws, tally), int(batch), int(layer),
+                                _ptr(qo_indptr), int(max_qo_len), int(n_rows), int(window),
+                                _ptr(q), _ptr(lse), float(scale), _stream(stream))
+    return _check("pkv_tally_extend", s) if check else s
+
+
+def pkv_tally_evict(ws, tally, batch, max_len, limit, budget, sinks=0, recent=0, stream=None,
+                    check=True):
+    """Every request longer than `limit` cut to `budget` tokens of each layer and KV head,
+    by the tally; max_len bounds the lengths."""
+    s = load().pkv_tally_evict(_ws(ws), _tally(ws, tally), int(batch), int(max_len), int(limit),
+                               int(budget), int(sinks), int(recent), _stream(stream))
+    return _check("pkv_tally_evict", s) if check else s
 
 
 def pkv_is_steady_increment(prev_ids, prev_lens, ids, lens) -> bool:

@@ -24,6 +24,8 @@ struct DecodeArgs {
   const void *v_new;
   int fused_merge;    // 1: the last split of each (request, KV head) merges
   int apportion;      // tensor-core kernel: apportioned splits (set by its launcher)
+  float *score = nullptr;      // with a tally: every token's scores (decode_mma.cuh)
+  long long score_tokens = 0;  // ... and the tokens a request has room for there
 };
 
 // CUDA-core split-KV decode.  Returns cudaErrorNotSupported for shapes
@@ -39,6 +41,14 @@ cudaError_t launch_decode_mma(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_plan(const DecodeArgs &a, cudaStream_t st);
 size_t plan_bytes();
 bool decode_mma_supported(int head_dim, int group);
+
+// The tally of attention weight (tally_decode.cu, tally_extend.cu, tally_evict.cu).
+cudaError_t launch_tally_decode(const DecodeArgs &a, const pkv_tally &t, cudaStream_t st);
+cudaError_t launch_tally_extend(const pkv_workspace &ws, const pkv_tally &t, int batch, int layer,
+                                const int *qo_indptr, int max_qo_len, int n_rows, int window,
+                                const void *q, const float *lse, float scale, cudaStream_t st);
+cudaError_t launch_tally_evict(const pkv_workspace &ws, const pkv_tally &t, int batch, int max_len,
+                               int limit, int budget, int sinks, int recent, cudaStream_t st);
 
 // 8-bit cache (kv8_cache.cu, kv8_decode.cu).
 struct Kv8Args;
@@ -58,10 +68,13 @@ cudaError_t launch_kv8_read(const pkv_workspace &ws, const pkv_kv8 &c, int batch
 cudaError_t launch_kv8_decode(const Kv8Args &a, cudaStream_t st);
 bool kv8_decode_supported(int head_dim, int group);
 
-// Norm and rotation of queries and keys (qk_norm_rope.cu).
-cudaError_t launch_qk_norm_rope(const pkv_qk_norm_rope_args &p, int n_tokens, const void *q,
+// Norm and rotation of queries and keys (qk_norm_rope.cu); axes: NULL for one axis
+// of plain positions.
+cudaError_t launch_qk_norm_rope(const pkv_qk_norm_rope_args &p, const pkv_rope_axes *axes,
+                                int n_tokens, const void *q,
                                 long long q_stride, const void *k, long long k_stride,
-                                const int *positions, void *q_out, long long q_out_stride,
+                                const int *positions, long long axis_stride, void *q_out,
+                                long long q_out_stride,
                                 void *k_out, long long k_out_stride, cudaStream_t st);
 
 cudaError_t launch_merge(const pkv_workspace &ws, int batch, int num_splits, int flags,

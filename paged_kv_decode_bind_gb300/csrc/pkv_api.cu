@@ -200,7 +200,8 @@ int pkv_choose_extend_splits(const pkv_workspace *ws, int batch, int max_qo_len,
 
 static pkv_status decode_common(const pkv_workspace *ws, int batch, int layer, const void *q,
                                 const void *k_new, const void *v_new, float scale,
-                                int num_splits, int flags, int fused, pkv_stream_t stream) {
+                                int num_splits, int flags, int fused, pkv_stream_t stream,
+                                const pkv_tally *tally = nullptr) {
   pkv_status st = check_shape(ws);
   if (st != PKV_OK) return st;
   if ((st = check_index(ws)) != PKV_OK) return st;
@@ -237,6 +238,7 @@ static pkv_status decode_common(const pkv_workspace *ws, int batch, int layer, c
     return PKV_OK;
   }
   DecodeArgs a{*ws, batch, layer, q, scale, num_splits, flags, k_new, v_new, fused, 0};
+  if (tally) return from_cuda(launch_tally_decode(a, *tally, s));
   return from_cuda(use_mma ? launch_decode_mma(a, s) : launch_decode_simt(a, s));
 }
 
@@ -454,10 +456,12 @@ pkv_status pkv_kv8_decode_layer(const pkv_workspace *ws, const pkv_kv8 *c, int b
   return from_cuda(launch_kv8_decode(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, const void *q,
-                            int64_t q_stride, const void *k, int64_t k_stride,
-                            const int32_t *positions, void *q_out, int64_t q_out_stride,
-                            void *k_out, int64_t k_out_stride, pkv_stream_t stream) {
+// axes: NULL for pkv_qk_norm_rope.
+static pkv_status norm_rope_common(const pkv_qk_norm_rope_args *args, const pkv_rope_axes *axes,
+                                   int n_tokens, const void *q, int64_t q_stride, const void *k,
+                                   int64_t k_stride, const int32_t *positions,
+                                   int64_t axis_stride, void *q_out, int64_t q_out_stride,
+                                   void *k_out, int64_t k_out_stride, pkv_stream_t stream) {
   if (!args || n_tokens < 0 || args->n_q_heads < 1 || args->n_kv_heads < 0 || !args->err ||
       args->max_positions < 0 || !(args->eps >= 0.f) || args->reserved != 0 ||
       (args->interleaved != 0 && args->interleaved != 1))
@@ -468,6 +472,14 @@ pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, con
   if (!aligned16(args->q_weight) || !aligned16(args->k_weight) || !aligned16(args->cos_sin))
     return PKV_ERR_INVALID;
   if (rot > 0 && !args->cos_sin) return PKV_ERR_INVALID;
+  if (axes) {
+    if (axes->n_axes < 1 || axes->n_axes > 4 || axes->n_rows < 0) return PKV_ERR_INVALID;
+    for (int i = 0; i < rot / 2; ++i)
+      if (axes->axis[i] >= axes->n_axes) return PKV_ERR_INVALID;
+    const bool shifts = axes->evicted || axes->delta;
+    if (shifts ? !axes->rows || axes->n_rows < 1 : axes->rows != nullptr) return PKV_ERR_INVALID;
+    if (axis_stride != 0 && axis_stride < n_tokens) return PKV_ERR_INVALID;
+  }
   if (n_tokens == 0) return PKV_OK;  // the tensors may be empty
   if (rot > 0 && !positions) return PKV_ERR_INVALID;
   const int64_t qw = (int64_t)args->n_q_heads * D, kw = (int64_t)args->n_kv_heads * D;
@@ -477,9 +489,99 @@ pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, con
   if (kw > 0 && (!k || !k_out || !aligned16(k) || !aligned16(k_out) || k_stride % 8 ||
                  k_out_stride % 8 || k_stride < kw || k_out_stride < kw))
     return PKV_ERR_INVALID;
-  return from_cuda(launch_qk_norm_rope(*args, n_tokens, q, q_stride, k, k_stride, positions, q_out,
-                                       q_out_stride, k_out, k_out_stride,
+  return from_cuda(launch_qk_norm_rope(*args, axes, n_tokens, q, q_stride, k, k_stride, positions,
+                                       axis_stride, q_out, q_out_stride, k_out, k_out_stride,
                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_qk_norm_rope(const pkv_qk_norm_rope_args *args, int n_tokens, const void *q,
+                            int64_t q_stride, const void *k, int64_t k_stride,
+                            const int32_t *positions, void *q_out, int64_t q_out_stride,
+                            void *k_out, int64_t k_out_stride, pkv_stream_t stream) {
+  return norm_rope_common(args, nullptr, n_tokens, q, q_stride, k, k_stride, positions, 0, q_out,
+                          q_out_stride, k_out, k_out_stride, stream);
+}
+
+pkv_status pkv_qk_norm_rope_axes(const pkv_qk_norm_rope_args *args, const pkv_rope_axes *axes,
+                                 int n_tokens, const void *q, int64_t q_stride, const void *k,
+                                 int64_t k_stride, const int32_t *positions, int64_t axis_stride,
+                                 void *q_out, int64_t q_out_stride, void *k_out,
+                                 int64_t k_out_stride, pkv_stream_t stream) {
+  if (!axes) return PKV_ERR_INVALID;
+  return norm_rope_common(args, axes, n_tokens, q, q_stride, k, k_stride, positions, axis_stride,
+                          q_out, q_out_stride, k_out, k_out_stride, stream);
+}
+
+// Checks of a tally against its workspace's shapes.
+static pkv_status check_tally(const pkv_workspace *ws, const pkv_tally *t) {
+  pkv_status st = check_shape(ws);
+  if (st != PKV_OK) return st;
+  if ((st = check_index(ws)) != PKV_OK) return st;
+  if (!t || t->reserved != 0) return PKV_ERR_INVALID;
+  if (!t->weight || !t->origin || !t->evicted) return PKV_ERR_INVALID;
+  if (!aligned4(t->weight) || !aligned4(t->origin) || !aligned4(t->evicted))
+    return PKV_ERR_INVALID;
+  return PKV_OK;
+}
+
+size_t pkv_tally_bytes(const pkv_workspace *ws, const pkv_tally *t, const char *which) {
+  if (!ws || !t || !which) return 0;
+  auto pos = [](int x) { return (size_t)(x > 0 ? x : 0); };
+  if (!strcmp(which, "weight") || !strcmp(which, "origin"))
+    return pos(ws->n_layers) * pos(ws->pool_slots) * pos(ws->n_kv_heads) * 4;
+  if (!strcmp(which, "evicted")) return pos(ws->max_reqs) * 4;
+  if (!strcmp(which, "score"))
+    return pos(ws->max_batch) * pos(ws->n_q_heads) * pos(t->score_tokens) * 4;
+  return 0;
+}
+
+pkv_status pkv_tally_decode_layer(const pkv_workspace *ws, const pkv_tally *t, int batch,
+                                  int layer, const void *q, const void *k_new,
+                                  const void *v_new, float scale, int num_splits, int flags,
+                                  pkv_stream_t stream) {
+  const pkv_status st = check_tally(ws, t);
+  if (st != PKV_OK) return st;
+  if ((flags & PKV_FLAG_FORCE_SIMT) || !t->score || !aligned16(t->score) || !ws->lse)
+    return PKV_ERR_INVALID;
+  if (t->score_tokens < len_cap(*ws)) return PKV_ERR_CAPACITY;
+  return decode_common(ws, batch, layer, q, k_new, v_new, scale, num_splits,
+                       flags | PKV_FLAG_FORCE_MMA | PKV_FLAG_WRITE_LSE, 1, stream, t);
+}
+
+pkv_status pkv_tally_extend(const pkv_workspace *ws, const pkv_tally *t, int batch, int layer,
+                            const int32_t *qo_indptr, int max_qo_len, int n_rows, int window,
+                            const void *q, const float *lse, float scale, pkv_stream_t stream) {
+  pkv_status st = check_tally(ws, t);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || layer < 0 || max_qo_len < 0 || n_rows < 0 || window < 1)
+    return PKV_ERR_INVALID;
+  if (batch > ws->max_batch || layer >= ws->n_layers) return PKV_ERR_CAPACITY;
+  if (!extend_supported(ws->head_dim, ws->n_q_heads / ws->n_kv_heads))
+    return PKV_ERR_UNSUPPORTED;
+  if (!qo_indptr || !ws->k_pool || !aligned16(ws->k_pool)) return PKV_ERR_INVALID;
+  if (n_rows > 0 && (!q || !lse || !aligned16(q) || !aligned4(lse))) return PKV_ERR_INVALID;
+  if (batch == 0 || max_qo_len == 0 || n_rows == 0) return PKV_OK;
+  return from_cuda(launch_tally_extend(*ws, *t, batch, layer, qo_indptr, max_qo_len, n_rows,
+                                       window, q, lse, scale,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_tally_evict(const pkv_workspace *ws, const pkv_tally *t, int batch, int max_len,
+                           int limit, int budget, int sinks, int recent, pkv_stream_t stream) {
+  const pkv_status st = check_tally(ws, t);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || max_len < 0 || budget < 1 || limit < budget || sinks < 0 || recent < 0 ||
+      (long long)sinks + recent > budget)
+    return PKV_ERR_INVALID;
+  if (batch > ws->max_batch) return PKV_ERR_CAPACITY;
+  if ((ws->head_dim != 64 && ws->head_dim != 128) || max_len > PKV_TALLY_MAX_LEN)
+    return PKV_ERR_UNSUPPORTED;
+  if (!ws->k_pool || !ws->v_pool || !aligned16(ws->k_pool) || !aligned16(ws->v_pool) ||
+      !ws->split_counters)
+    return PKV_ERR_INVALID;
+  if (batch == 0) return PKV_OK;
+  return from_cuda(launch_tally_evict(*ws, *t, batch, max_len, limit, budget, sinks, recent,
+                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int pkv_is_steady_increment(const int64_t *prev_ids, const int32_t *prev_lens, int n_prev,

@@ -22,6 +22,15 @@ namespace {
 
 constexpr int kRWarps = 4;
 
+// Positions of several axes: two bits a pair name its axis.
+struct AxesArgs {
+  uint32_t axis[8];
+  int used;  // bit a: some pair follows axis a
+  int n_rows;
+  long long stride;
+  const int *rows, *evicted, *delta;
+};
+
 struct RopeArgs {
   pkv_qk_norm_rope_args p;
   int n_tokens, per_token;  // warps per token
@@ -31,8 +40,65 @@ struct RopeArgs {
   uint16_t *q_out, *k_out;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kRWarps * 32) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+// Several axes: cosines and sines of this lane's eight pairs (first pair 8 l), each from
+// the row of its axis's position.  Returns whether the token is written as zeros.  A lane
+// reads the rows of the axes its pairs follow, whole, and picks: sections of 8 pairs and
+// more read one row, as without axes.
+__device__ __forceinline__ bool axes_rows(const pkv_qk_norm_rope_args &p, const AxesArgs &x,
+                                          const int *positions, long long tok, int l, bool turns,
+                                          bool lead, float (&cs)[8], float (&sn)[8]) {
+  const int rot = p.rot_dim;
+  int err = 0;
+  long long shift = 0;
+  if (x.rows) {
+    const int row = x.rows[tok];
+    if (row >= 0 && row < x.n_rows) {
+      if (x.evicted) shift += x.evicted[row];
+      if (x.delta) shift += x.delta[row];
+    } else {
+      err = 1;
+    }
+  }
+  long long pos[4];
+  bool none = true;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    pos[a] = -1;
+    if (!(x.used >> a & 1)) continue;
+    const int raw = positions[a * x.stride + tok];
+    none = none && raw == -1;
+    pos[a] = raw + shift;
+    if (pos[a] < 0 || pos[a] >= p.max_positions) err = 1;
+  }
+  if (err && !none && lead) atomicOr(p.err, PKV_DEVERR_POSITION);
+  if (err || none) return true;
+  if (turns) {
+    const uint32_t mine = x.axis[l >> 1] >> (16 * (l & 1));
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      unsigned take = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) take |= (unsigned)((mine >> (2 * e) & 3) == (uint32_t)a) << e;
+      if (take == 0) continue;
+      const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + pos[a] * rot);
+      float c[8], s[8];
+      *reinterpret_cast<float4 *>(c) = row[2 * l];
+      *reinterpret_cast<float4 *>(c + 4) = row[2 * l + 1];
+      *reinterpret_cast<float4 *>(s) = row[rot / 8 + 2 * l];
+      *reinterpret_cast<float4 *>(s + 4) = row[rot / 8 + 2 * l + 1];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        cs[e] = take >> e & 1 ? c[e] : cs[e];
+        sn[e] = take >> e & 1 ? s[e] : sn[e];
+      }
+    }
+  }
+  return false;
+}
+
+template <int D, bool AXES>
+__global__ void __launch_bounds__(kRWarps * 32)
+    qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ AxesArgs ax) {
   constexpr int LG = D / 16;    // lanes per head
   constexpr int HPW = 32 / LG;  // heads side by side in a warp
   pdl_wait();
@@ -59,7 +125,12 @@ __global__ void __launch_bounds__(kRWarps * 32) qk_norm_rope_kernel(const __grid
   }
   float cs[8], sn[8];
   bool bad = false;
-  if (rot > 0) {
+  if constexpr (AXES) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
+    if (rot > 0)
+      bad = axes_rows(p, ax, a.positions, tok, l, turns, part == 0 && lane == 0, cs, sn);
+  } else if (rot > 0) {
     const int pos = a.positions[tok];
     bad = pos < 0 || pos >= p.max_positions;
     // -1 is an empty request of a padded batch
@@ -149,7 +220,7 @@ __global__ void __launch_bounds__(kRWarps * 32) qk_norm_rope_kernel(const __grid
 }
 
 template <int D>
-cudaError_t launch_one(RopeArgs a, cudaStream_t st) {
+cudaError_t launch_one(RopeArgs a, const AxesArgs *axes, cudaStream_t st) {
   const int per_warp = 32 / (D / 16);
   const int groups = (a.p.n_q_heads + a.p.n_kv_heads + per_warp - 1) / per_warp;
   // Warps per token: one per group of heads while that fits about one wave
@@ -162,22 +233,38 @@ cudaError_t launch_one(RopeArgs a, cudaStream_t st) {
   a.per_token = (int)std::min<long long>(groups, std::max<long long>(1, wave / a.n_tokens));
   const long long blocks = ((long long)a.n_tokens * a.per_token + kRWarps - 1) / kRWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  return launch_pdl(qk_norm_rope_kernel<D>, dim3((unsigned)blocks), dim3(kRWarps * 32), 0, st, a);
+  const dim3 grid((unsigned)blocks), block(kRWarps * 32);
+  if (axes) return launch_pdl(qk_norm_rope_kernel<D, true>, grid, block, 0, st, a, *axes);
+  return launch_pdl(qk_norm_rope_kernel<D, false>, grid, block, 0, st, a, AxesArgs{});
 }
 
 }  // namespace
 
-cudaError_t launch_qk_norm_rope(const pkv_qk_norm_rope_args &p, int n_tokens, const void *q,
-                                long long q_stride, const void *k, long long k_stride,
-                                const int *positions, void *q_out, long long q_out_stride,
-                                void *k_out, long long k_out_stride, cudaStream_t st) {
+cudaError_t launch_qk_norm_rope(const pkv_qk_norm_rope_args &p, const pkv_rope_axes *axes,
+                                int n_tokens, const void *q, long long q_stride, const void *k,
+                                long long k_stride, const int *positions, long long axis_stride,
+                                void *q_out, long long q_out_stride, void *k_out,
+                                long long k_out_stride, cudaStream_t st) {
   const RopeArgs a{p, n_tokens, 1, static_cast<const uint16_t *>(q),
                    static_cast<const uint16_t *>(k), q_stride, k_stride, q_out_stride,
                    k_out_stride, positions, static_cast<uint16_t *>(q_out),
                    static_cast<uint16_t *>(k_out)};
-  if (p.head_dim == 64) return launch_one<64>(a, st);
-  if (p.head_dim == 128) return launch_one<128>(a, st);
-  if (p.head_dim == 256) return launch_one<256>(a, st);
+  AxesArgs x{};
+  if (axes) {
+    for (int i = 0; i < p.rot_dim / 2; ++i) {
+      x.axis[i / 16] |= (uint32_t)axes->axis[i] << (2 * (i % 16));
+      x.used |= 1 << axes->axis[i];
+    }
+    x.n_rows = axes->n_rows;
+    x.stride = axis_stride;
+    x.rows = axes->rows;
+    x.evicted = axes->evicted;
+    x.delta = axes->delta;
+  }
+  const AxesArgs *xp = axes ? &x : nullptr;
+  if (p.head_dim == 64) return launch_one<64>(a, xp, st);
+  if (p.head_dim == 128) return launch_one<128>(a, xp, st);
+  if (p.head_dim == 256) return launch_one<256>(a, xp, st);
   return cudaErrorNotSupported;
 }
 

@@ -1,0 +1,147 @@
+// Decode attention with the tally: the tensor-core kernel also stores every token's
+// scores (decode_mma.cuh), and a second launch turns them into weights.
+//
+//   weight[t, g] += sum over the group's heads of 2^(score_t,h - lse_h log2 e)
+//
+// A weight needs the log-sum-exp of its whole request, which exists only once the last
+// split is merged, so it cannot be added where the score is made.  The scores are 4 G
+// bytes a token and head beside the 4 D of its K and V (3 % at G = 4, D = 128), stay in
+// L2, and spare a second reading of K.
+#include "decode_mma.cuh"
+#include "tally.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kTThreads = 256;
+
+struct TallyArgs {
+  pkv_workspace ws;
+  pkv_tally t;
+  int batch, layer;
+  int appended;  // the newest token's entry starts anew
+  int early;     // lengths, tables and rows are older than the previous launch
+  int tl_log, hl_log;  // a warp takes 2^tl tokens of 2^hl KV heads
+};
+
+// One warp: 2^tl_log tokens x 2^hl_log heads, a lane each.  Tokens run fastest over the
+// lanes, so that a page's entries of a head, and a head's scores, are read in runs.
+template <int G>
+__global__ void __launch_bounds__(kTThreads)
+    tally_add_kernel(const __grid_constant__ TallyArgs a) {
+  const pkv_workspace &ws = a.ws;
+  pdl_trigger();
+  if (!a.early) pdl_wait();
+  Plan pl;
+  pl.set_pages(ws);
+  const int lane = threadIdx.x & 31;
+  const int ts = lane & ((1 << a.tl_log) - 1), hs = lane >> a.tl_log;
+  const int hgroups = (ws.n_kv_heads + (1 << a.hl_log) - 1) >> a.hl_log;
+  const int Hq = ws.n_q_heads;
+  bool waited = !a.early;
+  for (int b = blockIdx.y; b < a.batch; b += gridDim.y) {
+    const int L = usable_len(ws, b);
+    const ReqIndex ri = req_index(ws, b);
+    const int row = ws.req_pool_indices[b];
+    const bool row_ok = row >= 0 && row < ws.max_reqs;
+    const int tgroups = (L + (1 << a.tl_log) - 1) >> a.tl_log;
+    const long long items = (long long)tgroups * hgroups;
+    const long long step = (long long)gridDim.x * (kTThreads / 32);
+    for (long long it = (long long)blockIdx.x * (kTThreads / 32) + (threadIdx.x >> 5); it < items;
+         it += step) {
+      const int tg = (int)(it / hgroups), hg = (int)(it - (long long)tg * hgroups);
+      const int t = (tg << a.tl_log) + ts, g = (hg << a.hl_log) + hs;
+      const bool live = t < L && g < ws.n_kv_heads && ri.ok && row_ok;
+      long long slot = -1;
+      if (live) {
+        int kind = 0;  // the attention has raised it
+        slot = slot_from_raw(ws, pl, *index_src(ws, pl, ri, t), t, kind);
+      }
+      if (!waited) {
+        pdl_wait();  // scores, log-sum-exps and the tally
+        waited = true;
+      }
+      if (slot < 0) continue;
+      const int page = pl.page_of((int)slot);
+      const long long at = tally_at(ws, pl.n_pages, a.layer, page, g, (int)slot - page * pl.P);
+      const bool fresh = a.appended && t == L - 1;
+      const float was = fresh ? 0.f : a.t.weight[at];
+      const float *s = a.t.score + (((long long)b * ws.n_kv_heads + g) * a.t.score_tokens + t) * G;
+      const float *lse = ws.lse + (long long)b * Hq + g * G;
+      float x[G];
+      if constexpr (G >= 4) {
+#pragma unroll
+        for (int h = 0; h < G; h += 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + h));
+          x[h] = v.x;
+          x[h + 1] = v.y;
+          x[h + 2] = v.z;
+          x[h + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < G; ++h) x[h] = __ldcg(s + h);
+      }
+      float w = 0.f;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float l = lse[h];  // -inf: the head's attention was written as empty
+        w += l > -INFINITY ? tally_clean(exp2f(fmaf(-l, kLog2e, x[h]))) : 0.f;
+      }
+      a.t.weight[at] = was + w;
+      if (fresh) a.t.origin[at] = L - 1 + a.t.evicted[row];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0 && L > 0 && !row_ok)
+      atomicOr(ws.err, PKV_DEVERR_PAGE);
+  }
+  if (!waited) pdl_wait();
+}
+
+template <int G>
+cudaError_t launch_add(const DecodeArgs &a, const pkv_tally &t, cudaStream_t st) {
+  const pkv_workspace &ws = a.ws;
+  TallyArgs g{ws, t, a.batch, a.layer, a.k_new != nullptr, (a.flags & PKV_FLAG_PLAN_EARLY) != 0, 0, 0};
+  // Pages of 32 tokens and more: a warp reads 32 of one head's.  Smaller ones: the same
+  // page's next heads, whose entries follow, down to 4 tokens of 8 heads for flat
+  // indices, where a slot's heads share a 32-byte sector.
+  g.tl_log = 2;
+  while (g.tl_log < 5 && (2 << g.tl_log) <= ws.page_size) ++g.tl_log;
+  while (g.tl_log < 5 && (1 << (4 - g.tl_log)) >= ws.n_kv_heads) ++g.tl_log;
+  g.hl_log = 5 - g.tl_log;
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  // about one wave of resident warps, shared by the requests
+  const int by = a.batch < 65535 ? a.batch : 65535;
+  const int bx = (8 * sms + by - 1) / by;
+  return launch_pdl(tally_add_kernel<G>, dim3(bx, by), dim3(kTThreads), 0, st, g);
+}
+
+}  // namespace
+
+cudaError_t launch_tally_decode(const DecodeArgs &a0, const pkv_tally &t, cudaStream_t st) {
+  DecodeArgs a = a0;
+  a.flags |= PKV_FLAG_WRITE_LSE;
+  a.score = t.score;
+  a.score_tokens = t.score_tokens;
+  const int D = a.ws.head_dim, G = a.ws.n_q_heads / a.ws.n_kv_heads;
+  cudaError_t e = cudaErrorNotSupported;
+#define PKV_TALLY_CASE(DD, GG) \
+  if (D == DD && G == GG) e = launch_mma_one<DD, GG, true>(a, st);
+  PKV_TALLY_CASE(128, 1) PKV_TALLY_CASE(128, 2) PKV_TALLY_CASE(128, 4) PKV_TALLY_CASE(128, 8)
+  PKV_TALLY_CASE(128, 16) PKV_TALLY_CASE(64, 1) PKV_TALLY_CASE(64, 2) PKV_TALLY_CASE(64, 4)
+  PKV_TALLY_CASE(64, 8) PKV_TALLY_CASE(64, 16)
+#undef PKV_TALLY_CASE
+  if (e != cudaSuccess) return e;
+  switch (G) {
+    case 1: return launch_add<1>(a, t, st);
+    case 2: return launch_add<2>(a, t, st);
+    case 4: return launch_add<4>(a, t, st);
+    case 8: return launch_add<8>(a, t, st);
+    case 16: return launch_add<16>(a, t, st);
+  }
+  return cudaErrorNotSupported;
+}
+
+}  // namespace pkv

@@ -12,8 +12,20 @@ from __future__ import annotations
 import torch
 
 from . import _abi
-from .kv8 import check_cache
+from .kv8 import QkNormRopeAxes, check_cache
+from .tally import check_tally
 from .workspace import Workspace
+
+
+def _norm_struct(r):
+    return r.args if isinstance(r, QkNormRopeAxes) else r.struct
+
+
+class _AxesArgs:
+    """What pkv_qk_norm_rope_axes takes of a QkNormRopeAxes, with the step's error word."""
+
+    def __init__(self, args, axes, widths, max_tokens):
+        self.args, self.axes, self.widths, self.max_tokens = args, axes, widths, max_tokens
 
 
 class BindTracker:
@@ -29,6 +41,12 @@ class BindTracker:
         self.ids, self.lens = list(ids), list(lens)
         return _abi.PKV_BIND_STEADY if steady else _abi.PKV_BIND_REBUILD
 
+    def evicted(self, eviction):
+        """The step cut its requests past the limit (an Eviction): their next lengths
+        follow on the shorter ones."""
+        if self.lens is not None:
+            self.lens = [eviction.length(n) for n in self.lens]
+
 
 class DecodeRunner:
     """Drives libpkv for one batch size on one stream."""
@@ -36,17 +54,29 @@ class DecodeRunner:
     def __init__(self, ws: Workspace, batch: int, *, num_splits: int = 1, flags: int = 0,
                  scale: float | None = None, stream: torch.cuda.Stream | None = None,
                  fused: bool = True, plan: bool = False, out_per_layer: bool = False,
-                 cache=None, norm_rope=None):
+                 cache=None, norm_rope=None, tally=None, evict=None):
         """cache: a Kv8Cache of this workspace; the layers then append to and
         attend over it instead of the bf16 pools (flags: PKV_FLAG_OUT_F32 and
         PKV_FLAG_WRITE_LSE).  norm_rope: a QkNormRope, or one per layer, applied
         to the layer's q and k at ws.position_ids before they are used (its arguments
         are copied here); a step's device errors all go to ws.err, the norm's too,
-        whatever its own word is."""
+        whatever its own word is.  A QkNormRopeAxes takes ws.position_ids on every axis,
+        moved by its own evicted and delta (rows: ws.req_pool_indices).
+        tally: a Tally of this workspace; the layers add their attention weights to it
+        (fused layers on the bf16 pools).  evict: an Eviction that ends every step; a
+        norm_rope then has to be a QkNormRopeAxes with evicted=tally.evicted, as a token's
+        position is no longer its index."""
         if cache is not None and (not fused or plan):
             raise ValueError("a step on the 8-bit cache has no unfused or planned form")
         if cache is not None:
             check_cache(ws, cache)
+        if tally is not None and (cache is not None or not fused):
+            raise ValueError("the tally is of fused layers on the bf16 pools")
+        if evict is not None and tally is None:
+            raise ValueError("an eviction needs a tally")
+        if tally is not None:
+            check_tally(ws, tally, batch)
+        self.tally, self.evict = tally, evict
         self.cache = cache
         self.ws = ws
         self.batch = batch
@@ -67,15 +97,27 @@ class DecodeRunner:
             self.norm_rope = (list(norm_rope) if isinstance(norm_rope, (list, tuple))
                               else [norm_rope] * NL)
             if len(self.norm_rope) != NL or any(
-                    (r.struct.n_q_heads, r.struct.n_kv_heads, r.struct.head_dim) !=
-                    (sh["n_q_heads"], sh["n_kv_heads"], sh["head_dim"]) for r in self.norm_rope):
+                    (st.n_q_heads, st.n_kv_heads, st.head_dim) !=
+                    (sh["n_q_heads"], sh["n_kv_heads"], sh["head_dim"])
+                    for st in map(_norm_struct, self.norm_rope)):
                 raise ValueError("norm_rope: one QkNormRope of the workspace's heads per layer")
+            axes = [r for r in self.norm_rope if isinstance(r, QkNormRopeAxes)]
+            if any(r.rows is not None and r.rows.data_ptr() != ws.req_pool_indices.data_ptr()
+                   for r in axes):
+                raise ValueError("norm_rope: rows are the workspace's req_pool_indices")
+            if evict is not None and (len(axes) != NL or any(
+                    r.evicted is None or r.evicted.data_ptr() != tally.evicted.data_ptr()
+                    for r in axes)):
+                raise ValueError("a step that evicts takes its positions by a QkNormRopeAxes with "
+                                 "evicted=tally.evicted")
             if any(r.err.device != ws.err.device for r in self.norm_rope):
                 raise ValueError("norm_rope: its tensors are not on the workspace's device")
             self.rope_args = []
             for r in self.norm_rope:
-                args = _abi.PkvQkNormRopeArgs.from_buffer_copy(r.struct)
+                args = _abi.PkvQkNormRopeArgs.from_buffer_copy(_norm_struct(r))
                 args.err, args.widths = ws.err.data_ptr(), r.widths
+                if isinstance(r, QkNormRopeAxes):
+                    args = _AxesArgs(args, r.axes, r.widths, r.max_tokens)
                 self.rope_args.append(args)
             # one layer's rows at a time: the next layer's kernel waits for this one's
             self.q_use = torch.zeros_like(self.q_in[0])
@@ -108,13 +150,16 @@ class DecodeRunner:
         # programmatic dependent launch the plan saves no time, and a one-layer
         # step pays for the extra launch.
         self.use_plan = plan and fused and mma and ws.work_plan is not None
-        if cache is not None:
-            per_layer = 2  # append, attention (with its merge)
+        if cache is not None or tally is not None:
+            # append, attention (with its merge); or that and the weights' addition
+            per_layer = 2
         else:
             per_layer = 1 if fused and mma else 2 + int(split)
         per_layer += int(self.norm_rope is not None)
         self.launches_per_step = (1 + int(flat) + int(self.use_plan and 0 < batch <= 256) +
-                                  NL * per_layer)
+                                  NL * per_layer + int(evict is not None))
+        # the most that a request of this step may hold, for the eviction's launch
+        self.evict_len = min(sh["max_pages_per_req"] * sh["page_size"], _abi.PKV_TALLY_MAX_LEN)
 
     def _wsl(self, l):
         return self.views[l] if self.views is not None else self.ws
@@ -132,8 +177,10 @@ class DecodeRunner:
         s = self._s()
         q, k = self.q_in[l], self.k_in[l]
         if self.norm_rope is not None:
-            _abi.pkv_qk_norm_rope(self.rope_args[l], self.batch, q, k, self.ws.position_ids,
-                                  self.q_use, self.k_use, s)
+            call = (_abi.pkv_qk_norm_rope_axes if isinstance(self.rope_args[l], _AxesArgs)
+                    else _abi.pkv_qk_norm_rope)
+            call(self.rope_args[l], self.batch, q, k, self.ws.position_ids, self.q_use,
+                 self.k_use, s)
             q, k = self.q_use, self.k_use
         if self.cache is not None:
             if events is not None:
@@ -152,8 +199,13 @@ class DecodeRunner:
             # more launches earlier, so they may start before layer l-1 ends.
             early = _abi.PKV_FLAG_PLAN_EARLY if (l > 0 and events is None) else 0
             use = _abi.PKV_FLAG_USE_PLAN if self.use_plan else 0
-            _abi.pkv_decode_layer(self._wsl(l), self.batch, l, q, k, self.v_in[l], self.scale,
-                                  self.num_splits, self.flags | early | use, s)
+            if self.tally is not None:
+                _abi.pkv_tally_decode_layer(self._wsl(l), self.tally, self.batch, l, q, k,
+                                            self.v_in[l], self.scale, self.num_splits,
+                                            self.flags | early | use, s)
+            else:
+                _abi.pkv_decode_layer(self._wsl(l), self.batch, l, q, k, self.v_in[l], self.scale,
+                                      self.num_splits, self.flags | early | use, s)
             if events is not None:
                 events[1].record(s)
             return
@@ -173,6 +225,10 @@ class DecodeRunner:
         self.bind(mode)
         for l in range(self.ws.shape["n_layers"]):
             self.layer(l, None if layer_events is None else layer_events[l])
+        if self.evict is not None:
+            e = self.evict
+            _abi.pkv_tally_evict(self.ws, self.tally, self.batch, self.evict_len, e.limit, e.budget,
+                                 e.sinks, e.recent, self._s())
 
     # --- CUDA graph -----------------------------------------------------------
     def capture(self, mode=_abi.PKV_BIND_STEADY, layer_events=None):

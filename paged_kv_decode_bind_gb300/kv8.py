@@ -171,6 +171,51 @@ class QkNormRope:
             cos_sin=_abi._ptr(cos_sin) if rot_dim else None, err=self.err.data_ptr())
 
 
+class QkNormRopeAxes:
+    """Arguments of ``pkv_qk_norm_rope_axes``: a QkNormRope whose pairs follow several
+    axes (time, height, width).
+
+    axis_of_pair: the axis of each of the rot_dim / 2 pairs, or sections: how many pairs
+    in a row each axis has, as (16, 24, 24).  Neither: one axis.
+    rows, evicted, delta: int32 device tensors; a token's positions move by
+    evicted[rows[t]] + delta[rows[t]] (either may be None).  In a decode step rows is
+    ws.req_pool_indices and evicted a Tally's, so that the position is the count of all the
+    request's tokens; delta is what its images took from that.  Other arguments are
+    QkNormRope's."""
+
+    def __init__(self, *, axis_of_pair=None, sections=None, rows=None, evicted=None, delta=None,
+                 **norm):
+        self.norm = QkNormRope(**norm)
+        self.args, self.err, self.widths = self.norm.struct, self.norm.err, self.norm.widths
+        pairs = self.args.rot_dim // 2
+        if axis_of_pair is not None and sections is not None:
+            raise ValueError("axis_of_pair or sections, not both")
+        if sections is not None:
+            axis_of_pair = [a for a, n in enumerate(sections) for _ in range(n)]
+        elif axis_of_pair is None:
+            axis_of_pair = [0] * pairs
+        axis_of_pair = [int(a) for a in axis_of_pair]
+        if len(axis_of_pair) != pairs or any(not 0 <= a < 4 for a in axis_of_pair):
+            raise ValueError(f"an axis 0 .. 3 for each of {pairs} pairs")
+        shifts = [x for x in (evicted, delta) if x is not None]
+        if (rows is None) != (not shifts):
+            raise ValueError("rows goes with evicted or delta")
+        for x in [rows] * (rows is not None) + shifts:
+            if x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous():
+                raise ValueError("rows, evicted and delta are dense int32 vectors")
+            if x.device != self.err.device:
+                raise ValueError(f"the tensors are on {x.device} and {self.err.device}")
+        if len({x.numel() for x in shifts}) > 1:
+            raise ValueError("evicted and delta are of one length")
+        self.rows, self.evicted, self.delta = rows, evicted, delta
+        self.max_tokens = rows.numel() if rows is not None else 2 ** 31 - 1
+        n_axes = len(sections) if sections is not None else max(axis_of_pair, default=0) + 1
+        self.axes = _abi.PkvRopeAxes(
+            n_axes=n_axes, n_rows=shifts[0].numel() if shifts else 0, rows=_abi._ptr(rows),
+            evicted=_abi._ptr(evicted), delta=_abi._ptr(delta),
+            axis=(_abi.ctypes.c_uint8 * 128)(*axis_of_pair))
+
+
 def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
     """cos_sin of positions 0 .. positions - 1: angle p * base^(-2 i / rot_dim) of
     pair i, taken in 64 bits (a far position's angle loses its fraction in 32)."""
