@@ -238,6 +238,18 @@ def test_extend_window(cuda, window, heads):
     _check_tally(tally, ref)
 
 
+@pytest.mark.parametrize("window", [40, 100, 150])  # one query tile, two, three
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 5)])
+def test_extend_more_units_than_ctas(cuda, window, d, page):
+    """Every CTA takes several units, whose key and query tiles follow one another through
+    the same shared memory."""
+    lens, new = [2600, 2500, 900, 2300, 130], [150, 149, 150, 20, 130]
+    p = P.problem(lens, page=page, heads=(32, 8), d=d)
+    ws, tally, ref, _ = _extend(p, lens, new, window=window)
+    assert int(ws.err.item()) == 0
+    _check_tally(tally, ref)
+
+
 def test_extend_sums_to_the_observed_queries(cuda):
     """A whole prompt: every observed query's weights sum to one a head, whatever the
     tiles; a long context of several key tiles and query tiles a unit."""
