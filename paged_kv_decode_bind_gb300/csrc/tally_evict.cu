@@ -11,7 +11,7 @@
 // every kept token behind the first gap (at 4096 -> 1024 tokens about twice the rows).
 // Keys carry their rotation, so attention does not depend on a token's index.
 //
-// A (request, layer, head) unit is a cluster of C CTAs (1 to 8), each with a contiguous
+// A (request, layer, head) unit is a cluster of C CTAs (1 to 16), each with a contiguous
 // segment of the request's tokens; histograms, counts and the lists of movers and free
 // indices are read from the other CTAs' shared memory.  The unit that finishes last of a
 // request (a ticket on split_counters) writes its new length.
@@ -25,12 +25,14 @@ namespace pkv {
 
 namespace {
 
-constexpr int kEThreads = 512;
+constexpr int kEThreads = 256;
 constexpr int kEWarps = kEThreads / 32;
-constexpr int kEMaxCluster = 8;
-constexpr int kESegMax = PKV_TALLY_MAX_LEN / kEMaxCluster;  // tokens of a CTA at most
+constexpr int kEPerSM = 4;        // CTAs of an SM: some choose while others move rows
+constexpr int kEMaxCluster = 16;  // (8 where the device has no room for 16)
+constexpr int kESegMax = PKV_TALLY_MAX_LEN / 8;  // tokens of a CTA at most
+constexpr int kEBatch = 16;       // rows that a warp moves at a time
 constexpr int kECopies = 8;    // of a histogram: lanes of a warp often hit one bin
-constexpr int kEPer = 4;       // keys of a thread per scan chunk
+constexpr int kEPer = 8;       // keys of a thread per scan chunk
 
 struct EvictArgs {
   pkv_workspace ws;
@@ -48,6 +50,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::
                    : "memory");
+}
+// 32-bit word at this CTA's shared address `addr`, in every CTA of the cluster: their sum
+__device__ __forceinline__ int ld_cluster(uint32_t addr, int rank);
+__device__ __forceinline__ int sum_cluster(uint32_t addr, int C) {
+  int sum = 0;
+  for (int c0 = 0; c0 < C; c0 += 4) {  // C is a power of two; four loads in flight
+    int v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c0 + j < C) v[j] = ld_cluster(addr, c0 + j);
+    sum += (v[0] + v[1]) + (v[2] + v[3]);
+  }
+  return sum;
 }
 // 32-bit word at this CTA's shared address `addr`, in CTA `rank` of the cluster
 __device__ __forceinline__ int ld_cluster(uint32_t addr, int rank) {
@@ -101,14 +116,16 @@ __device__ __forceinline__ void block_scan2(int &x, int &y, int *s, int &tx, int
 }
 
 template <int D>
-__global__ void __launch_bounds__(kEThreads, 2)
+__global__ void __launch_bounds__(kEThreads, kEPerSM)
     tally_evict_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint32_t s_key[];  // [seg] keys, then the CTA's list
   __shared__ int s_hist[4][256];
   __shared__ int s_copy[kECopies][256];
   __shared__ int s_scan[2 * kEWarps];
-  __shared__ int s_bin[2];     // the pass's digit, and how many of its keys are wanted
-  __shared__ int s_info[4];    // for the cluster: bad page bits, ties, free indices, movers
+  __shared__ int s_bin[3];   // the pass's digit, how many of its keys are wanted, and all
+  __shared__ int s_info[4];  // for the cluster: bad page bits, ties, free indices, movers
+  // of each CTA of the cluster: free indices and movers before it, its free indices
+  __shared__ int s_fbase[kEMaxCluster + 1], s_mbase[kEMaxCluster + 1], s_fcnt[kEMaxCluster];
   const pkv_workspace &ws = a.ws;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.cluster, rank = (int)cluster_rank();
@@ -143,23 +160,38 @@ __global__ void __launch_bounds__(kEThreads, 2)
   __syncthreads();
   // ---- keys of the segment, and the histogram of their first digit ----
   int bad = 0;
-#pragma unroll 4
-  for (int i = tid; i < n; i += kEThreads) {
-    const int t = t0 + i;
-    const int page = table[pl.page_of(t)];
-    uint32_t key = 0;
-    if (page >= 0 && page < pl.n_pages) {
-      const long long at = tally_at(ws, pl.n_pages, layer, page, g, pl.in_page(t));
-      const int o = a.t.origin[at];
-      key = rank_key(a.t.weight[at], o < a.sinks || o >= late);
-    } else {
-      bad = 1;
+  constexpr int KU = 8;  // keys whose loads a thread has in flight
+  for (int i0 = tid; i0 < n; i0 += KU * kEThreads) {
+    int page[KU], org[KU];
+    float wgt[KU];
+#pragma unroll
+    for (int j = 0; j < KU; ++j) {
+      const int i = i0 + j * kEThreads;
+      page[j] = i < n ? table[pl.page_of(t0 + i)] : 0;
     }
-    s_key[i] = key;
-    atomicAdd(&s_copy[lane & (kECopies - 1)][key >> 24], 1);
+#pragma unroll
+    for (int j = 0; j < KU; ++j) {
+      const int i = i0 + j * kEThreads;
+      if (page[j] < 0 || page[j] >= pl.n_pages) {
+        bad = 1;
+        page[j] = 0;
+      }
+      if (i >= n) continue;
+      const long long at = tally_at(ws, pl.n_pages, layer, page[j], g, pl.in_page(t0 + i));
+      org[j] = a.t.origin[at];
+      wgt[j] = a.t.weight[at];
+    }
+#pragma unroll
+    for (int j = 0; j < KU; ++j) {
+      const int i = i0 + j * kEThreads;
+      if (i >= n) continue;
+      const uint32_t key = rank_key(wgt[j], org[j] < a.sinks || org[j] >= late);
+      s_key[i] = key;
+      atomicAdd(&s_copy[lane & (kECopies - 1)][key >> 24], 1);
+    }
   }
   bad = __syncthreads_or(bad);
-  if (tid < 256) {
+  {
     int sum = 0;
 #pragma unroll
     for (int c = 0; c < kECopies; ++c) sum += s_copy[c][tid];
@@ -168,6 +200,10 @@ __global__ void __launch_bounds__(kEThreads, 2)
   if (tid == 0) s_info[0] = bad;
   // ---- radix select of the budget-th key ----
   uint32_t prefix = 0;
+  auto unit_sync = [&]() {
+    if (C == 1) __syncthreads();
+    else cluster_sync();
+  };
   int want = a.budget;  // of the keys that share the prefix, how many stay
   int equal = 0;        // keys of the cluster equal to the one found
   for (int pass = 0; pass < 4; ++pass) {
@@ -178,49 +214,39 @@ __global__ void __launch_bounds__(kEThreads, 2)
         if ((key >> (shift + 8)) == prefix) atomicAdd(&s_hist[pass][(key >> shift) & 255], 1);
       }
     }
-    cluster_sync();  // every CTA's histogram of the pass (each pass has its own)
+    unit_sync();  // every CTA's histogram of the pass (each pass has its own)
     if (pass == 0) {
-      for (int c = 0; c < C; ++c) bad |= ld_cluster(smem_addr(&s_info[0]), c);
+      bad = sum_cluster(smem_addr(&s_info[0]), C);
     }
-    if (warp == 0) {
-      // lane l: the eight bins from the top, 255 - 8 l ... 248 - 8 l
-      int cnt[8], sum = 0;
+    // a bin a thread, from the top
+    const uint32_t bin = smem_addr(&s_hist[pass][255 - tid]);
+    int cnt = 0;
+    if (C == 1) cnt = s_hist[pass][255 - tid];
+    else cnt = sum_cluster(bin, C);
+    int above = cnt;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        cnt[j] = 0;
-        for (int c = 0; c < C; ++c)
-          cnt[j] += ld_cluster(smem_addr(&s_hist[pass][255 - 8 * lane - j]), c);
-        sum += cnt[j];
-      }
-      int above = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, above, d);
-        if (lane >= d) above += v;
-      }
-      above -= sum;  // keys in bins above this lane's
-      if (above < want && want <= above + sum) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (above < want && want <= above + cnt[j]) {
-            s_bin[0] = 255 - 8 * lane - j;
-            s_bin[1] = want - above;
-            s_scan[0] = cnt[j];
-          }
-          above += cnt[j];
-        }
-      }
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, above, d);
+      if (lane >= d) above += v;
+    }
+    if (lane == 31) s_scan[warp] = above;
+    __syncthreads();
+    above -= cnt;
+    for (int w = 0; w < warp; ++w) above += s_scan[w];
+    if (above < want && want <= above + cnt) {
+      s_bin[0] = 255 - tid;
+      s_bin[1] = want - above;
+      s_bin[2] = cnt;
     }
     __syncthreads();
     prefix = (prefix << 8) | (uint32_t)s_bin[0];
     want = s_bin[1];
-    equal = s_scan[0];
-    __syncthreads();
+    equal = s_bin[2];
   }
   // every CTA of the cluster agrees on `bad`, and a request's units read the same table
   if (bad) {
     if (first) atomicOr(ws.err, PKV_DEVERR_PAGE);
-    cluster_sync();  // no shared memory leaves while a neighbour may read it
+    unit_sync();  // no shared memory leaves while a neighbour may read it
     return;
   }
   // ---- ties: those of lower index stay, so each CTA needs the count before it ----
@@ -231,7 +257,7 @@ __global__ void __launch_bounds__(kEThreads, 2)
     int zero = 0, tot, z;
     block_scan2(mine, zero, s_scan, tot, z);
     if (tid == 0) s_info[1] = tot;
-    cluster_sync();
+    unit_sync();
     tie_left = want;
     for (int c = 0; c < rank; ++c) tie_left -= ld_cluster(smem_addr(&s_info[1]), c);
   }
@@ -241,12 +267,18 @@ __global__ void __launch_bounds__(kEThreads, 2)
   for (int c0 = 0; c0 < n; c0 += kEThreads * kEPer) {
     const int i0 = c0 + tid * kEPer;
     uint32_t key[kEPer];
+#pragma unroll
+    for (int j = 0; j < kEPer; j += 4) {
+      const uint4 k4 = i0 + j < n ? *reinterpret_cast<const uint4 *>(s_key + i0 + j)
+                                  : make_uint4(0, 0, 0, 0);
+      key[j] = k4.x;
+      key[j + 1] = k4.y;
+      key[j + 2] = k4.z;
+      key[j + 3] = k4.w;
+    }
     int eq = 0;
 #pragma unroll
-    for (int j = 0; j < kEPer; ++j) {
-      key[j] = i0 + j < n ? s_key[i0 + j] : 0u;
-      eq += i0 + j < n && key[j] == prefix;
-    }
+    for (int j = 0; j < kEPer; ++j) eq += i0 + j < n && key[j] == prefix;
     int tie = eq, dummy = 0, ttot, dtot;
     if (want < equal) {
       block_scan2(tie, dummy, s_scan, ttot, dtot);
@@ -282,82 +314,83 @@ __global__ void __launch_bounds__(kEThreads, 2)
     s_info[2] = freed;
     s_info[3] = listed - freed;
   }
-  cluster_sync();
-  // ---- the rows move: mover j of the unit to free index j, shared out evenly ----
-  int fbase[kEMaxCluster + 1], mbase[kEMaxCluster + 1], fcnt[kEMaxCluster];
-  fbase[0] = mbase[0] = 0;
+  unit_sync();
+  if (warp == 0) {
+    const int f = lane < C ? ld_cluster(smem_addr(&s_info[2]), lane) : 0;
+    const int m = lane < C ? ld_cluster(smem_addr(&s_info[3]), lane) : 0;
+    int fs = f, ms = m;
 #pragma unroll
-  for (int c = 0; c < kEMaxCluster; ++c) {
-    const int f = c < C ? ld_cluster(smem_addr(&s_info[2]), c) : 0;
-    const int m = c < C ? ld_cluster(smem_addr(&s_info[3]), c) : 0;
-    fcnt[c] = f;
-    fbase[c + 1] = fbase[c] + f;
-    mbase[c + 1] = mbase[c] + m;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, fs, d), y = __shfl_up_sync(0xffffffffu, ms, d);
+      if (lane >= d) {
+        fs += x;
+        ms += y;
+      }
+    }
+    if (lane <= kEMaxCluster) {  // those past C hold the totals
+      s_fbase[lane] = fs - f;
+      s_mbase[lane] = ms - m;
+      if (lane < kEMaxCluster) s_fcnt[lane] = f;
+    }
   }
-  const int M = min(mbase[kEMaxCluster], fbase[kEMaxCluster]);  // equal
+  __syncthreads();
+  // ---- the rows move: mover j of the unit to free index j, shared out evenly ----
+  const int M = min(s_mbase[C], s_fbase[C]);  // equal
   constexpr int LPR = D / 8;     // lanes of a row, 16 bytes each
   constexpr int RPW = 32 / LPR;  // rows a warp instruction
-  constexpr int UN = 4;          // warp instructions in flight (K and V each)
+  constexpr int UN = 2;          // warp instructions in flight (K and V each)
   const int sub = lane / LPR, ch = lane % LPR;
   const long long head0 = ((long long)layer * ws.pool_slots * ws.n_kv_heads + g) * LPR + ch;
   uint4 *kp = static_cast<uint4 *>(ws.k_pool) + head0;
   uint4 *vp = static_cast<uint4 *>(ws.v_pool) + head0;
   const long long slot_vecs = (long long)ws.n_kv_heads * LPR;
-  for (int j0 = (rank * kEWarps + warp) * 32; j0 < M; j0 += C * kEThreads) {
-    const int j = j0 + lane;
+  for (int j0 = (rank * kEWarps + warp) * kEBatch; j0 < M; j0 += C * kEWarps * kEBatch) {
+    const int j = j0 + lane, m = min(kEBatch, M - j0);
     int src = 0, dst = 0;  // slots of this lane's mover
-    if (j < M) {
+    if (lane < m) {
       int cf = 0, cm = 0;
-#pragma unroll
-      for (int c = 1; c < kEMaxCluster; ++c) {
-        cf += j >= fbase[c];
-        cm += j >= mbase[c];
-      }
-      int fb = 0, mb = 0, fn = 0;
-#pragma unroll
-      for (int c = 0; c < kEMaxCluster; ++c) {
-        if (c == cf) fb = fbase[c];
-        if (c == cm) {
-          mb = mbase[c];
-          fn = fcnt[c];
-        }
+      for (int c = 1; c < C; ++c) {
+        cf += j >= s_fbase[c];
+        cm += j >= s_mbase[c];
       }
       const uint32_t list = smem_addr(s_key);
-      const int to = ld_cluster(list + 4 * (j - fb), cf);
-      const int from = ld_cluster(list + 4 * (fn + j - mb), cm);
+      const int to = ld_cluster(list + 4 * (j - s_fbase[cf]), cf);
+      const int from = ld_cluster(list + 4 * (s_fcnt[cm] + j - s_mbase[cm]), cm);
       const int ps = table[pl.page_of(from)], pd = table[pl.page_of(to)];
       src = ps * pl.P + pl.in_page(from);
       dst = pd * pl.P + pl.in_page(to);
       const long long as = tally_at(ws, pl.n_pages, layer, ps, g, pl.in_page(from));
       const long long ad = tally_at(ws, pl.n_pages, layer, pd, g, pl.in_page(to));
-      a.t.weight[ad] = a.t.weight[as];
-      a.t.origin[ad] = a.t.origin[as];
+      const float w = a.t.weight[as];
+      const int o = a.t.origin[as];
+      a.t.weight[ad] = w;
+      a.t.origin[ad] = o;
     }
-    const int m = min(32, M - j0);
-    for (int k0 = 0; k0 < m; k0 += UN * RPW) {
+#pragma unroll
+    for (int k0 = 0; k0 < kEBatch; k0 += UN * RPW) {
       uint4 kx[UN], vx[UN];
-      int to[UN];
+      long long to[UN];
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
         const int k = k0 + u * RPW + sub;
-        const int from = __shfl_sync(0xffffffffu, src, k & 31);
-        to[u] = __shfl_sync(0xffffffffu, dst, k & 31);
+        const long long from = __shfl_sync(0xffffffffu, src, k) * slot_vecs;
+        to[u] = __shfl_sync(0xffffffffu, dst, k) * slot_vecs;
         if (k >= m) to[u] = -1;
         if (to[u] >= 0) {
-          kx[u] = kp[from * slot_vecs];
-          vx[u] = vp[from * slot_vecs];
+          kx[u] = kp[from];
+          vx[u] = vp[from];
         }
       }
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
         if (to[u] >= 0) {
-          kp[to[u] * slot_vecs] = kx[u];
-          vp[to[u] * slot_vecs] = vx[u];
+          kp[to[u]] = kx[u];
+          vp[to[u]] = vx[u];
         }
       }
     }
   }
-  cluster_sync();  // the lists stay until every CTA has read them
+  unit_sync();  // the lists stay until every CTA has read them
   if (rank == 0 && tid == 0) {
     // every unit of the request has read its length before its ticket
     int *ctr = ws.split_counters + b;
@@ -375,25 +408,42 @@ cudaError_t launch_one(EvictArgs a, cudaStream_t st) {
   cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
   const long long units = (long long)a.batch * a.ws.n_layers * a.ws.n_kv_heads;
-  // CTAs per unit: segments of 8192 tokens at most while the cluster can grow, and more
+  auto kern = tally_evict_kernel<D>;
+  static int most[64] = {0};  // CTAs of a cluster at most, by device
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  int &top = most[dev & 63];
+  if (top == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kESegMax * 4);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kEMaxCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.gridDim = dim3(kEMaxCluster);
+    c.blockDim = dim3(kEThreads);
+    c.dynamicSmemBytes = PKV_TALLY_MAX_LEN / kEMaxCluster * 4;
+    c.attrs = at;
+    c.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &c) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    top = n > 0 ? kEMaxCluster : 8;
+  }
+  // CTAs per unit: segments of 4096 tokens at most while the cluster can grow, and more
   // CTAs while the units leave SMs idle and segments stay at 1024 tokens or more
   int C = 1;
-  while (C < kEMaxCluster &&
-         (a.max_len > 8192 * C || (units * C * 2 <= sms && a.max_len >= 2048 * C)))
+  while (C < top && (a.max_len > 4096 * C || (units * C * 2 <= sms && a.max_len >= 2048 * C)))
     C *= 2;
   if (units * C > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   a.cluster = C;
   a.seg = ((a.max_len + C - 1) / C + kEPer - 1) / kEPer * kEPer;
   const size_t smem = (size_t)a.seg * 4;
-  auto kern = tally_evict_kernel<D>;
-  static bool set[64] = {false};
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if (!set[dev & 63]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kESegMax * 4);
-    if (e != cudaSuccess) return e;
-    set[dev & 63] = true;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * C));
   cfg.blockDim = dim3(kEThreads);
