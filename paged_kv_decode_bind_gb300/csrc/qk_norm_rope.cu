@@ -41,9 +41,10 @@ struct RopeArgs {
 };
 
 // Several axes: cosines and sines of this lane's eight pairs (first pair 8 l), each from
-// the row of its axis's position.  Returns whether the token is written as zeros.  A lane
-// reads the rows of the axes its pairs follow, whole, and picks: sections of 8 pairs and
-// more read one row, as without axes.
+// the row of its axis's position.  Returns whether the token is written as zeros.  Where
+// the eight pairs of every lane follow one axis (sections of 8 pairs and more), a lane
+// reads its row as without axes, 16 bytes at a time; else pair by pair, all sixteen loads
+// in flight.
 __device__ __forceinline__ bool axes_rows(const pkv_qk_norm_rope_args &p, const AxesArgs &x,
                                           const int *positions, long long tok, int l, bool turns,
                                           bool lead, float (&cs)[8], float (&sn)[8]) {
@@ -72,25 +73,24 @@ __device__ __forceinline__ bool axes_rows(const pkv_qk_norm_rope_args &p, const 
   }
   if (err && !none && lead) atomicOr(p.err, PKV_DEVERR_POSITION);
   if (err || none) return true;
-  if (turns) {
-    const uint32_t mine = x.axis[l >> 1] >> (16 * (l & 1));
+  const uint32_t mine = (x.axis[l >> 1] >> (16 * (l & 1))) & 0xffffu;
+  const float *row0 = p.cos_sin + 8 * l;
+  if (__all_sync(0xffffffffu, !turns || mine == (mine & 3u) * 0x5555u)) {
+    if (!turns) return false;
+    const int a = mine & 3;
+    const long long at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
+    const float4 *row = reinterpret_cast<const float4 *>(row0 + at * rot);
+    *reinterpret_cast<float4 *>(cs) = row[0];
+    *reinterpret_cast<float4 *>(cs + 4) = row[1];
+    *reinterpret_cast<float4 *>(sn) = row[rot / 8];
+    *reinterpret_cast<float4 *>(sn + 4) = row[rot / 8 + 1];
+  } else if (turns) {
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      unsigned take = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) take |= (unsigned)((mine >> (2 * e) & 3) == (uint32_t)a) << e;
-      if (take == 0) continue;
-      const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + pos[a] * rot);
-      float c[8], s[8];
-      *reinterpret_cast<float4 *>(c) = row[2 * l];
-      *reinterpret_cast<float4 *>(c + 4) = row[2 * l + 1];
-      *reinterpret_cast<float4 *>(s) = row[rot / 8 + 2 * l];
-      *reinterpret_cast<float4 *>(s + 4) = row[rot / 8 + 2 * l + 1];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        cs[e] = take >> e & 1 ? c[e] : cs[e];
-        sn[e] = take >> e & 1 ? s[e] : sn[e];
-      }
+    for (int e = 0; e < 8; ++e) {
+      const int a = mine >> (2 * e) & 3;
+      const long long at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
+      cs[e] = row0[at * rot + e];
+      sn[e] = row0[at * rot + rot / 2 + e];
     }
   }
   return false;

@@ -7,6 +7,8 @@
 // split is merged, so it cannot be added where the score is made.  The scores are 4 G
 // bytes a token and head beside the 4 D of its K and V (3 % at G = 4, D = 128), stay in
 // L2, and spare a second reading of K.
+#include <algorithm>
+
 #include "decode_mma.cuh"
 #include "tally.cuh"
 
@@ -15,82 +17,115 @@ namespace pkv {
 namespace {
 
 constexpr int kTThreads = 256;
+constexpr int kAddItems = 2;  // items of a warp whose loads are in flight (4: spilled registers)
 
 struct TallyArgs {
   pkv_workspace ws;
   pkv_tally t;
   int batch, layer;
   int appended;  // the newest token's entry starts anew
-  int early;     // lengths, tables and rows are older than the previous launch
   int tl_log, hl_log;  // a warp takes 2^tl tokens of 2^hl KV heads
 };
 
-// One warp: 2^tl_log tokens x 2^hl_log heads, a lane each.  Tokens run fastest over the
-// lanes, so that a page's entries of a head, and a head's scores, are read in runs.
+// G consecutive values.
+template <int G, bool CG>
+__device__ __forceinline__ void load_group(float (&x)[G], const float *s) {
+  if constexpr (G >= 4) {
+#pragma unroll
+    for (int h = 0; h < G; h += 4) {
+      const float4 *p = reinterpret_cast<const float4 *>(s + h);
+      const float4 v = CG ? __ldcg(p) : *p;
+      x[h] = v.x;
+      x[h + 1] = v.y;
+      x[h + 2] = v.z;
+      x[h + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < G; ++h) x[h] = CG ? __ldcg(s + h) : s[h];
+  }
+}
+
+// One item of a warp: 2^tl_log tokens x 2^hl_log heads, a lane each.  Tokens run fastest
+// over the lanes, so that a page's entries of a head, and a head's scores, are read in
+// runs.  A warp has UN items' loads in flight.
+//
+// The launch waits for the attention only where it reads what that writes, the scores and
+// log-sum-exps: lengths, tables and the tally are older than the attention's own start,
+// as this launch starts behind the attention's wait for its predecessor.
 template <int G>
-__global__ void __launch_bounds__(kTThreads)
+__global__ void __launch_bounds__(kTThreads, 4)
     tally_add_kernel(const __grid_constant__ TallyArgs a) {
+  constexpr int UN = kAddItems;
   const pkv_workspace &ws = a.ws;
   pdl_trigger();
-  if (!a.early) pdl_wait();
   Plan pl;
   pl.set_pages(ws);
   const int lane = threadIdx.x & 31;
   const int ts = lane & ((1 << a.tl_log) - 1), hs = lane >> a.tl_log;
   const int hgroups = (ws.n_kv_heads + (1 << a.hl_log) - 1) >> a.hl_log;
   const int Hq = ws.n_q_heads;
-  bool waited = !a.early;
+  bool waited = false;
   for (int b = blockIdx.y; b < a.batch; b += gridDim.y) {
     const int L = usable_len(ws, b);
     const ReqIndex ri = req_index(ws, b);
     const int row = ws.req_pool_indices[b];
     const bool row_ok = row >= 0 && row < ws.max_reqs;
-    const int tgroups = (L + (1 << a.tl_log) - 1) >> a.tl_log;
-    const long long items = (long long)tgroups * hgroups;
-    const long long step = (long long)gridDim.x * (kTThreads / 32);
-    for (long long it = (long long)blockIdx.x * (kTThreads / 32) + (threadIdx.x >> 5); it < items;
-         it += step) {
-      const int tg = (int)(it / hgroups), hg = (int)(it - (long long)tg * hgroups);
-      const int t = (tg << a.tl_log) + ts, g = (hg << a.hl_log) + hs;
-      const bool live = t < L && g < ws.n_kv_heads && ri.ok && row_ok;
-      long long slot = -1;
-      if (live) {
+    // a warp keeps its head group and strides over the groups of tokens
+    const int tgroups = row_ok && ri.ok ? (L + (1 << a.tl_log) - 1) >> a.tl_log : 0;
+    const int wid = blockIdx.x * (kTThreads / 32) + (threadIdx.x >> 5);
+    const int step = gridDim.x * (kTThreads / 32) / hgroups;  // >= 1
+    const int tg0 = wid / hgroups, g = ((wid - tg0 * hgroups) << a.hl_log) + hs;
+    const int first = g < ws.n_kv_heads && tg0 < step ? tg0 : tgroups;
+    float l2[G];  // the heads' lse log2 e; +inf: the attention was written as empty
+    for (int t0 = first; __any_sync(0xffffffffu, t0 < tgroups); t0 += UN * step) {
+      int raw[UN];
+      long long at[UN];
+      float was[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int t = ((t0 + u * step) << a.tl_log) + ts;
+        raw[u] = t0 + u * step < tgroups && t < L ? *index_src(ws, pl, ri, t) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int t = ((t0 + u * step) << a.tl_log) + ts;
         int kind = 0;  // the attention has raised it
-        slot = slot_from_raw(ws, pl, *index_src(ws, pl, ri, t), t, kind);
+        const int slot = (int)slot_from_raw(ws, pl, raw[u], t, kind);
+        at[u] = -1;
+        was[u] = 0.f;
+        if (slot < 0) continue;
+        const int page = pl.page_of(slot);
+        at[u] = tally_at(ws, pl.n_pages, a.layer, page, g, slot - page * pl.P);
+        if (!(a.appended && t == L - 1)) was[u] = a.t.weight[at[u]];
       }
       if (!waited) {
-        pdl_wait();  // scores, log-sum-exps and the tally
+        pdl_wait();
         waited = true;
       }
-      if (slot < 0) continue;
-      const int page = pl.page_of((int)slot);
-      const long long at = tally_at(ws, pl.n_pages, a.layer, page, g, (int)slot - page * pl.P);
-      const bool fresh = a.appended && t == L - 1;
-      const float was = fresh ? 0.f : a.t.weight[at];
-      const float *s = a.t.score + (((long long)b * ws.n_kv_heads + g) * a.t.score_tokens + t) * G;
-      const float *lse = ws.lse + (long long)b * Hq + g * G;
-      float x[G];
-      if constexpr (G >= 4) {
+      float x[UN][G];
 #pragma unroll
-        for (int h = 0; h < G; h += 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + h));
-          x[h] = v.x;
-          x[h + 1] = v.y;
-          x[h + 2] = v.z;
-          x[h + 3] = v.w;
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < G; ++h) x[h] = __ldcg(s + h);
+      for (int u = 0; u < UN; ++u) {
+        const int t = ((t0 + u * step) << a.tl_log) + ts;
+        if (at[u] >= 0)
+          load_group<G, true>(
+              x[u], a.t.score + (((long long)b * ws.n_kv_heads + g) * a.t.score_tokens + t) * G);
       }
-      float w = 0.f;
+      if (t0 == first) {
+        if (g < ws.n_kv_heads) load_group<G, true>(l2, ws.lse + (long long)b * Hq + g * G);
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        const float l = lse[h];  // -inf: the head's attention was written as empty
-        w += l > -INFINITY ? tally_clean(exp2f(fmaf(-l, kLog2e, x[h]))) : 0.f;
+        for (int h = 0; h < G; ++h) l2[h] = l2[h] > -INFINITY ? l2[h] * kLog2e : INFINITY;
       }
-      a.t.weight[at] = was + w;
-      if (fresh) a.t.origin[at] = L - 1 + a.t.evicted[row];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int t = ((t0 + u * step) << a.tl_log) + ts;
+        if (at[u] < 0) continue;
+        float w = 0.f;
+#pragma unroll
+        for (int h = 0; h < G; ++h) w += tally_clean(exp2f(x[u][h] - l2[h]));
+        a.t.weight[at[u]] = was[u] + w;
+        if (a.appended && t == L - 1) a.t.origin[at[u]] = L - 1 + a.t.evicted[row];
+      }
     }
     if (blockIdx.x == 0 && threadIdx.x == 0 && L > 0 && !row_ok)
       atomicOr(ws.err, PKV_DEVERR_PAGE);
@@ -101,7 +136,7 @@ __global__ void __launch_bounds__(kTThreads)
 template <int G>
 cudaError_t launch_add(const DecodeArgs &a, const pkv_tally &t, cudaStream_t st) {
   const pkv_workspace &ws = a.ws;
-  TallyArgs g{ws, t, a.batch, a.layer, a.k_new != nullptr, (a.flags & PKV_FLAG_PLAN_EARLY) != 0, 0, 0};
+  TallyArgs g{ws, t, a.batch, a.layer, a.k_new != nullptr, 0, 0};
   // Pages of 32 tokens and more: a warp reads 32 of one head's.  Smaller ones: the same
   // page's next heads, whose entries follow, down to 4 tokens of 8 heads for flat
   // indices, where a slot's heads share a 32-byte sector.
@@ -112,9 +147,15 @@ cudaError_t launch_add(const DecodeArgs &a, const pkv_tally &t, cudaStream_t st)
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
-  // about one wave of resident warps, shared by the requests
+  // about one wave of resident warps, shared by the requests, and no more than the longest
+  // request that the table allows has items for
   const int by = a.batch < 65535 ? a.batch : 65535;
-  const int bx = (8 * sms + by - 1) / by;
+  const int hgroups = (ws.n_kv_heads + (1 << g.hl_log) - 1) >> g.hl_log;
+  constexpr int per = kTThreads / 32;
+  const long long items = ((len_cap(ws) + (1 << g.tl_log) - 1) >> g.tl_log) * hgroups;
+  const long long need = (items + kAddItems * per - 1) / (kAddItems * per);
+  const int wave = (8 * sms + by - 1) / by, least = (hgroups + per - 1) / per;
+  const int bx = std::max(least, (int)std::min<long long>(wave, need));
   return launch_pdl(tally_add_kernel<G>, dim3(bx, by), dim3(kTThreads), 0, st, g);
 }
 
