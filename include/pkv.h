@@ -576,7 +576,9 @@ pkv_status pkv_kv8_decode_layer(const pkv_workspace *ws, const pkv_kv8 *c, int b
  * each cached token has, for each layer and KV head, the sum of the weights that
  * queries gave it and the place it took in its request.  A request past a limit is
  * cut to a budget of tokens, chosen for each layer and head by that sum; the kept
- * rows move together, so page table, lengths and attention stay as they are.
+ * rows move together, so page table, lengths and attention stay as they are.  Every
+ * token that an eviction may meet was appended through a call that tallies it (the other
+ * calls leave what its slot's entry held before).
  * ------------------------------------------------------------------------ */
 
 /* A tally beside a workspace.  Page p of a layer holds [Hkv][page_size] entries. */
@@ -607,9 +609,10 @@ size_t pkv_tally_bytes(const pkv_workspace *ws, const pkv_tally *t, const char *
  * (PKV_FLAG_WRITE_LSE may be given).  Two launches; PKV_FLAG_PLAN_EARLY's guarantee is
  * the same.  A weight that is NaN adds nothing, and the tokens of a split that is
  * written as empty (a bad page, a wait that ran out, scores that are not finite) gain
- * nothing from it.  Entries of a batch must not share the pages they append to or tally.
+ * nothing from it.  Requests of a batch must not share pages: additions to one entry
+ * would be lost.
  * Host errors: as pkv_decode_layer; PKV_ERR_INVALID for PKV_FLAG_FORCE_SIMT, a null
- * buffer of the tally or a null ws->lse; PKV_ERR_CAPACITY when score_tokens is less than
+ * buffer of the tally, a null ws->lse or one not 16-byte aligned; PKV_ERR_CAPACITY when score_tokens is less than
  * a request may hold; PKV_ERR_UNSUPPORTED for shapes without the tensor-core kernel.
  * Device errors: as pkv_decode_layer; PKV_DEVERR_PAGE also for a request row (flat
  * mode, where the attention reads none) outside the page table: not tallied.
@@ -626,10 +629,10 @@ pkv_status pkv_tally_decode_layer(const pkv_workspace *ws, const pkv_tally *t, i
  *   w = sum over observed i with position p_i >= t, and the group's heads h, of
  *       exp(scale * q_ih . k_t - lse_ih).
  * A cached token (t < seq_lens[b] - n_b) gains w; a new one starts with it, weight = w,
- * origin = t + evicted[row].  Every weight enters with the scores of exact bf16 products
- * summed in fp32 and ex2's 2^-22; the sum over queries is fp32, in an order that does
- * not depend on the launch.  A weight that is NaN, or of a query whose lse is -inf, NaN
- * or +inf, adds nothing.
+ * origin = t + evicted[row].  Scores are exact bf16 products summed in fp32 with lse (in
+ * 24 bits of it), the exponential is 2^-22 exact, the sum over queries fp32, in an order
+ * that depends on the request's lengths alone.  A weight that is NaN, or of a query whose lse is
+ * -inf, NaN or +inf, adds nothing.  Requests of a batch must not share pages.
  *   n_rows      rows that q and lse hold (qo_indptr[batch] or more).
  *   window      >= 1; max_qo_len or more observes every new token.
  *   q           bf16 [n_rows, Hq, D], 16-byte aligned.

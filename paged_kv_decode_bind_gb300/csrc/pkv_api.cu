@@ -541,7 +541,8 @@ pkv_status pkv_tally_decode_layer(const pkv_workspace *ws, const pkv_tally *t, i
                                   pkv_stream_t stream) {
   const pkv_status st = check_tally(ws, t);
   if (st != PKV_OK) return st;
-  if ((flags & PKV_FLAG_FORCE_SIMT) || !t->score || !aligned16(t->score) || !ws->lse)
+  if ((flags & PKV_FLAG_FORCE_SIMT) || !t->score || !aligned16(t->score) || !ws->lse ||
+      !aligned16(ws->lse))
     return PKV_ERR_INVALID;
   if (t->score_tokens < len_cap(*ws)) return PKV_ERR_CAPACITY;
   return decode_common(ws, batch, layer, q, k_new, v_new, scale, num_splits,

@@ -672,17 +672,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
 // q [n_rows, Hq, D] as (64 columns, 64-column half, head, row): a box of one half, the
 // group's G heads and 256 / G rows lands as 256 swizzled rows, row = token * G + head.
 bool encode_q_map(CUtensorMap *m, const void *q, const pkv_workspace &ws, int n_rows, int G) {
-  static XTmapEncodeFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+  static const XTmapEncodeFn fn = [] {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &r) == cudaSuccess &&
-        r == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<XTmapEncodeFn>(p);
-  }
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
+    return e == cudaSuccess && r == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<XTmapEncodeFn>(p)
+               : nullptr;
+  }();
   if (!fn) return false;
   const cuuint64_t D = (cuuint64_t)ws.head_dim, H = (cuuint64_t)ws.n_q_heads;
   const cuuint64_t dims[4] = {64, D / 64, H, (cuuint64_t)n_rows};

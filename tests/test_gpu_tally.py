@@ -229,6 +229,14 @@ def test_extend(cuda, heads, d, page):
     assert int(ws.err.item()) == 0
 
 
+def test_extend_one_row(cuda):
+    """One new token: fewer rows than a query tile, on a context of one, of a tile's edge."""
+    for L in (1, 128, 129, 257):
+        p = P.problem([L], heads=(2, 2), d=64)
+        ws, tally, ref, _ = _extend(p, [L], [1])
+        _check_tally(tally, ref)
+
+
 @pytest.mark.parametrize("window", [1, 7, 64, 130])
 @pytest.mark.parametrize("heads", [(2, 2), (8, 2), (16, 1)])
 def test_extend_window(cuda, window, heads):
@@ -632,6 +640,93 @@ def test_graph_replays_as_eager(cuda):
                                         ws.v_pool.view(torch.int16))])
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_prompt_captured_and_replayed_with_other_inputs(cuda):
+    """TallyExtender and the eviction in one graph, replayed on other rows, lengths and
+    new-token counts, as the same calls run eagerly."""
+    p = P.problem([300, 200], heads=(8, 2), d=64, layers=2, steps=0)
+    lens, new = [[300, 200], [257, 130], [300, 1]], [[100, 64], [33, 100], [1, 1]]
+    got = []
+    for graph in (False, True):
+        ws, tally = P.device(p)
+        ext = TallyExtender(ws, tally, 2, max_new=100, scale=p.scale, window=50)
+        q = torch.zeros((200, 8, 64), dtype=torch.bfloat16, device="cuda")
+        k, v = (torch.zeros((200, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        out, qo = torch.zeros_like(q), torch.zeros(3, dtype=torch.int32, device="cuda")
+
+        def calls():
+            for layer in range(2):
+                ext.layer(layer, qo, 100, q, k, v, out)
+            A.pkv_tally_evict(ws, tally, 2, 300, 150, 120, 4, 16)
+
+        st = torch.cuda.Stream()
+        g = None
+        for i in range(3):
+            q.copy_(_bf16(tuple(q.shape), 80 + i))
+            k.copy_(_bf16(tuple(k.shape), 90 + i))
+            v.copy_(_bf16(tuple(v.shape), 95 + i))
+            ws.seq_lens.copy_(torch.tensor(lens[i], dtype=torch.int32))
+            qo.copy_(torch.tensor([0, new[i][0], sum(new[i])], dtype=torch.int32))
+            torch.cuda.synchronize()
+            if not graph:
+                calls()
+            else:
+                if g is None:
+                    g = torch.cuda.CUDAGraph()
+                    with torch.cuda.stream(st), torch.cuda.graph(g, stream=st):
+                        calls()
+                g.replay()
+            torch.cuda.synchronize()
+            assert int(ws.err.item()) == 0
+            got.append([x.clone() for x in (tally.weight, tally.origin, tally.evicted, ws.seq_lens,
+                                            ws.k_pool.view(torch.int16), out.view(torch.int16))])
+    for a, b in zip(got[:3], got[3:]):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(cuda, seed):
+    """Seeded combinations of everything: a prompt's tally, a decode layer's, an eviction."""
+    r = np.random.default_rng(1000 + seed)
+    H = int(r.choice([1, 2, 3, 5, 8]))
+    heads, d = (H * int(r.choice([1, 2, 4, 8])), H), int(r.choice([64, 128]))
+    page, B = int(r.choice([1, 3, 7, 16, 24, 32, 80])), int(r.integers(1, 9))
+    lens = [int(x) for x in r.integers(0, 400, B)]
+    new = [int(r.integers(0, n + 1)) for n in lens]
+    if not sum(new):
+        lens[0], new[0] = 9, 4
+    p = P.problem(lens, page=page, heads=heads, d=d, layers=2)
+    layer = int(r.integers(0, 2))
+    ws, tally, ref, _ = _extend(p, lens, new, window=int(r.integers(1, 300)), layer=layer)
+    _check_tally(tally, ref, "prompt")
+    S = int(r.integers(1, 4))
+    ws, tally = P.device(p, max_splits=S)
+    q = _bf16((B, heads[0], d), seed).cuda()
+    k, v = (_bf16((B, H, d), seed + s).cuda() for s in (100, 200))
+    add = bool(r.integers(0, 2))
+    if add:  # the oracle's view of the pool
+        old = ws.k_pool.clone()
+        for b, n in enumerate(lens):
+            if n:
+                ws.k_pool[layer, P.slots(p, b, n)[-1]] = k[b]
+    ref = _decode_reference(p, ws, tally, layer, q, lens, add)
+    if add:
+        ws.k_pool.copy_(old)
+    A.pkv_tally_decode_layer(ws, tally, B, layer, q, k if add else None, v if add else None,
+                             p.scale, S)
+    torch.cuda.synchronize()
+    _check_tally(tally, ref, "decode")
+    _set_tally(p, ws, tally, ["random", "ties", "odd"][seed % 3], seed)
+    budget = int(r.integers(1, 300))
+    sinks = int(r.integers(0, min(5, budget) + 1))
+    recent = int(r.integers(0, budget - sinks + 1))
+    limit = budget + int(r.integers(0, 50))
+    ref = _evict_reference(p, ws, tally, lens, budget, limit, sinks, recent)
+    A.pkv_tally_evict(ws, tally, B, int(r.integers(400, 9000)), limit, budget, sinks, recent)
+    _check_evict(p, ws, tally, ref)
+    assert int(ws.err.item()) == 0
 
 
 def test_another_stream(cuda):

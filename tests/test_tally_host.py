@@ -96,6 +96,7 @@ BAD_TALLY = [dict(weight=None), dict(origin=None), dict(evicted=None), dict(rese
     ({}, dict(score_tokens=63), 1, 0, 1, 0, A.PKV_ERR_CAPACITY),
     (dict(max_seq_len=63), dict(score_tokens=63), 0, 0, 1, 0, A.PKV_OK),
     (dict(lse=None), {}, 1, 0, 1, 0, A.PKV_ERR_INVALID),
+    (dict(lse=4100), {}, 1, 0, 1, 0, A.PKV_ERR_INVALID),
     ({}, {}, 1, 0, 1, A.PKV_FLAG_FORCE_SIMT, A.PKV_ERR_INVALID),
     (dict(head_dim=256), {}, 1, 0, 1, 0, A.PKV_ERR_UNSUPPORTED),
     (dict(n_q_heads=6), {}, 1, 0, 1, 0, A.PKV_ERR_UNSUPPORTED),
