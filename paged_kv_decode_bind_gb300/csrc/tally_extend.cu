@@ -17,9 +17,10 @@
 //
 // One persistent CTA per SM.  Two shapes of unit, by how many query tiles a request has
 // at most:
-//   few (one or two)  a unit is one key tile; the query tiles stay in shared memory over
-//               a CTA's consecutive key tiles of the same request and head, and only keys
-//               stream: the last chunk of a long prompt.
+//   few (one or two)  the query tiles stay in shared memory over a CTA's consecutive keys
+//               of the same request and head, and only keys stream, two tiles a unit (one
+//               where there are two query tiles, and room for two key tiles): the last
+//               chunk of a long prompt.
 //   many        a unit is two key tiles; they stay while the query tiles that see them
 //               pass, each used twice.
 // Units are dealt out in snake order of their cost (many) or in even runs (few).
@@ -97,9 +98,9 @@ struct TallyXArgs {
   pkv_workspace ws;
   pkv_tally t;
   int b0, batch, total_batch, layer, max_qo_len, n_rows, window;
-  int few;     // units of one key tile, query tiles kept (see above)
+  int few;     // 1: query tiles kept over a run of keys (see above)
+  int block;   // keys of a unit
   int nk, nq;  // stages of the key and the query ring
-  int lag;     // key tiles whose copies may be under way behind the newest
   const int *qo_indptr;
   const float *lse;
   float scale;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   const pkv_workspace &ws = a.ws;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hq = ws.n_q_heads, hkv = ws.n_kv_heads;
-  const int block = a.few ? kTM : 2 * kTM;  // keys of a unit
+  const int block = a.block;  // keys of a unit: one key tile, or two
   if (tid < kBadRing) s_bad[tid] = 0;
   // the ninth step of the keys, and finite values behind and in the query rows'
   if (tid < kTM * 2) {
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     x.L = r.y;
     x.q0 = r.z;
     x.t0 = (w - s_pref[lo]) * block;
-    x.nk = a.few || x.t0 + kTM >= x.L ? 1 : 2;
+    x.nk = block == kTM || x.t0 + kTM >= x.L ? 1 : 2;
     x.before = x.L - x.n;
     x.i0 = max(max(0, x.n - a.window), x.t0 - x.before);  // < n, as t0 < L
     x.T = (x.n - x.i0 + TQ - 1) / TQ;
@@ -286,9 +287,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
     if (a.few) {
       const long long u = u_lo + i;
       if (u >= u_hi) return false;
-      if (i > 0 && x.t0 + kTM < x.L) {  // the next key tile of the same request and head
+      if (i > 0 && x.t0 + block < x.L) {  // the next keys of the same request and head
         const int was = x.i0;
-        x.t0 += kTM;
+        x.t0 += block;
+        if (x.t0 + kTM >= x.L) x.nk = 1;
         x.i0 = max(max(0, x.n - a.window), x.t0 - x.before);
         x.same = x.i0 == was;
         if (!x.same) x.T = (x.n - x.i0 + TQ - 1) / TQ;
@@ -546,13 +548,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
         atomicOr(ws.err, bad);
         atomicOr(&s_bad[kt % kBadRing], bad);
       }
-      // Tiles whose copies may still be under way when the next one is issued.  A unit of
-      // two tiles fills a ring of two: the stage of the next tile is free only once this
-      // tile's products are done, so it is published first.
-      if (a.lag == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-      else if (a.lag == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-      else asm volatile("cp.async.wait_group 2;" ::: "memory");
-      if (kt >= a.lag) publish(1);
+      // The copies of one tile may still be under way when the next is issued (few).  A
+      // unit of two tiles that fills a ring of two (many): the stage of the next tile is
+      // free only once this tile's products are done, so it is published first.
+      if (a.few) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (kt >= a.few) publish(1);
       ++kt;
       kr.next(a.nk);
       x = y;
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       have = have2;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!dead) publish(min(kt, a.lag));
+    if (!dead) publish(min(kt, a.few));
   } else if (warp >= kSumWarp) {
     // ------------------------------------------------- weights ----
     const int grp = (warp - kSumWarp) >> 2, wq = warp & 3;
@@ -728,8 +729,9 @@ cudaError_t launch_tally_extend(const pkv_workspace &ws, const pkv_tally &t, int
   // and two
   const long long most = ((long long)std::min(window, max_qo_len) * G + kTN - 1) / kTN;
   const int few = most <= kMaxQ, nq = most <= 1 ? 1 : 2, nk = nq == 1 ? 4 : 2;
-  const TallyXArgs a{ws, t, 0, 0, batch, layer, max_qo_len, n_rows, window, few, nk, nq,
-                     few ? nk / 2 : 0, qo_indptr, lse, scale};
+  const int block = few && nq == 2 ? kTM : 2 * kTM;
+  const TallyXArgs a{ws,  t,     0,  0,  batch,     layer, max_qo_len, n_rows, window,
+                     few, block, nk, nq, qo_indptr, lse,   scale};
 #define PKV_TX_CASE(DD, GG) \
   if (D == DD && G == GG) return launch_one<DD, GG>(a, q, batch, st);
   PKV_TX_CASE(128, 1) PKV_TX_CASE(128, 2) PKV_TX_CASE(128, 4) PKV_TX_CASE(128, 8)
