@@ -70,12 +70,15 @@ def check_tally(ws, tally, batch=0):
 @dataclasses.dataclass(frozen=True)
 class Eviction:
     """Requests of more than `limit` tokens (None: budget) keep `budget`: the first `sinks`
-    and the last `recent` of all their tokens, then those of the largest tally."""
+    and the last `recent` of all their tokens, then those of the largest tally.  max_len:
+    a bound on the lengths that a step meets (None: what a table row holds, at most
+    PKV_TALLY_MAX_LEN); longer requests are left as they are, with PKV_DEVERR_LEN."""
 
     budget: int
     limit: int | None = None
     sinks: int = 0
     recent: int = 0
+    max_len: int | None = None
 
     def __post_init__(self):
         if self.limit is None:
@@ -83,6 +86,8 @@ class Eviction:
         if self.budget < 1 or self.limit < self.budget or self.sinks < 0 or self.recent < 0 or \
                 self.sinks + self.recent > self.budget:
             raise ValueError("1 <= budget <= limit, and budget holds sinks and recent")
+        if self.max_len is not None and not self.limit < self.max_len <= _abi.PKV_TALLY_MAX_LEN:
+            raise ValueError("max_len is past the limit, at most PKV_TALLY_MAX_LEN")
 
     def length(self, n: int) -> int:
         """A request's tokens after the eviction."""

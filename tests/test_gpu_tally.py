@@ -456,6 +456,33 @@ def test_evict(cuda, kind, page, d, heads, budget, limit, sinks, recent):
     assert int(ws.err.item()) == 0
 
 
+@pytest.mark.parametrize("kind", ["random", "ties", "equal", "odd"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (1, 1, 0), (100, 4, 32), (100, 100, 0),
+                                                 (100, 0, 100), (3000, 4, 100)])
+def test_evict_one_token(cuda, kind, d, budget, sinks, recent):
+    """A request one token over: the token that ranks last goes, whatever the others do."""
+    lens = [budget + 1, budget, budget + 2, budget + 1, 0]
+    p = P.problem(lens, page=16 if d == 64 else 5, heads=(6, 3), d=d, layers=2)
+    ws, tally = P.device(p)
+    _set_tally(p, ws, tally, kind)
+    ref = _evict_reference(p, ws, tally, lens, budget, budget, sinks, recent)
+    A.pkv_tally_evict(ws, tally, p.batch, budget + 2, budget, budget, sinks, recent)
+    _check_evict(p, ws, tally, ref)
+    assert int(ws.err.item()) == 0
+
+
+def test_evict_one_token_bad_page(cuda):
+    p = P.problem([51, 51], heads=(4, 2), d=64, layers=2)
+    ws, tally = P.device(p)
+    _set_tally(p, ws, tally, "random")
+    ws.page_table[int(p.req_pool_indices[1]), 2] = -4
+    ref = _evict_reference(p, ws, tally, [51, 51], 50, 50, 2, 10, (1,))
+    A.pkv_tally_evict(ws, tally, 2, 51, 50, 50, 2, 10)
+    _check_evict(p, ws, tally, ref)
+    assert int(ws.err.item()) == A.PKV_DEVERR_PAGE
+
+
 @pytest.mark.parametrize("kind", ["random", "ties"])
 @pytest.mark.parametrize("lens,max_len,budget", [
     ([5000, 2049], 5000, 1025),      # clusters for idle SMs
@@ -620,12 +647,12 @@ def test_graph_replays_as_eager(cuda):
     """Two layers with the early start, captured and replayed, as the same steps run
     eagerly: bit for bit, attention, tally and evictions."""
     got = []
-    for graph in (False, True):
+    for graph, plan in ((False, False), (True, False), (True, True)):
         p = P.problem([500, 70, 130], heads=(8, 2), layers=3, steps=8)
         ws, tally = P.device(p, max_splits=4)
-        run = DecodeRunner(ws, 3, num_splits=4, scale=p.scale, tally=tally,
+        run = DecodeRunner(ws, 3, num_splits=4, scale=p.scale, tally=tally, plan=plan,
                            norm_rope=_axes_rope(ws, tally, 8, 2, 128, 1000),
-                           evict=Eviction(budget=72, limit=75, sinks=2, recent=8),
+                           evict=Eviction(budget=72, limit=75, sinks=2, recent=8, max_len=501),
                            out_per_layer=True)
         for i, x in enumerate((run.q_in, run.k_in, run.v_in)):
             x.copy_(_bf16(tuple(x.shape), 70 + i))
@@ -638,8 +665,9 @@ def test_graph_replays_as_eager(cuda):
         got.append([x.clone() for x in (run.outs.view(torch.int16), tally.weight, tally.origin,
                                         tally.evicted, ws.seq_lens, ws.k_pool.view(torch.int16),
                                         ws.v_pool.view(torch.int16))])
-    for a, b in zip(*got):
-        assert torch.equal(a, b)
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a, b)
 
 
 def test_prompt_captured_and_replayed_with_other_inputs(cuda):

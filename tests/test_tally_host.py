@@ -248,7 +248,8 @@ def test_eviction():
     e = pkv.Eviction(budget=10, limit=20)
     assert (e.length(20), e.length(21)) == (20, 10)
     for kw in (dict(budget=0), dict(budget=5, limit=4), dict(budget=5, sinks=3, recent=3),
-               dict(budget=5, sinks=-1), dict(budget=5, recent=-1)):
+               dict(budget=5, sinks=-1), dict(budget=5, recent=-1), dict(budget=5, max_len=5),
+               dict(budget=5, max_len=A.PKV_TALLY_MAX_LEN + 1)):
         with pytest.raises(ValueError):
             pkv.Eviction(**kw)
 
@@ -286,7 +287,8 @@ def test_runner_refusals():
     table = torch.zeros(8, 64)
     heads = dict(n_q_heads=8, n_kv_heads=2, head_dim=64, cos_sin=table)
     axes = dict(rows=ws.req_pool_indices, evicted=t.evicted, **heads)
-    pkv.DecodeRunner(ws, 2, tally=t, evict=e)
+    assert pkv.DecodeRunner(ws, 2, tally=t, evict=e).evict_len == 64
+    assert pkv.DecodeRunner(ws, 2, tally=t, evict=pkv.Eviction(8, max_len=9)).evict_len == 9
     pkv.DecodeRunner(ws, 2, tally=t, evict=e, norm_rope=pkv.QkNormRopeAxes(**axes))
     other = dict(axes, rows=ws.req_pool_indices.clone())
     loose = dict(axes, evicted=t.evicted.clone())
