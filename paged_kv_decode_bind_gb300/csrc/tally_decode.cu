@@ -7,6 +7,11 @@
 // split is merged, so it cannot be added where the score is made.  The scores are 4 G
 // bytes a token and head beside the 4 D of its K and V (3 % at G = 4, D = 128), stay in
 // L2, and spare a second reading of K.
+//
+// Measured (GB300, us a layer in graphs of 24): 64 requests of 1024-4096 tokens, 16/2 heads
+// 44.2 (34.1 without the tally), 16 of 2048, 32/8 heads, 33.2 (27.4), 4 of 512-2048 11.7
+// (8.8), 16 flat of 200-4000 42.5 (33.5).  Of 4 x 65536 tokens (190 us, 161 without) the
+// scores' stores take 13 us and the second launch 16.
 #include <algorithm>
 
 #include "decode_mma.cuh"
@@ -17,7 +22,14 @@ namespace pkv {
 namespace {
 
 constexpr int kTThreads = 256;
-constexpr int kAddItems = 2;  // items of a warp whose loads are in flight (4: spilled registers)
+template <int G>
+constexpr int kAddBlocks = G <= 8 ? 6 : 4;  // of an SM (16 heads' scores and lse: 64 registers)
+// Items of a warp whose loads are in flight, as many as the registers of six blocks hold
+// (24 layers' steps, us a layer: 16 requests of 2048 tokens, G = 4, 32.9 with two items and
+// six blocks, 34.4 with four blocks, 34.9 with one item; 64 of 1024-4096, G = 8, 45.1 with
+// one item, 50.1 with two, which spill).
+template <int G>
+constexpr int kAddItems = G <= 4 ? 2 : 1;
 
 struct TallyArgs {
   pkv_workspace ws;
@@ -27,14 +39,13 @@ struct TallyArgs {
   int tl_log, hl_log;  // a warp takes 2^tl tokens of 2^hl KV heads
 };
 
-// G consecutive values.
-template <int G, bool CG>
+// G consecutive values that the launch before has written.
+template <int G>
 __device__ __forceinline__ void load_group(float (&x)[G], const float *s) {
   if constexpr (G >= 4) {
 #pragma unroll
     for (int h = 0; h < G; h += 4) {
-      const float4 *p = reinterpret_cast<const float4 *>(s + h);
-      const float4 v = CG ? __ldcg(p) : *p;
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + h));
       x[h] = v.x;
       x[h + 1] = v.y;
       x[h + 2] = v.z;
@@ -42,7 +53,7 @@ __device__ __forceinline__ void load_group(float (&x)[G], const float *s) {
     }
   } else {
 #pragma unroll
-    for (int h = 0; h < G; ++h) x[h] = CG ? __ldcg(s + h) : s[h];
+    for (int h = 0; h < G; ++h) x[h] = __ldcg(s + h);
   }
 }
 
@@ -54,9 +65,9 @@ __device__ __forceinline__ void load_group(float (&x)[G], const float *s) {
 // log-sum-exps: lengths, tables and the tally are older than the attention's own start,
 // as this launch starts behind the attention's wait for its predecessor.
 template <int G>
-__global__ void __launch_bounds__(kTThreads, 4)
+__global__ void __launch_bounds__(kTThreads, kAddBlocks<G>)
     tally_add_kernel(const __grid_constant__ TallyArgs a) {
-  constexpr int UN = kAddItems;
+  constexpr int UN = kAddItems<G>;
   const pkv_workspace &ws = a.ws;
   pdl_trigger();
   Plan pl;
@@ -108,11 +119,11 @@ __global__ void __launch_bounds__(kTThreads, 4)
       for (int u = 0; u < UN; ++u) {
         const int t = ((t0 + u * step) << a.tl_log) + ts;
         if (at[u] >= 0)
-          load_group<G, true>(
+          load_group<G>(
               x[u], a.t.score + (((long long)b * ws.n_kv_heads + g) * a.t.score_tokens + t) * G);
       }
       if (t0 == first) {
-        if (g < ws.n_kv_heads) load_group<G, true>(l2, ws.lse + (long long)b * Hq + g * G);
+        if (g < ws.n_kv_heads) load_group<G>(l2, ws.lse + (long long)b * Hq + g * G);
 #pragma unroll
         for (int h = 0; h < G; ++h) l2[h] = l2[h] > -INFINITY ? l2[h] * kLog2e : INFINITY;
       }
@@ -153,8 +164,9 @@ cudaError_t launch_add(const DecodeArgs &a, const pkv_tally &t, cudaStream_t st)
   const int hgroups = (ws.n_kv_heads + (1 << g.hl_log) - 1) >> g.hl_log;
   constexpr int per = kTThreads / 32;
   const long long items = ((len_cap(ws) + (1 << g.tl_log) - 1) >> g.tl_log) * hgroups;
-  const long long need = (items + kAddItems * per - 1) / (kAddItems * per);
-  const int wave = (8 * sms + by - 1) / by, least = (hgroups + per - 1) / per;
+  constexpr int each = kAddItems<G> * per;
+  const long long need = (items + each - 1) / each;
+  const int wave = (kAddBlocks<G> * sms + by - 1) / by, least = (hgroups + per - 1) / per;
   const int bx = std::max(least, (int)std::min<long long>(wave, need));
   return launch_pdl(tally_add_kernel<G>, dim3(bx, by), dim3(kTThreads), 0, st, g);
 }

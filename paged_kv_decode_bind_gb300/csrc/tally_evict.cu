@@ -19,6 +19,10 @@
 // segment of the request's tokens; histograms, counts and the lists of movers and free
 // indices are read from the other CTAs' shared memory.  The unit that finishes last of a
 // request (a ticket on split_counters) writes its new length.
+//
+// Measured (GB300): 64 requests of 1024-4096 tokens to 1024, 4 layers of 2 heads, 82 us, 4 x
+// 65536 to 8192, 8 heads, 74 us; the choice alone 18 and 30, the rows then move at 4.9 and
+// 5.4 TB/s (256-byte rows, read and written).  CTAs of 512 threads, two an SM: 111 and 91 us.
 #include <algorithm>
 
 #include "decode_plan.cuh"

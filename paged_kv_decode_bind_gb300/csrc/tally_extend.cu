@@ -13,7 +13,8 @@
 // The log-sum-exps enter through the tensor cores too, as a ninth step of 16 dims: a key
 // has 1, 1, 1, 0 ... there, a query row -lse / scale in three bf16 parts (2^-24 of it).
 // Read from shared memory a column at a time they came to every lane of every warp, as
-// many bytes as the products' operands (prompt_whole: 266 us, 227 without the reads).
+// many bytes as the products' operands (a whole 8192-token prompt 266 us, 227 without the
+// reads).
 //
 // One persistent CTA per SM.  Two shapes of unit, by how many query tiles a request has
 // at most:
@@ -32,6 +33,15 @@
 // columns each of every other product.  Every mbarrier wait is bounded (~1 s): one that
 // runs out raises PKV_DEVERR_TIMEOUT and stops the CTA, which writes no further entry and
 // waits (again bounded) for its copies and products before the TMEM is freed.
+//
+// Measured (GB300, 32/8 heads, D = 128): a whole 8192-token prompt 220 us, 1250 TFLOP/s (65 %
+// of the measured bf16 burst; the tensor pipe 67 % busy, the exponentials' 59 %): a product
+// takes ~1500 cycles of the issuing warp, and the costliest CTA has 18 % above the mean; the
+// last 64 queries on 32768 tokens 27.4 us (2.5 TB/s of keys): the hand-offs of a unit; four
+// 256-token chunks on 661-2014 26 us: launch, first tiles, and 16 products in a row.
+// Not kept: two issuing warps, a buffer each (whole prompt 277 us: their MMAs alternate and
+// both finish late), key tiles by tensor-map boxes (27 us where cp.async took 26), two
+// groups of loader warps (no difference).
 #include <algorithm>
 #include <cstring>
 
