@@ -638,12 +638,13 @@ pkv_status pkv_tally_decode_layer(const pkv_workspace *ws, const pkv_tally *t, i
  *   window      >= 1; max_qo_len or more observes every new token.
  *   q           bf16 [n_rows, Hq, D], 16-byte aligned.
  *   lse         fp32 [n_rows, Hq], natural log, as ws->lse of the attention.
+ *   scale       the attention's; finite (|scale| below 1e-30 counts as 1e-30).
  * Device errors: PKV_DEVERR_LEN (a length or new-token count out of range, or rows
  * outside [0, n_rows)) and PKV_DEVERR_TOTAL, _PAGE for the request's row: the request is
  * skipped; PKV_DEVERR_PAGE, _SLOT: the entries of the 128-token tile that meets a bad
  * index keep what they held; PKV_DEVERR_TIMEOUT (a wait that ran out: the same).
- * Host errors: as pkv_extend_attn; PKV_ERR_INVALID (n_rows < 0, window < 1, a null
- * buffer); PKV_ERR_UNSUPPORTED (head_dim not 64 / 128, or G not 1, 2, 4, 8, 16).
+ * Host errors: as pkv_extend_attn; PKV_ERR_INVALID (n_rows < 0, window < 1, a scale that
+ * is not finite, a null buffer); PKV_ERR_UNSUPPORTED (head_dim not 64 / 128, or G not 1, 2, 4, 8, 16).
  */
 pkv_status pkv_tally_extend(const pkv_workspace *ws, const pkv_tally *t, int batch, int layer,
                             const int32_t *qo_indptr, int max_qo_len, int n_rows, int window,

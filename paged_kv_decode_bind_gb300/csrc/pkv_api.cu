@@ -1,6 +1,7 @@
 // C-ABI entry points of libpkv (declared in include/pkv.h): host-side
 // validation, then kernel launches on the caller's stream.  Nothing here
 // allocates, synchronises or reads device memory.
+#include <cmath>
 #include <cstring>
 
 #include "kernels.cuh"
@@ -554,7 +555,8 @@ pkv_status pkv_tally_extend(const pkv_workspace *ws, const pkv_tally *t, int bat
                             const void *q, const float *lse, float scale, pkv_stream_t stream) {
   pkv_status st = check_tally(ws, t);
   if (st != PKV_OK) return st;
-  if (batch < 0 || layer < 0 || max_qo_len < 0 || n_rows < 0 || window < 1)
+  if (batch < 0 || layer < 0 || max_qo_len < 0 || n_rows < 0 || window < 1 ||
+      !std::isfinite(scale))
     return PKV_ERR_INVALID;
   if (batch > ws->max_batch || layer >= ws->n_layers) return PKV_ERR_CAPACITY;
   if (!extend_supported(ws->head_dim, ws->n_q_heads / ws->n_kv_heads))

@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
     __syncthreads();
   }
-  // the CTA's i-th unit, x being the one before; false past the last.  few: an even run of (request, head, tile);
-  // else snake order over (block by cost, head)
+  // The CTA's i-th unit, x being the one before; false past the last.  few: an even run of
+  // (request, head, block); else snake order over (block by cost, head).
   const long long u_lo = units * blockIdx.x / gridDim.x, u_hi = units * (blockIdx.x + 1) / gridDim.x;
   auto unit_at = [&](int i, TUnit &x) -> bool {
     if (a.few) {

@@ -122,6 +122,8 @@ def test_decode_refuses_half_an_append():
     *[({}, kw, {}, A.PKV_ERR_INVALID) for kw in BAD_TALLY],
     ({}, {}, dict(qo=None), A.PKV_ERR_INVALID),
     ({}, {}, dict(window=0), A.PKV_ERR_INVALID),
+    ({}, {}, dict(scale=math.nan), A.PKV_ERR_INVALID),
+    ({}, {}, dict(scale=-math.inf), A.PKV_ERR_INVALID),
     ({}, {}, dict(n_rows=-1), A.PKV_ERR_INVALID),
     ({}, {}, dict(max_qo=-1), A.PKV_ERR_INVALID),
     ({}, {}, dict(batch=-1), A.PKV_ERR_INVALID),
@@ -138,10 +140,10 @@ def test_decode_refuses_half_an_append():
     ({}, {}, dict(max_qo=0), A.PKV_OK),
 ])
 def test_extend_refusals(ws, t, kw, status):
-    d = dict(batch=1, layer=0, qo=4096, max_qo=4, n_rows=4, window=4, q=4096, lse=4096)
+    d = dict(batch=1, layer=0, qo=4096, max_qo=4, n_rows=4, window=4, q=4096, lse=4096, scale=1.0)
     d.update(kw)
     assert A.pkv_tally_extend(_ws(**ws), _t(**t), d["batch"], d["layer"], d["qo"], d["max_qo"],
-                              d["n_rows"], d["window"], d["q"], d["lse"], 1.0, stream=0,
+                              d["n_rows"], d["window"], d["q"], d["lse"], d["scale"], stream=0,
                               check=False) == status
 
 
