@@ -20,9 +20,11 @@
 // indices are read from the other CTAs' shared memory.  The unit that finishes last of a
 // request (a ticket on split_counters) writes its new length.
 //
-// Measured (GB300): 64 requests of 1024-4096 tokens to 1024, 4 layers of 2 heads, 82 us, 4 x
-// 65536 to 8192, 8 heads, 74 us; the choice alone 18 and 30, the rows then move at 4.9 and
-// 5.4 TB/s (256-byte rows, read and written).  CTAs of 512 threads, two an SM: 111 and 91 us.
+// Measured (GB300): 64 requests of 1024-4096 tokens to 1024, 4 layers of 2 heads, 81 us, 4 x
+// 65536 to 8192, 8 heads, 74 us; the choice alone 18 and 29 (launch 2, keys 7 and 9, four
+// passes 6 and 14, lists 4), the rows then move at 5.1 and 5.4 TB/s.  That is what 256-byte
+// rows at scattered places give: half as many rows in flight, or lookups a batch ahead, change
+// nothing.  CTAs of 512 threads, two an SM: 111 and 91 us.
 #include <algorithm>
 
 #include "decode_plan.cuh"
@@ -417,6 +419,9 @@ __global__ void __launch_bounds__(kEThreads, kEPerSM)
   for (int j0 = (rank * kEWarps + warp) * kEBatch; j0 < M; j0 += C * kEWarps * kEBatch) {
     const int j = j0 + lane, m = min(kEBatch, M - j0);
     int src = 0, dst = 0;  // slots of this lane's mover
+    long long ad = 0;      // its tally entry's new place; stored behind the rows
+    float w = 0.f;
+    int o = 0;
     if (lane < m) {
       int cf = 0, cm = 0;
       for (int c = 1; c < C; ++c) {
@@ -430,11 +435,9 @@ __global__ void __launch_bounds__(kEThreads, kEPerSM)
       src = ps * pl.P + pl.in_page(from);
       dst = pd * pl.P + pl.in_page(to);
       const long long as = tally_at(ws, pl.n_pages, layer, ps, g, pl.in_page(from));
-      const long long ad = tally_at(ws, pl.n_pages, layer, pd, g, pl.in_page(to));
-      const float w = a.t.weight[as];
-      const int o = a.t.origin[as];
-      a.t.weight[ad] = w;
-      a.t.origin[ad] = o;
+      ad = tally_at(ws, pl.n_pages, layer, pd, g, pl.in_page(to));
+      w = a.t.weight[as];
+      o = a.t.origin[as];
     }
 #pragma unroll
     for (int k0 = 0; k0 < kEBatch; k0 += UN * RPW) {
@@ -458,6 +461,10 @@ __global__ void __launch_bounds__(kEThreads, kEPerSM)
           vp[to[u]] = vx[u];
         }
       }
+    }
+    if (lane < m) {
+      a.t.weight[ad] = w;
+      a.t.origin[ad] = o;
     }
   }
   unit_sync();  // the lists stay until every CTA has read them
