@@ -612,8 +612,9 @@ size_t pkv_tally_bytes(const pkv_workspace *ws, const pkv_tally *t, const char *
  * nothing from it.  Requests of a batch must not share pages: additions to one entry
  * would be lost.
  * Host errors: as pkv_decode_layer; PKV_ERR_INVALID for PKV_FLAG_FORCE_SIMT, a null
- * buffer of the tally, a null ws->lse or one not 16-byte aligned; PKV_ERR_CAPACITY when score_tokens is less than
- * a request may hold; PKV_ERR_UNSUPPORTED for shapes without the tensor-core kernel.
+ * buffer of the tally, a null ws->lse or one not 16-byte aligned; PKV_ERR_CAPACITY when
+ * score_tokens is less than a request may hold; PKV_ERR_UNSUPPORTED for shapes without
+ * the tensor-core kernel.
  * Device errors: as pkv_decode_layer; PKV_DEVERR_PAGE also for a request row (flat
  * mode, where the attention reads none) outside the page table: not tallied.
  */
@@ -644,7 +645,8 @@ pkv_status pkv_tally_decode_layer(const pkv_workspace *ws, const pkv_tally *t, i
  * skipped; PKV_DEVERR_PAGE, _SLOT: the entries of the 128-token tile that meets a bad
  * index keep what they held; PKV_DEVERR_TIMEOUT (a wait that ran out: the same).
  * Host errors: as pkv_extend_attn; PKV_ERR_INVALID (n_rows < 0, window < 1, a scale that
- * is not finite, a null buffer); PKV_ERR_UNSUPPORTED (head_dim not 64 / 128, or G not 1, 2, 4, 8, 16).
+ * is not finite, a null buffer); PKV_ERR_UNSUPPORTED (head_dim not 64 / 128, or G not 1,
+ * 2, 4, 8, 16).
  */
 pkv_status pkv_tally_extend(const pkv_workspace *ws, const pkv_tally *t, int batch, int layer,
                             const int32_t *qo_indptr, int max_qo_len, int n_rows, int window,

@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
   if (tid < kBadRing) s_bad[tid] = 0;
   // the ninth step of the keys, and finite values behind and in the query rows'
   if (tid < kTM * 2) {
-    const uint32_t at = sbase + C::OFF_ONE + (tid >> 4) * 256 + ((tid >> 3) & 1) * 128 + (tid & 7) * 16;
+    const uint32_t at =
+        sbase + C::OFF_ONE + (tid >> 4) * 256 + ((tid >> 3) & 1) * 128 + (tid & 7) * 16;
     const bool first = ((tid >> 3) & 1) == 0;
     st_shared_v4(at, first ? 0x3f803f80u : 0u, first ? 0x3f80u : 0u, 0u, 0u);
   }
@@ -292,7 +293,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
   }
   // The CTA's i-th unit, x being the one before; false past the last.  few: an even run of
   // (request, head, block); else snake order over (block by cost, head).
-  const long long u_lo = units * blockIdx.x / gridDim.x, u_hi = units * (blockIdx.x + 1) / gridDim.x;
+  const long long u_lo = units * blockIdx.x / gridDim.x;
+  const long long u_hi = units * (blockIdx.x + 1) / gridDim.x;
   auto unit_at = [&](int i, TUnit &x) -> bool {
     if (a.few) {
       const long long u = u_lo + i;
@@ -687,7 +689,8 @@ bool encode_q_map(CUtensorMap *m, const void *q, const pkv_workspace &ws, int n_
     void *p = nullptr;
     cudaDriverEntryPointQueryResult r;
     const cudaError_t e =
-        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &r);
     return e == cudaSuccess && r == cudaDriverEntryPointSuccess
                ? reinterpret_cast<XTmapEncodeFn>(p)
                : nullptr;
