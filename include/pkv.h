@@ -607,7 +607,7 @@ size_t pkv_tally_bytes(const pkv_workspace *ws, const pkv_tally *t, const char *
  * With k_new and v_new NULL nothing is appended and every token adds.
  * Arguments, outputs and errors are pkv_decode_layer's; ws->lse is always written
  * (PKV_FLAG_WRITE_LSE may be given).  Two launches; PKV_FLAG_PLAN_EARLY's guarantee is
- * the same.  A weight that is NaN adds nothing, and the tokens of a split that is
+ * the same.  A weight that is NaN or infinite adds nothing, and the tokens of a split that is
  * written as empty (a bad page, a wait that ran out, scores that are not finite) gain
  * nothing from it.  Requests of a batch must not share pages: additions to one entry
  * would be lost.
@@ -632,9 +632,9 @@ pkv_status pkv_tally_decode_layer(const pkv_workspace *ws, const pkv_tally *t, i
  * A cached token (t < seq_lens[b] - n_b) gains w; a new one starts with it, weight = w,
  * origin = t + evicted[row].  Scores are exact bf16 products summed in fp32 with lse (in
  * 24 bits of it), the exponential is 2^-22 exact, the sum over queries fp32, in an order
- * that the request's lengths, window and max_qo_len settle.  A weight that is NaN, or of a
- * query whose lse is -inf, NaN or +inf, adds nothing.  Requests of a batch must not share
- * pages.
+ * that the request's lengths, window and max_qo_len settle.  A weight that is NaN or past
+ * fp32 (an lse far below its score), or of a query whose lse is -inf, NaN or +inf, adds
+ * nothing.  Requests of a batch must not share pages.
  *   n_rows      rows that q and lse hold (qo_indptr[batch] or more).
  *   window      >= 1; max_qo_len or more observes every new token.
  *   q           bf16 [n_rows, Hq, D], 16-byte aligned.

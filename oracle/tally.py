@@ -14,11 +14,14 @@ import math
 
 import numpy as np
 
+FLT_MAX = float(np.finfo(np.float32).max)
+
 
 def weights(q, k, lse, scale, positions):
     """q [n, Hq, D] at `positions` [n], k [L, H, D], lse [n, Hq] -> (w [L, H], err [L, H]):
     the weights, and sum of weight * sum_d |q_d k_d| * |scale| (what a rounding of a score
-    is relative to).  NaN weights, and those of an lse of -inf or NaN, are nothing."""
+    is relative to).  NaN weights, those past fp32, and those of an lse of -inf or NaN, are
+    nothing."""
     n, Hq, _ = q.shape
     L, H, _ = k.shape
     G = Hq // H
@@ -30,7 +33,7 @@ def weights(q, k, lse, scale, positions):
             s = k[:, g] @ q[:, h].T * scale  # [L, n]
             size = np.abs(k[:, g]) @ np.abs(q[:, h]).T * abs(scale)
             p = np.exp(s - lse[:, h][None, :])
-            p = np.where(sees & np.isfinite(p) & (lse[:, h] > -math.inf)[None, :], p, 0.0)
+            p = np.where(sees & (p <= FLT_MAX) & (lse[:, h] > -math.inf)[None, :], p, 0.0)
         w[:, g] += p.sum(1)
         err[:, g] += np.where(p > 0, p * np.where(np.isfinite(size), size, 0), 0).sum(1)
     return w, err

@@ -13,7 +13,8 @@ __device__ __forceinline__ long long tally_at(const pkv_workspace &ws, int n_pag
   return (((long long)layer * n_pages + page) * ws.n_kv_heads + g) * ws.page_size + in_page;
 }
 
-// A weight that is NaN counts as nothing.
-__device__ __forceinline__ float tally_clean(float w) { return w == w ? w : 0.f; }
+// A weight that is NaN or infinite counts as nothing: it would stay in its entry, and
+// rank its token, for good.
+__device__ __forceinline__ float tally_clean(float w) { return fabsf(w) < INFINITY ? w : 0.f; }
 
 }  // namespace pkv

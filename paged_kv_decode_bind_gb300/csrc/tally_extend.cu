@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (__all_sync(0xffffffffu, s1 < INFINITY)) {
           sum += s1;
         } else {
-          // weights that are NaN (nothing) or infinite, one by one, and the columns that
+          // weights that are NaN or infinite (nothing), one by one, and the columns that
           // weigh nothing by their lse looked up
 #pragma unroll 1
           for (int c0 = 0; c0 < kTN / 2; c0 += 16) {

@@ -375,6 +375,22 @@ def test_extender(cuda, page, flags, splits):
     assert int(ws.err.item()) == 0
 
 
+def test_extend_weights_past_fp32(cuda):
+    """A log-sum-exp far below its scores gives weights past fp32: they add nothing, the
+    other queries' weights of the same tokens count."""
+    lens, new = [200, 140], [70, 30]
+
+    def spoil(ws, q, lse):
+        lse[5, 1] = -1000.0  # past 64 bits too
+        lse[40] = -300.0     # e^300: past fp32 alone
+        lse[90, 0] = -700.0
+
+    p = P.problem(lens, heads=(4, 2), d=64)
+    ws, tally, ref, _ = _extend(p, lens, new, spoil=spoil)
+    _check_tally(tally, ref)
+    assert torch.isfinite(tally.weight).all()
+
+
 # ------------------------------------------------------------------- evict ----
 def _evict_reference(p, ws, tally, lens, budget, limit, sinks, recent, skip=()):
     state = {n: P.by_slot(getattr(tally, n)).copy() for n in ("weight", "origin")}

@@ -25,6 +25,13 @@ def test_weights_by_hand():
     assert np.allclose(w, [[2.0], [0.0]])
 
 
+def test_weights_past_fp32_are_nothing():
+    q, k = np.array([[[1.0]], [[1.0]], [[1.0]], [[1.0]]]), np.array([[[0.0]], [[1.0]]])
+    lse = np.array([[-80.0], [-89.0], [-1000.0], [1.0]])  # fp32 ends at e^88.7
+    w, _ = T.weights(q, k, lse, 1.0, [1] * 4)
+    assert np.allclose(w, [[math.exp(80.0)], [math.exp(81.0)]], rtol=1e-12)
+
+
 def test_keep_and_moves_by_hand():
     w = np.array([0.5, 3.0, np.nan, 0.5, 0.5, 0.1, 0.2])
     o = np.array([0, 9, 10, 11, 12, 13, 14])
