@@ -632,9 +632,10 @@ pkv_status pkv_tally_decode_layer(const pkv_workspace *ws, const pkv_tally *t, i
  * A cached token (t < seq_lens[b] - n_b) gains w; a new one starts with it, weight = w,
  * origin = t + evicted[row].  Scores are exact bf16 products summed in fp32 with lse (in
  * 24 bits of it), the exponential is 2^-22 exact, the sum over queries fp32, in an order
- * that the request's lengths, window and max_qo_len settle.  A weight that is NaN or past
- * fp32 (an lse far below its score), or of a query whose lse is -inf, NaN or +inf, adds
- * nothing.  Requests of a batch must not share pages.
+ * that the request's lengths, window and max_qo_len settle (for a token with weights that
+ * are not finite: and which ones).  A weight that is NaN or past fp32 (an lse far below its
+ * score), or of a query whose lse is -inf, NaN or +inf, adds nothing.  Requests of a batch
+ * must not share pages.
  *   n_rows      rows that q and lse hold (qo_indptr[batch] or more).
  *   window      >= 1; max_qo_len or more observes every new token.
  *   q           bf16 [n_rows, Hq, D], 16-byte aligned.

@@ -643,8 +643,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (__all_sync(0xffffffffu, s1 < INFINITY)) {
           sum += s1;
         } else {
-          // weights that are NaN or infinite (nothing), one by one, and the columns that
-          // weigh nothing by their lse looked up
+          // A lane whose sum is not finite takes its weights one by one, those that are NaN
+          // or infinite as nothing, and looks up the columns that weigh nothing by their
+          // lse.  The others keep their sum: a key's weight is its own.
+          float rest = 0.f;
 #pragma unroll 1
           for (int c0 = 0; c0 < kTN / 2; c0 += 16) {
             tmem_ld16(u, src + c0);
@@ -656,9 +658,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
               const float w = ex2_approx(__uint_as_float(u[e]) * fs);
               const int i = it + (col0 + col) / G;
               const float l = a.lse[(long long)(x.q0 + i) * Hq + x.g * G + (col0 + col) % G];
-              if (fabsf(l) < INFINITY) sum += tally_clean(w);
+              if (fabsf(l) < INFINITY) rest += tally_clean(w);
             }
           }
+          sum += s1 < INFINITY ? s1 : rest;
         }
         tc_fence_before();
         __syncwarp();

@@ -391,6 +391,27 @@ def test_extend_weights_past_fp32(cuda):
     assert torch.isfinite(tally.weight).all()
 
 
+@pytest.mark.parametrize("window", [10 ** 6, 20])
+def test_extend_a_key_that_is_not_finite_changes_no_other(cuda, window):
+    """NaN and infinite keys weigh nothing, and every other token's weight keeps its bits."""
+    lens, new = [300, 140], [70, 30]
+    p = P.problem(lens, heads=(8, 2), d=64)
+    _, clean, _, (_, _, lse) = _extend(p, lens, new, window=window)
+    s0, s1 = P.slots(p, 0, 300), P.slots(p, 1, 140)
+
+    def spoil(ws, q, lse):
+        ws.k_pool[0, s0[3], 0] = float("nan")
+        ws.k_pool[0, s0[250], 1] = float("inf")  # a new token, masked for some queries
+        ws.k_pool[0, s1[70], 1] = float("nan")
+
+    _, tally, ref, _ = _extend(p, lens, new, window=window, lse=lse.cpu(), spoil=spoil)
+    _check_tally(tally, ref)
+    a, b = (P.by_slot(x.weight).view(np.int32)[0].copy() for x in (clean, tally))
+    for slot, h in ((s0[3], 0), (s0[250], 1), (s1[70], 1)):
+        a[slot, h] = b[slot, h] = 0
+    assert np.array_equal(a, b)
+
+
 # ------------------------------------------------------------------- evict ----
 def _evict_reference(p, ws, tally, lens, budget, limit, sinks, recent, skip=()):
     state = {n: P.by_slot(getattr(tally, n)).copy() for n in ("weight", "origin")}
