@@ -159,8 +159,7 @@ class DecodeRunner:
         self.launches_per_step = (1 + int(flat) + int(self.use_plan and 0 < batch <= 256) +
                                   NL * per_layer + int(evict is not None))
         # the most that a request of this step may hold, for the eviction's launch
-        most = evict.max_len if evict is not None and evict.max_len is not None \
-            else _abi.PKV_TALLY_MAX_LEN
+        most = evict.bound if evict is not None else _abi.PKV_TALLY_MAX_LEN
         self.evict_len = min(sh["max_pages_per_req"] * sh["page_size"], most)
 
     def _wsl(self, l):

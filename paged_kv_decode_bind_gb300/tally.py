@@ -89,9 +89,14 @@ class Eviction:
         if self.max_len is not None and not self.limit < self.max_len <= _abi.PKV_TALLY_MAX_LEN:
             raise ValueError("max_len is past the limit, at most PKV_TALLY_MAX_LEN")
 
+    @property
+    def bound(self) -> int:
+        """The most tokens of a request that is cut."""
+        return _abi.PKV_TALLY_MAX_LEN if self.max_len is None else self.max_len
+
     def length(self, n: int) -> int:
         """A request's tokens after the eviction."""
-        return self.budget if n > self.limit else n
+        return self.budget if self.limit < n <= self.bound else n
 
 
 class TallyExtender:

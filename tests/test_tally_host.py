@@ -272,6 +272,19 @@ def test_bind_tracker_follows_an_eviction():
     assert t.mode([1, 2], [11, 7]) == A.PKV_BIND_STEADY
 
 
+def test_an_eviction_leaves_requests_past_its_bound():
+    """As the device does: those longer than max_len stay as they are."""
+    e = pkv.Eviction(budget=10, limit=12, max_len=20)
+    assert [e.length(n) for n in (12, 13, 20, 21, 500)] == [12, 10, 10, 21, 500]
+    t = pkv.BindTracker()
+    t.mode([1, 2], [20, 21])
+    t.evicted(e)
+    assert t.mode([1, 2], [11, 22]) == A.PKV_BIND_STEADY
+    e = pkv.Eviction(budget=10)
+    assert e.length(A.PKV_TALLY_MAX_LEN) == 10
+    assert e.length(A.PKV_TALLY_MAX_LEN + 1) == A.PKV_TALLY_MAX_LEN + 1
+
+
 def test_extender_refusals():
     ws = _workspace()
     t = pkv.Tally(ws)
