@@ -469,7 +469,7 @@ def _axis_positions(x, rows, n_axes):
             (x.stride(-1) == 1 or x.shape[-1] <= 1):
         if x.dim() == 1:
             return x.data_ptr(), 0
-        if x.shape[0] == n_axes and (n_axes == 1 or x.stride(0) >= rows):
+        if x.shape[0] == n_axes and (n_axes == 1 or x.stride(0) == 0 or x.stride(0) >= rows):
             return x.data_ptr(), 0 if n_axes == 1 else x.stride(0)
     raise ValueError(f"positions are int32 [tokens >= {rows}] or [{n_axes}, tokens], dense along "
                      f"the tokens, got {x.dtype} {tuple(x.shape)} with strides {x.stride()}")

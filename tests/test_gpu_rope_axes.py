@@ -102,6 +102,24 @@ def test_one_axis_is_the_plain_rotation(cuda, norm):
         assert torch.equal(a, b)
 
 
+def test_one_row_of_positions_for_every_axis(cuda):
+    """[tokens], the same row expanded, and a copy of it for each axis: the same bits."""
+    T, hq, hkv, d = 9, 4, 2, 64
+    q, k = _bf16((T, hq, d), 1).cuda(), _bf16((T, hkv, d), 2).cuda()
+    rope = QkNormRopeAxes(n_q_heads=hq, n_kv_heads=hkv, head_dim=d, sections=(8, 12, 12),
+                          cos_sin=rope_table(SPAN, d))
+    pos = torch.randint(0, SPAN, (T,), generator=torch.Generator().manual_seed(5)).int().cuda()
+    outs = []
+    for x in (pos, pos.expand(3, T), pos.expand(3, T).contiguous()):
+        outs.append([torch.zeros_like(y) for y in (q, k)])
+        A.pkv_qk_norm_rope_axes(rope, T, q, k, x, *outs[-1])
+    torch.cuda.synchronize()
+    assert int(rope.err.item()) == 0
+    for other in outs[1:]:
+        for a, b in zip(outs[0], other):
+            assert torch.equal(a, b)
+
+
 def test_positions_outside_the_table(cuda):
     """Zeros and an error for a position of an axis in use, or a row, that is out of range;
     zeros alone for an empty request; no look at an axis that no pair follows."""

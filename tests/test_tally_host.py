@@ -358,3 +358,12 @@ def test_axes_tensors_are_checked():
         A.pkv_qk_norm_rope_axes(r.norm, 1, q, k, good, q, k)
     with pytest.raises((AttributeError, ctypes.ArgumentError)):
         A.pkv_qk_norm_rope(r, 1, q, k, good[0], q, k)
+
+
+def test_axes_take_one_row_for_every_axis():
+    """An expanded row is the same as the row itself: no elements between the axes."""
+    one = torch.arange(5, dtype=torch.int32)[1:]
+    assert A._axis_positions(one.expand(2, 4), 4, 2) == A._axis_positions(one, 4, 2) == \
+        (one.data_ptr(), 0)
+    with pytest.raises(ValueError):
+        A._axis_positions(one.expand(2, 4), 5, 2)
