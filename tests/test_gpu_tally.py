@@ -412,6 +412,24 @@ def test_extend_a_key_that_is_not_finite_changes_no_other(cuda, window):
     assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("window", [500, 40])
+def test_extend_every_query_weighs_one(cuda, window):
+    """From a tally of zeros each KV head holds the group's heads times the observed
+    queries, within the sum of its tokens' bounds and of fp32's lse."""
+    lens, new = [1500, 129], [700, 60]
+    p = P.problem(lens, heads=(8, 2))
+    ws, tally, ref, (qo, q, lse) = _extend(p, lens, new, window=window)
+    tally.weight.zero_()
+    A.pkv_tally_extend(ws, tally, 2, 0, qo, 700, sum(new), window, q, lse, p.scale)
+    torch.cuda.synchronize()
+    got = P.by_slot(tally.weight).astype(np.float64)[0]
+    for b, (L, n) in enumerate(zip(lens, new)):
+        s = P.slots(p, b, L)
+        count = 4 * min(n, window)
+        off = ref[2][0, s].sum(0) + 2 * P.EPS32 * float(lse.abs().max()) * count
+        assert np.all(np.abs(got[s].sum(0) - count) <= off)
+
+
 # ------------------------------------------------------------------- evict ----
 def _evict_reference(p, ws, tally, lens, budget, limit, sinks, recent, skip=()):
     state = {n: P.by_slot(getattr(tally, n)).copy() for n in ("weight", "origin")}
@@ -749,6 +767,80 @@ def test_prompt_captured_and_replayed_with_other_inputs(cuda):
     for a, b in zip(got[:3], got[3:]):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("page,heads", [(16, (8, 2)), (1, (16, 8)), (5, (2, 2))])
+@pytest.mark.parametrize("lens", [[70], [900, 3, 260, 64], [400] * 40])
+@pytest.mark.parametrize("turns", [False, True])
+def test_decode_back_to_back(cuda, page, heads, lens, turns):
+    """Decode layers with nothing between them, each reading early the weights that the one
+    before stores: bit for bit as the same calls with a wait behind each.  turns: every
+    other call takes the first request alone, so that other blocks come to its tokens."""
+    calls, B = 24, len(lens)
+    qs = [_bf16((B, heads[0], 64), 300 + i).cuda() for i in range(calls)]
+    got = []
+    for wait in (True, False):
+        for layers in (1, 3):
+            p = P.problem(lens, page=page, heads=heads, d=64, layers=layers)
+            ws, tally = P.device(p, max_splits=3)
+            torch.cuda.synchronize()
+            for i, q in enumerate(qs):
+                early = A.PKV_FLAG_PLAN_EARLY if i > 0 else 0
+                n = 1 if turns and i % 2 else B
+                A.pkv_tally_decode_layer(ws, tally, n, i % layers, q, None, None, p.scale, 3, early)
+                if wait:
+                    torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            assert int(ws.err.item()) == 0
+            got.append((tally.weight.clone(), ws.lse.clone()))
+    for a, b in zip(got[:2], got[2:]):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_back_to_back_sums_to_the_calls(cuda):
+    """The same against the oracle: weights of many calls, from one layer's tally of zeros."""
+    lens, calls = [260, 900, 1], 20
+    p = P.problem(lens, page=1, heads=(16, 8), d=64)
+    ws, tally = P.device(p, max_splits=3)
+    tally.weight.zero_()
+    qs = [_bf16((3, 16, 64), 300 + i).cuda() for i in range(calls)]
+    torch.cuda.synchronize()
+    for q in qs:
+        A.pkv_tally_decode_layer(ws, tally, 3, 0, q, None, None, p.scale, 3)
+    torch.cuda.synchronize()
+    got = P.by_slot(tally.weight).astype(np.float64)
+    tally.weight.zero_()
+    w, bound = 0.0, 0.0
+    for q in qs:
+        one = _decode_reference(p, ws, tally, 0, q, lens, False)
+        w, bound = w + one[0], bound + one[2]
+    # and an addition's rounding for each call
+    assert np.all(np.abs(got - w) <= bound + calls * P.EPS32 * w)
+
+
+@pytest.mark.parametrize("page", [16, 1])
+def test_decode_right_behind_an_eviction(cuda, page):
+    """A layer whose lengths, weights and rows the launch before it wrote, without and with
+    a wait between the two."""
+    lens, got = [300, 90, 700], []
+    q = _bf16((3, 8, 128), 5).cuda()
+    for wait in (True, False):
+        p = P.problem(lens, page=page, heads=(8, 4))
+        ws, tally = P.device(p, max_splits=3)
+        _set_tally(p, ws, tally, "random")
+        torch.cuda.synchronize()
+        for budget in (200, 120, 64):
+            A.pkv_tally_evict(ws, tally, 3, 700, budget, budget, 4, 16)
+            if wait:
+                torch.cuda.synchronize()
+            A.pkv_tally_decode_layer(ws, tally, 3, 0, q, None, None, p.scale, 3)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert ws.seq_lens.tolist() == [64, 64, 64] and int(ws.err.item()) == 0
+        got.append((tally.weight.clone(), tally.origin.clone(), ws.out_bf16(3).clone()))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("seed", range(24))
