@@ -9,8 +9,8 @@
 // L2, and spare a second reading of K.
 //
 // Measured (GB300, us a layer in graphs of 24): 64 requests of 1024-4096 tokens, 16/2 heads
-// 44.0 (34.1 without the tally), 16 of 2048, 32/8 heads, 33.6 (27.3), 4 of 512-2048 11.8
-// (8.8), 16 flat of 200-4000 43.1 (33.5).  Of 4 x 65536 tokens (190 us, 161 without) the
+// 43.8 (33.9 without the tally), 16 of 2048, 32/8 heads, 32.7 (27.2), 4 of 512-2048 11.7
+// (8.9), 16 flat of 200-4000 42.5 (33.3).  Of 4 x 65536 tokens (190 us, 161 without) the
 // scores' stores take 13 us and the second launch 16.
 #include <algorithm>
 
@@ -23,12 +23,15 @@ namespace {
 
 constexpr int kTThreads = 256;
 template <int G>
-constexpr int kAddBlocks = G <= 8 ? 5 : 4;  // of an SM (16 heads' scores and lse: 64 registers)
-// Items of a warp whose loads are in flight, beside the next ones' indices (24 layers'
-// steps, us a layer: 64 requests of 1024-4096 tokens, G = 8, 44.0 with one item and five
-// blocks, 44.4 with four, 44.5 with six, 44.9 with two items and four; 16 of 2048 and 4 of
-// 512-2048, G = 4, 33.6 and 11.8 with two items, 34.5 and 12.0 with one, 33.2 and 12.2 with
-// three).
+constexpr int kAddBlocks = G == 4 ? 6 : G <= 8 ? 5 : 4;  // of an SM (G = 16: 64 registers)
+// Whether the next items' indices come beside an item's loads.  24 layers' steps, us a layer,
+// of 16 requests of 2048 tokens and 16 flat of 200-4000 (G = 8: 64 of 1024-4096), with them in
+// five blocks, and without in six: G = 1 31.7 and 40.5, 31.5 and 40.6; G = 2 32.6 and 42.8,
+// 33.1 and 43.8 (40 registers spill); G = 4 33.6 and 43.1, 32.8 and 42.4; G = 8 44.0, 44.2.
+template <int G>
+constexpr bool kAddAhead = G != 4;
+// Items of a warp whose loads are in flight (the same loads: G = 8 44.9 with two in four
+// blocks, G = 4 34.9 with one).
 template <int G>
 constexpr int kAddItems = G <= 4 ? 2 : 1;
 
@@ -60,7 +63,7 @@ __device__ __forceinline__ void load_group(float (&x)[G], const float *s) {
 
 // One item of a warp: 2^tl_log tokens x 2^hl_log heads, a lane each.  Tokens run fastest
 // over the lanes, so that a page's entries of a head, and a head's scores, are read in
-// runs.  A warp has UN items' loads in flight, and looks the next ones' indices up beside
+// runs.  A warp has UN items' loads in flight, and may look the next ones' indices up beside
 // them.
 //
 // The launch waits for the attention only where it reads what that writes, the scores and
@@ -99,8 +102,9 @@ __global__ void __launch_bounds__(kTThreads, kAddBlocks<G>)
         raw[u] = t0 + u * step < tgroups && t < L ? *index_src(ws, pl, ri, t) : -1;
       }
     };
-    look_up(first);
+    if constexpr (kAddAhead<G>) look_up(first);
     for (int t0 = first; __any_sync(0xffffffffu, t0 < tgroups); t0 += UN * step) {
+      if constexpr (!kAddAhead<G>) look_up(t0);
       long long at[UN];
       float was[UN];
 #pragma unroll
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(kTThreads, kAddBlocks<G>)
         at[u] = tally_at(ws, pl.n_pages, a.layer, page, g, slot - page * pl.P);
         if (!(a.appended && t == L - 1)) was[u] = a.t.weight[at[u]];
       }
-      look_up(t0 + UN * step);
+      if constexpr (kAddAhead<G>) look_up(t0 + UN * step);
       if (!waited) {
         pdl_wait();
         waited = true;
