@@ -36,9 +36,10 @@
 //
 // Measured (GB300, 32/8 heads, D = 128): a whole 8192-token prompt 220 us, 1250 TFLOP/s (65 %
 // of the measured bf16 burst; the tensor pipe 67 % busy, the exponentials' 59 %): a product
-// takes ~1500 cycles of the issuing warp, and the costliest CTA has 18 % above the mean; the
+// takes ~1500 cycles of the issuing warp, and the costliest CTA has 15 % above the mean; the
 // last 64 queries on 32768 tokens 27.4 us (2.5 TB/s of keys): the hand-offs of a unit; four
-// 256-token chunks on 661-2014 26 us: launch, first tiles, and 16 products in a row.
+// chunks of up to 256 tokens on 820-1845 26 us: launch, first tiles, and the costliest CTA's
+// 14 products in a row, where the mean is 9.7.
 // Not kept: two issuing warps, a buffer each (whole prompt 277 us: their MMAs alternate and
 // both finish late), key tiles by tensor-map boxes (27 us where cp.async took 26), two
 // groups of loader warps (no difference).

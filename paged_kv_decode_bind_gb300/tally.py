@@ -72,7 +72,10 @@ class Eviction:
     """Requests of more than `limit` tokens (None: budget) keep `budget`: the first `sinks`
     and the last `recent` of all their tokens, then those of the largest tally.  max_len:
     a bound on the lengths that a step meets (None: what a table row holds, at most
-    PKV_TALLY_MAX_LEN); longer requests are left as they are, with PKV_DEVERR_LEN."""
+    PKV_TALLY_MAX_LEN); longer requests are left as they are, with PKV_DEVERR_LEN.  It
+    settles what the eviction's launch costs: in a decode loop give limit + 1 (24 layers, 16
+    requests at their budget of 2048 in rows of 131072 tokens: 822 us a step with it, 1293
+    without)."""
 
     budget: int
     limit: int | None = None
